@@ -53,7 +53,8 @@ typedef enum {
   BL_ERR_CUDA = 5,           /* a CUDA runtime call or launch failed */
   BL_ERR_DEVICE_TIMEOUT = 6, /* a bounded device-side wait gave up */
   BL_ERR_NONFINITE = 7,      /* a kernel met a NaN or Inf input */
-  BL_ERR_IO = 8              /* a checkpoint file could not be written or read, or is malformed */
+  BL_ERR_IO = 8,             /* a checkpoint file could not be written or read, or is malformed */
+  BL_ERR_RANGE = 9           /* a position, slot, page or length read on the device is out of range */
 } bl_status;
 
 /* Weight storage formats. */
@@ -369,6 +370,150 @@ size_t bl_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K);
 bl_status bl_linear_backward(const float* dY, const float* X, const float* W, int64_t M, int64_t N, int64_t K,
                              float* dX, float* dW, float* db, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- attention between the projections -------------------------------------
+ * What stands between the Q/K/V BitLinears and the O BitLinear of a block
+ * ("ultragraph -- when the graph is the 1-bit LLM, part 2", section "attention,
+ * as graph ops"; RoPE and the KV cache of "ultragraph-1bit 0.12.0" (PyPI)):
+ * per-head norms with the position rotation, attention over packed sequences
+ * with its gradient, and attention of one new token over a paged cache.
+ *
+ * Conventions of this section
+ *   - Element types: float32 for what the BitLinears write and read, float16 or
+ *     bfloat16 for queries, keys, values and their gradients.  Sums, softmax
+ *     statistics and norms are float32; products contract with FMA.
+ *   - D is the head size, a multiple of 8 (8 <= D <= 128); Hq is a multiple of
+ *     Hkv, and query head h reads key/value head h / (Hq / Hkv).
+ *   - Visibility: the token at position p of a sequence sees the keys j <= p with
+ *     j > p - window or j < sinks; window = 0 means no window (sinks is then
+ *     without effect).  A row that sees no key gives 0 (its lse -inf, its
+ *     gradient 0).
+ *   - `scale` multiplies the scores (1/sqrt(D) for the usual attention).
+ *   - Values that no row sees (behind a sequence's end, outside every window,
+ *     the unused rest of a page) may hold anything, NaN included.  A NaN or Inf
+ *     that a row does see sets BL_ERR_NONFINITE in the status word; in
+ *     bl_attention and its backward it may then reach the other rows of the same
+ *     sequence.
+ *   - Positions, slots, page numbers and lengths live on the device.  One out of
+ *     range sets BL_ERR_RANGE in the status word; what it would have addressed is
+ *     neither read nor written. */
+typedef enum { BL_T_F32 = 0, BL_T_F16 = 1, BL_T_BF16 = 2 } bl_dtype;
+
+/* Fills table [P, R] float32 with cos (first R/2 columns) and sin (last R/2) of
+ * p * base^(-2i/R), i < R/2, the angles formed and reduced in float64.  R even,
+ * 2 <= R; base finite, > 0. */
+bl_status bl_rope_table(float* table, int64_t P, int R, double base, cudaStream_t stream);
+
+/* Rows of queries, keys and values as the projections write them. */
+typedef struct {
+  int64_t M;                  /* tokens */
+  int32_t Hq, Hkv, D;
+  const float *q, *k, *v;     /* [M, Hq D], [M, Hkv D], [M, Hkv D] float32, 16-byte aligned */
+  int64_t ldq, ldk, ldv;      /* floats between tokens, multiples of 4 (one fused projection: all the same) */
+  const int32_t* pos;         /* [M] position of each token, 0 <= pos < P */
+  const float* table;         /* [P, R] of bl_rope_table, 16-byte aligned */
+  int64_t P;
+  int32_t R;                  /* rotated elements of each head, a multiple of 8, 0 <= R <= D (0: no rotation) */
+  int32_t interleaved;        /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+  const float *gq, *gk;       /* [D] gains, 16-byte aligned, or NULL (all ones) */
+  float eps;                  /* finite, > 0 */
+} bl_qkv_rows;
+
+/* Per-head RMSNorm of queries and keys with the position rotation in the same
+ * pass: y = x / sqrt(mean(x^2) + eps) * g over each head's D elements, then the
+ * pairs (a, b) of its first R elements become (a cos - b sin, a sin + b cos).
+ * Values are converted only.  q [M, Hq, D], k and v [M, Hkv, D]: contiguous
+ * outputs of type t (any bl_dtype), 16-byte aligned.  Here D may be up to 256.
+ * Rows of a token whose position is out of range are not written. */
+bl_status bl_qk_norm_rope(const bl_qkv_rows* rows, bl_dtype t, void* q, void* k, void* v, cudaStream_t stream);
+
+/* A paged key-value cache: page n holds `page` tokens of every head as
+ * [Hkv, page, D] at k + n * Hkv * page * D (and the same in v). */
+typedef struct {
+  bl_dtype t;                 /* BL_T_F16 or BL_T_BF16 */
+  void *k, *v;                /* [pages, Hkv, page, D] contiguous, 16-byte aligned */
+  int64_t pages;
+  int32_t page;               /* tokens per page, >= 1 */
+  int32_t Hkv, D;
+} bl_kv_pages;
+
+/* bl_qk_norm_rope with the keys and values written into a cache: token m goes to
+ * slot slots[m] (= page number * page + place in the page; negative: its key and
+ * value are not stored).  q [M, Hq, D] of the cache's type.  Slots of one call
+ * must differ.  A token whose slot is past the cache is not stored. */
+bl_status bl_qk_norm_rope_append(const bl_qkv_rows* rows, void* q, const bl_kv_pages* cache, const int64_t* slots,
+                                 cudaStream_t stream);
+
+/* Gradients of bl_qk_norm_rope with respect to its input rows and gains:
+ *   dq [M, Hq, D], dk, dv [M, Hkv, D]: contiguous, type t (any bl_dtype).
+ *   dxq, dxk, dxv: float32 rows, strides lddq, lddk, lddv (multiples of 4; a
+ *     fused [M, (Hq + 2 Hkv) D] dY of the projection, for instance).
+ *   dgq, dgk [D] float32, or NULL (not wanted); summed over tokens and heads in a
+ *     fixed order.
+ *   ws >= bl_qk_norm_rope_backward_workspace_size(rows) bytes, 256-byte aligned
+ *     (its contents need no clearing).
+ * rows->v is not read (it may be NULL).  Rows of a token whose position is out
+ * of range are not written and add nothing to the gains' gradients. */
+size_t bl_qk_norm_rope_backward_workspace_size(const bl_qkv_rows* rows);
+bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const void* dq, const void* dk, const void* dv,
+                                   float* dxq, int64_t lddq, float* dxk, int64_t lddk, float* dxv, int64_t lddv,
+                                   float* dgq, float* dgk, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* One call of bl_attention: B sequences packed end to end.  Sequence b has the
+ * query rows cu_q[b] .. cu_q[b+1] - 1 and the key rows cu_k[b] .. cu_k[b+1] - 1
+ * (Lq and Lk of them); its query i stands at position i + Lk - Lq, so that the
+ * last query sees the last key (rows with a negative position see nothing). */
+typedef struct {
+  bl_dtype t;                 /* BL_T_F16 or BL_T_BF16 */
+  int32_t Hq, Hkv, D;
+  const void *q, *k, *v;      /* [Tq, Hq, D], [Tk, Hkv, D], [Tk, Hkv, D]; heads D apart, 16-byte aligned */
+  int64_t ldq, ldk, ldv;      /* elements between tokens, multiples of 8 */
+  int64_t Tq, Tk;             /* rows of the buffers (< 2^31) */
+  const int32_t *cu_q, *cu_k; /* [B + 1], not falling, within 0 .. Tq and 0 .. Tk */
+  int32_t B;
+  int32_t max_q, max_k;       /* at least the longest Lq and Lk (max_k: the backward only) */
+  int32_t window, sinks;      /* >= 0 */
+  float scale;                /* finite, > 0 */
+} bl_attn_call;
+
+/* O = softmax(scale Q K^T over the visible keys) V and the row's log-sum-exp.
+ *   out [Tq, Hq, D] contiguous, type t; lse [Hq, Tq] float32 (natural log), or NULL.
+ * Probabilities are rounded to type t before they meet V (as the operands of the
+ * tensor cores); sums are float32.  Rows that belong to no sequence are left as
+ * they were.  A sequence whose bounds are out of range, or longer than max_q, is
+ * left out. */
+bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStream_t stream);
+
+/* Its gradients from out, lse and dout [Tq, Hq, D] (contiguous, type t):
+ * P = exp(scale Q K^T - lse), dV = P^T dO, dS = P (dO V^T - rowsum(dO O)),
+ * dQ = scale dS K, dK = scale dS^T Q, dK and dV summed over the query heads that
+ * share a key head.  dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]: contiguous, type t.
+ * Every sum is taken in a fixed order.  Rows that belong to no sequence are left
+ * as they were.
+ *   ws >= bl_attention_backward_workspace_size(call) bytes, 256-byte aligned (its
+ *   contents need no clearing). */
+size_t bl_attention_backward_workspace_size(const bl_attn_call* call);
+bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
+                                void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of one new token per sequence over a paged cache (its own key and
+ * value stored already): the query of sequence b stands at position lens[b] - 1
+ * and sees the cache's tokens as above.
+ *   q [B, Hq, D] contiguous, of the cache's type, 16-byte aligned.
+ *   table [B, ldt] int32: page number of tokens n * page .. of each sequence; only
+ *     the pages that the query sees are looked up.
+ *   lens [B] int32, 0 <= lens[b] <= ldt * page (0: the row is 0).
+ *   out [B, Hq, D] contiguous, float32 or of the cache's type; probabilities keep
+ *     float32's precision.
+ *   ws >= bl_paged_attention_workspace_size(B, Hq, cache) bytes, 256-byte
+ *     aligned, ZERO-FILLED before its first use; every call leaves its counters
+ *     zero again.  Calls sharing one workspace must not overlap on the GPU.
+ * One launch: the sequences' visible tokens are shared out evenly over the SMs,
+ * and the last CTA to finish a head joins its parts in a fixed order. */
+size_t bl_paged_attention_workspace_size(int64_t B, int Hq, const bl_kv_pages* cache);
+bl_status bl_paged_attention(const void* q, int64_t B, int Hq, const bl_kv_pages* cache, const int32_t* table,
+                             int64_t ldt, const int32_t* lens, int32_t window, int32_t sinks, float scale,
+                             bl_dtype out_t, void* out, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ---- deployed checkpoint ---------------------------------------------------
  * "ultragraph-1bit 0.12.0" (PyPI), section "A whole ternary GPT": a deployed
  * checkpoint stores the ternary weights at five per byte (~1.6 bits each) plus
@@ -414,8 +559,8 @@ bl_status bl_load_deployed_layer(const char* path, int index, uint8_t* Wp, int64
                                  float* bias_dev, cudaStream_t stream);
 
 /* Synchronizes `stream`, then reads and clears this device's status word:
- * BL_ERR_DEVICE_TIMEOUT or BL_ERR_NONFINITE if a kernel recorded one, BL_ERR_CUDA
- * if the stream reports an error, else BL_OK. */
+ * BL_ERR_DEVICE_TIMEOUT, BL_ERR_WORKSPACE, BL_ERR_RANGE or BL_ERR_NONFINITE if a
+ * kernel recorded one, BL_ERR_CUDA if the stream reports an error, else BL_OK. */
 bl_status bl_sync_status(cudaStream_t stream);
 
 /* Self-test of the device timeout path: one thread waits, with the bounded

@@ -24,7 +24,7 @@ FLAG_STATIC_WEIGHTS = 0x100            # BL_FLAG_STATIC_WEIGHTS
 
 STATUS = {0: "BL_OK", 1: "BL_ERR_INVALID_ARG", 2: "BL_ERR_ALIGNMENT", 3: "BL_ERR_UNSUPPORTED",
           4: "BL_ERR_WORKSPACE", 5: "BL_ERR_CUDA", 6: "BL_ERR_DEVICE_TIMEOUT",
-          7: "BL_ERR_NONFINITE", 8: "BL_ERR_IO"}
+          7: "BL_ERR_NONFINITE", 8: "BL_ERR_IO", 9: "BL_ERR_RANGE"}
 
 # Every symbol the header declares, with (restype, argtypes).
 _P, _I64, _SZ, _F, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
@@ -505,3 +505,11 @@ def sync_status(device=None) -> str:
     dev = torch.device("cuda") if device is None else device
     code = lib.bl_sync_status(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
     return STATUS.get(code, str(code))
+
+
+from . import attn as _attn  # noqa: E402  (needs the names above)
+from .attn import (AttnCall, KvPages, QkvRows, attention, attention_backward, paged_attention,  # noqa: E402,F401
+                        paged_attention_workspace_size, qk_norm_rope, qk_norm_rope_append, qk_norm_rope_backward,
+                        rope_table)
+
+SIGNATURES.update(_attn.SIGNATURES)

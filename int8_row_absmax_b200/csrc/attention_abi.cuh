@@ -1,0 +1,381 @@
+// C ABI of the attention operators (declared in include/bitlinear.h): argument
+// checks, workspace sizes and launches.  Included by bitlinear_lib.cu, whose
+// helpers it uses.
+#pragma once
+
+#include "attn.cuh"
+#include "paged_attn.cuh"
+#include "qk_rope.cuh"
+
+namespace bl {
+namespace {
+
+constexpr int kAttnMaxD = 128, kRopeMaxD = 256;
+
+bool half_type(bl_dtype t) { return t == BL_T_F16 || t == BL_T_BF16; }
+bool any_type(bl_dtype t) { return t == BL_T_F32 || half_type(t); }
+bool int32_max(int64_t v) { return v < (int64_t(1) << 31); }
+
+// ---- norms and rotation ----------------------------------------------------------
+bl_status check_rows(const bl_qkv_rows* r, bool values) {
+  if (!r) return BL_ERR_INVALID_ARG;
+  if (r->M < 0 || !int32_max(r->M) || r->Hq < 1 || r->Hkv < 1 || r->Hq > 65535 || r->Hkv > 65535 ||
+      r->Hq % r->Hkv != 0)
+    return BL_ERR_INVALID_ARG;
+  if (r->D < 8 || r->D % 8 != 0 || r->D > kRopeMaxD) return BL_ERR_INVALID_ARG;
+  if (r->R < 0 || r->R % 8 != 0 || r->R > r->D || (r->interleaved != 0 && r->interleaved != 1)) return BL_ERR_INVALID_ARG;
+  if (!eps_ok(r->eps)) return BL_ERR_INVALID_ARG;
+  if (r->R > 0 && r->P < 1) return BL_ERR_INVALID_ARG;
+  if (r->M == 0) return BL_OK;
+  if (!r->q || !r->k || (values && !r->v) || (r->R > 0 && (!r->pos || !r->table))) return BL_ERR_INVALID_ARG;
+  const int64_t wq = int64_t(r->Hq) * r->D, wk = int64_t(r->Hkv) * r->D;
+  if (r->ldq < wq || r->ldk < wk || (values && r->ldv < wk)) return BL_ERR_INVALID_ARG;
+  if (r->ldq % 4 != 0 || r->ldk % 4 != 0 || (values && r->ldv % 4 != 0)) return BL_ERR_ALIGNMENT;
+  if (!is_aligned(r->q, 16) || !is_aligned(r->k, 16) || (values && !is_aligned(r->v, 16))) return BL_ERR_ALIGNMENT;
+  if (!is_aligned(r->gq, 16) || !is_aligned(r->gk, 16)) return BL_ERR_ALIGNMENT;
+  if (r->R > 0 && (!is_aligned(r->table, 16) || !is_aligned(r->pos, 4))) return BL_ERR_ALIGNMENT;
+  return BL_OK;
+}
+
+QrArgs rows_args(const bl_qkv_rows* r) {
+  QrArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = r->M;
+  a.Hq = r->Hq;
+  a.Hkv = r->Hkv;
+  a.D = r->D;
+  a.q = r->q;
+  a.k = r->k;
+  a.v = r->v;
+  a.ldq = r->ldq;
+  a.ldk = r->ldk;
+  a.ldv = r->ldv;
+  a.pos = r->pos;
+  a.table = r->table;
+  a.P = r->P;
+  a.R = r->R;
+  a.interleaved = r->interleaved;
+  a.gq = r->gq;
+  a.gk = r->gk;
+  a.eps = r->eps;
+  a.page = 1;
+  a.lanes = 1;
+  while (a.lanes < r->D / 8) a.lanes *= 2;
+  return a;
+}
+
+// Four heads an item once that still fills the SMs (eight loads in flight a
+// thread), one head an item below, where latency counts.
+template <typename T, bool kAppend>
+bl_status launch_norm_rope(const QrArgs& a, cudaStream_t st) {
+  const int per_block = kQrThreads / a.lanes, heads = a.Hq + 2 * a.Hkv;
+  const int64_t many = a.M * ceil_div(heads, 4);
+  if (many >= int64_t(num_sms()) * 4 * per_block)
+    qk_norm_rope_kernel<T, kAppend, 4><<<grid_for(many, per_block, 16), kQrThreads, 0, st>>>(a);
+  else
+    qk_norm_rope_kernel<T, kAppend, 1><<<grid_for(a.M * heads, per_block, 16), kQrThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+// CTAs of the backward (and rows of its partial sums): planned for 148 SMs.
+constexpr int kQrBackCtas = 148 * 4;
+int rows_back_grid(const bl_qkv_rows* r) {
+  int lanes = 1;
+  while (lanes < r->D / 8) lanes *= 2;
+  const int64_t g = ceil_div(r->M * (r->Hq + 2 * int64_t(r->Hkv)), int64_t(kQrThreads / lanes));
+  return int(g < 1 ? 1 : g < kQrBackCtas ? g : kQrBackCtas);
+}
+
+bl_status check_cache(const bl_kv_pages* c) {
+  if (!c || !c->k || !c->v || !half_type(c->t)) return BL_ERR_INVALID_ARG;
+  if (c->pages < 1 || !int32_max(c->pages) || c->page < 1 || c->Hkv < 1 || c->Hkv > 65535) return BL_ERR_INVALID_ARG;
+  if (c->D < 8 || c->D % 8 != 0) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(c->k, 16) || !is_aligned(c->v, 16)) return BL_ERR_ALIGNMENT;
+  return BL_OK;
+}
+
+// ---- attention over packed sequences ----------------------------------------------
+bl_status check_attn(const bl_attn_call* c) {
+  if (!c || !half_type(c->t)) return BL_ERR_INVALID_ARG;
+  if (c->Hq < 1 || c->Hkv < 1 || c->Hq > 65535 || c->Hq % c->Hkv != 0) return BL_ERR_INVALID_ARG;
+  if (c->D < 8 || c->D % 8 != 0 || c->D > kAttnMaxD) return BL_ERR_INVALID_ARG;
+  if (c->Tq < 0 || c->Tk < 0 || !int32_max(c->Tq) || !int32_max(c->Tk)) return BL_ERR_INVALID_ARG;
+  if (c->B < 0 || c->B > 65535 || c->max_q < 0 || c->max_k < 0 || c->window < 0 || c->sinks < 0) return BL_ERR_INVALID_ARG;
+  if (!std::isfinite(c->scale) || !(c->scale > 0.f)) return BL_ERR_INVALID_ARG;
+  if (c->B == 0 || c->Tq == 0) return BL_OK;
+  if (!c->q || !c->cu_q || !c->cu_k || (c->Tk > 0 && (!c->k || !c->v))) return BL_ERR_INVALID_ARG;
+  const int64_t wq = int64_t(c->Hq) * c->D, wk = int64_t(c->Hkv) * c->D;
+  if (c->ldq < wq || (c->Tk > 0 && (c->ldk < wk || c->ldv < wk))) return BL_ERR_INVALID_ARG;
+  if (c->ldq % 8 != 0 || c->ldk % 8 != 0 || c->ldv % 8 != 0) return BL_ERR_ALIGNMENT;
+  if (!is_aligned(c->q, 16) || !is_aligned(c->k, 16) || !is_aligned(c->v, 16) || !is_aligned(c->cu_q, 4) ||
+      !is_aligned(c->cu_k, 4))
+    return BL_ERR_ALIGNMENT;
+  return BL_OK;
+}
+
+AttnArgs attn_args(const bl_attn_call* c) {
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = c->q;
+  a.k = c->k;
+  a.v = c->v;
+  a.ldq = c->ldq;
+  a.ldk = c->ldk;
+  a.ldv = c->ldv;
+  a.Tq = c->Tq;
+  a.Tk = c->Tk;
+  a.cu_q = c->cu_q;
+  a.cu_k = c->cu_k;
+  a.Hq = c->Hq;
+  a.Hkv = c->Hkv;
+  a.D = c->D;
+  a.B = c->B;
+  a.max_q = c->max_q;
+  a.max_k = c->max_k;
+  a.window = c->window;
+  a.sinks = c->sinks;
+  a.scale = c->scale;
+  return a;
+}
+
+template <typename T>
+bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
+  attn_simple_kernel<T><<<dim3(unsigned(ceil_div(a.max_q, kSimpleWarps)), unsigned(a.Hq), unsigned(a.B)),
+                          32 * kSimpleWarps, 0, st>>>(a);
+  return launch_status();
+}
+
+template <typename T>
+bl_status run_attn_backward(const AttnArgs& a, cudaStream_t st) {
+  attn_delta_kernel<T><<<unsigned(ceil_div(a.Tq * a.Hq, 4)), 128, 0, st>>>(a);
+  if (a.max_q > 0)
+    attn_dq_simple_kernel<T><<<dim3(unsigned(ceil_div(a.max_q, kSimpleWarps)), unsigned(a.Hq), unsigned(a.B)),
+                               32 * kSimpleWarps, 0, st>>>(a);
+  if (a.max_k > 0)
+    attn_dkv_simple_kernel<T><<<dim3(unsigned(ceil_div(a.max_k, kSimpleWarps)), unsigned(a.Hkv), unsigned(a.B)),
+                                32 * kSimpleWarps, 0, st>>>(a);
+  return launch_status();
+}
+
+// ---- paged attention ----------------------------------------------------------------
+int paged_pad(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+int paged_nt(int Hq, int Hkv) { return Hq / Hkv <= 8 ? 1 : 2; }
+constexpr size_t kPaCountBytes = 2048;
+static_assert(kPaCtas * 4 <= kPaCountBytes, "counters fit");
+
+template <typename T, int DP, int NT, typename OutT>
+bl_status launch_paged(const PaArgs& a, cudaStream_t st) {
+  constexpr int smem = PaCfg<T, DP, NT>::kSmem;
+  if (cudaFuncSetAttribute(paged_attn_kernel<T, DP, NT, OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return BL_ERR_CUDA;
+  const int64_t most = a.B * a.Hkv * a.chunks * ceil_div(a.ldt * a.page, kPaTile);
+  const int64_t grid = most < 1 ? 1 : most < kPaCtas ? most : kPaCtas;
+  paged_attn_kernel<T, DP, NT, OutT><<<unsigned(grid), kPaThreads, smem, st>>>(a);
+  return launch_status();
+}
+template <typename T, int DP, int NT>
+bl_status launch_paged_out(const PaArgs& a, bool f32, cudaStream_t st) {
+  return f32 ? launch_paged<T, DP, NT, float>(a, st) : launch_paged<T, DP, NT, T>(a, st);
+}
+template <typename T>
+bl_status launch_paged_t(const PaArgs& a, bool f32, cudaStream_t st) {
+  const int dp = paged_pad(a.D), nt = paged_nt(a.Hq, a.Hkv);
+  if (nt == 1)
+    return dp == 32 ? launch_paged_out<T, 32, 1>(a, f32, st)
+                    : dp == 64 ? launch_paged_out<T, 64, 1>(a, f32, st) : launch_paged_out<T, 128, 1>(a, f32, st);
+  return dp == 32 ? launch_paged_out<T, 32, 2>(a, f32, st)
+                  : dp == 64 ? launch_paged_out<T, 64, 2>(a, f32, st) : launch_paged_out<T, 128, 2>(a, f32, st);
+}
+
+}  // namespace
+}  // namespace bl
+
+extern "C" {
+
+bl_status bl_rope_table(float* table, int64_t P, int R, double base, cudaStream_t stream) {
+  if (!table || P < 1 || R < 2 || R % 2 != 0 || !std::isfinite(base) || !(base > 0.0)) return BL_ERR_INVALID_ARG;
+  if (P > (int64_t(1) << 40) / R) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(table, 4)) return BL_ERR_ALIGNMENT;
+  rope_table_kernel<<<grid_for(P * (R / 2), 256), 256, 0, stream>>>(table, P, R / 2, base);
+  return launch_status();
+}
+
+bl_status bl_qk_norm_rope(const bl_qkv_rows* rows, bl_dtype t, void* q, void* k, void* v, cudaStream_t stream) {
+  const bl_status st = check_rows(rows, true);
+  if (st != BL_OK) return st;
+  if (!any_type(t)) return BL_ERR_INVALID_ARG;
+  if (rows->M == 0) return BL_OK;
+  if (!q || !k || !v) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(k, 16) || !is_aligned(v, 16)) return BL_ERR_ALIGNMENT;
+  QrArgs a = rows_args(rows);
+  a.oq = q;
+  a.ok = k;
+  a.ov = v;
+  if (t == BL_T_F32) return launch_norm_rope<float, false>(a, stream);
+  return t == BL_T_F16 ? launch_norm_rope<__half, false>(a, stream) : launch_norm_rope<__nv_bfloat16, false>(a, stream);
+}
+
+bl_status bl_qk_norm_rope_append(const bl_qkv_rows* rows, void* q, const bl_kv_pages* cache, const int64_t* slots,
+                                 cudaStream_t stream) {
+  bl_status st = check_rows(rows, true);
+  if (st != BL_OK) return st;
+  st = check_cache(cache);
+  if (st != BL_OK) return st;
+  if (cache->Hkv != rows->Hkv || cache->D != rows->D) return BL_ERR_INVALID_ARG;
+  if (rows->M == 0) return BL_OK;
+  if (!q || !slots) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(slots, 8)) return BL_ERR_ALIGNMENT;
+  QrArgs a = rows_args(rows);
+  a.oq = q;
+  a.ok = cache->k;
+  a.ov = cache->v;
+  a.slots = slots;
+  a.nslots = cache->pages * cache->page;
+  a.page = cache->page;
+  return cache->t == BL_T_F16 ? launch_norm_rope<__half, true>(a, stream)
+                              : launch_norm_rope<__nv_bfloat16, true>(a, stream);
+}
+
+size_t bl_qk_norm_rope_backward_workspace_size(const bl_qkv_rows* rows) {
+  if (check_rows(rows, false) != BL_OK || rows->M == 0) return 0;
+  return align_up(size_t(rows_back_grid(rows)) * 2 * size_t(rows->D) * 4);
+}
+
+bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const void* dq, const void* dk, const void* dv,
+                                   float* dxq, int64_t lddq, float* dxk, int64_t lddk, float* dxv, int64_t lddv,
+                                   float* dgq, float* dgk, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  bl_status st = check_rows(rows, false);
+  if (st != BL_OK) return st;
+  if (!any_type(t)) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(dgq, 4) || !is_aligned(dgk, 4)) return BL_ERR_ALIGNMENT;
+  if (rows->M == 0) {                                  // no rows: the gains' gradients are zero
+    if (dgq && cudaMemsetAsync(dgq, 0, size_t(rows->D) * 4, stream) != cudaSuccess) return BL_ERR_CUDA;
+    if (dgk && cudaMemsetAsync(dgk, 0, size_t(rows->D) * 4, stream) != cudaSuccess) return BL_ERR_CUDA;
+    return BL_OK;
+  }
+  if (!dq || !dk || !dv || !dxq || !dxk || !dxv) return BL_ERR_INVALID_ARG;
+  const int64_t wq = int64_t(rows->Hq) * rows->D, wk = int64_t(rows->Hkv) * rows->D;
+  if (lddq < wq || lddk < wk || lddv < wk) return BL_ERR_INVALID_ARG;
+  if (lddq % 4 != 0 || lddk % 4 != 0 || lddv % 4 != 0) return BL_ERR_ALIGNMENT;
+  if (!is_aligned(dq, 16) || !is_aligned(dk, 16) || !is_aligned(dv, 16) || !is_aligned(dxq, 16) ||
+      !is_aligned(dxk, 16) || !is_aligned(dxv, 16))
+    return BL_ERR_ALIGNMENT;
+  QrArgs a = rows_args(rows);
+  const int grid = rows_back_grid(rows);
+  if (dgq || dgk) {
+    st = check_ws(ws, ws_bytes, bl_qk_norm_rope_backward_workspace_size(rows));
+    if (st != BL_OK) return st;
+    a.part = static_cast<float*>(ws);
+  }
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dxq = dxq;
+  a.dxk = dxk;
+  a.dxv = dxv;
+  a.lddq = lddq;
+  a.lddk = lddk;
+  a.lddv = lddv;
+  const int smem = (kQrThreads / a.lanes) * 2 * a.D * 4;       // at most 16 KB
+  const void* fn = t == BL_T_F32   ? reinterpret_cast<const void*>(qk_norm_rope_backward_kernel<float>)
+                   : t == BL_T_F16 ? reinterpret_cast<const void*>(qk_norm_rope_backward_kernel<__half>)
+                                   : reinterpret_cast<const void*>(qk_norm_rope_backward_kernel<__nv_bfloat16>);
+  void* args[] = {&a};
+  if (cudaLaunchKernel(fn, dim3(unsigned(grid)), dim3(kQrThreads), args, size_t(smem), stream) != cudaSuccess)
+    return BL_ERR_CUDA;
+  if (a.part) gain_sum_kernel<<<unsigned(ceil_div(2 * a.D, 32)), 256, 0, stream>>>(a.part, grid, a.D, dgq, dgk);
+  return launch_status();
+}
+
+bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStream_t stream) {
+  const bl_status st = check_attn(call);
+  if (st != BL_OK) return st;
+  if (call->B == 0 || call->Tq == 0 || call->max_q == 0) return BL_OK;
+  if (!out) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(out, 16) || !is_aligned(lse, 4)) return BL_ERR_ALIGNMENT;
+  AttnArgs a = attn_args(call);
+  a.out = out;
+  a.lse = lse;
+  return call->t == BL_T_F16 ? run_attn<__half>(a, stream) : run_attn<__nv_bfloat16>(a, stream);
+}
+
+size_t bl_attention_backward_workspace_size(const bl_attn_call* call) {
+  if (check_attn(call) != BL_OK || call->B == 0 || call->Tq == 0) return 0;
+  return align_up(size_t(call->Tq) * size_t(call->Hq) * 4);
+}
+
+bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
+                                void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  bl_status st = check_attn(call);
+  if (st != BL_OK) return st;
+  if (call->B == 0 || call->Tq == 0) return BL_OK;
+  if (!out || !lse || !dout || !dq || (call->Tk > 0 && (!dk || !dv))) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(dout, 16) || !is_aligned(dq, 16) ||
+      !is_aligned(dk, 16) || !is_aligned(dv, 16))
+    return BL_ERR_ALIGNMENT;
+  st = check_ws(ws, ws_bytes, bl_attention_backward_workspace_size(call));
+  if (st != BL_OK) return st;
+  AttnArgs a = attn_args(call);
+  a.o = out;
+  a.lse = const_cast<float*>(lse);
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.delta = static_cast<float*>(ws);
+  return call->t == BL_T_F16 ? run_attn_backward<__half>(a, stream) : run_attn_backward<__nv_bfloat16>(a, stream);
+}
+
+size_t bl_paged_attention_workspace_size(int64_t B, int Hq, const bl_kv_pages* cache) {
+  if (!cache || B < 1 || Hq < 1 || cache->Hkv < 1 || Hq % cache->Hkv != 0 || cache->D < 8 || cache->D > kAttnMaxD) return 0;
+  const int heads = 8 * paged_nt(Hq, cache->Hkv);
+  return kPaCountBytes + align_up(size_t(2 * kPaCtas) * size_t(heads) * size_t(paged_pad(cache->D) + 2) * 4);
+}
+
+bl_status bl_paged_attention(const void* q, int64_t B, int Hq, const bl_kv_pages* cache, const int32_t* table,
+                             int64_t ldt, const int32_t* lens, int32_t window, int32_t sinks, float scale,
+                             bl_dtype out_t, void* out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  bl_status st = check_cache(cache);
+  if (st != BL_OK) return st;
+  if (B < 0 || !int32_max(B) || Hq < 1 || Hq > 65535 || Hq % cache->Hkv != 0 || cache->D > kAttnMaxD) return BL_ERR_INVALID_ARG;
+  if (ldt < 1 || !int32_max(ldt) || window < 0 || sinks < 0 || !std::isfinite(scale) || !(scale > 0.f))
+    return BL_ERR_INVALID_ARG;
+  if (out_t != BL_T_F32 && out_t != cache->t) return BL_ERR_INVALID_ARG;
+  if (B == 0) return BL_OK;
+  if (!q || !table || !lens || !out) return BL_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(table, 4) || !is_aligned(lens, 4) || !is_aligned(out, 16)) return BL_ERR_ALIGNMENT;
+  st = check_ws(ws, ws_bytes, bl_paged_attention_workspace_size(B, Hq, cache));
+  if (st != BL_OK) return st;
+  PaArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.table = table;
+  a.lens = lens;
+  a.ldt = ldt;
+  a.pages = cache->pages;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = cache->Hkv;
+  a.D = cache->D;
+  a.page = cache->page;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = scale * kLog2e;
+  a.out = out;
+  a.count = static_cast<unsigned int*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kPaCountBytes);
+  a.group = Hq / cache->Hkv;
+  a.chunks = int(ceil_div(a.group, 8 * paged_nt(Hq, cache->Hkv)));
+  // j / page for j < 2^31 as umulhi(j, magic) >> shift, shift = ceil(log2 page) - 1
+  if (a.page > 1) {
+    while ((uint64_t(2) << a.page_shift) < uint64_t(a.page)) ++a.page_shift;
+    a.page_magic = uint32_t((uint64_t(1) << (32 + a.page_shift)) / uint64_t(a.page) + 1);
+  }
+  const bool f32 = out_t == BL_T_F32;
+  return cache->t == BL_T_F16 ? launch_paged_t<__half>(a, f32, stream) : launch_paged_t<__nv_bfloat16>(a, f32, stream);
+}
+
+}  // extern "C"

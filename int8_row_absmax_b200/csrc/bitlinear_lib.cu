@@ -1558,6 +1558,7 @@ bl_status bl_sync_status(cudaStream_t stream) {
   if (word && cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return BL_ERR_CUDA;
   if (word & kDevTimeout) return BL_ERR_DEVICE_TIMEOUT;
   if (word & kDevBadWorkspace) return BL_ERR_WORKSPACE;
+  if (word & kDevRange) return BL_ERR_RANGE;
   if (word & kDevNonFinite) return BL_ERR_NONFINITE;
   return launch_status();
 }
@@ -1573,8 +1574,11 @@ const char* bl_status_string(bl_status s) {
     case BL_ERR_DEVICE_TIMEOUT: return "BL_ERR_DEVICE_TIMEOUT";
     case BL_ERR_NONFINITE: return "BL_ERR_NONFINITE";
     case BL_ERR_IO: return "BL_ERR_IO";
+    case BL_ERR_RANGE: return "BL_ERR_RANGE";
   }
   return "BL_ERR_UNKNOWN";
 }
 
 }  // extern "C"
+
+#include "attention_abi.cuh"

@@ -10,7 +10,7 @@
 namespace bl {
 
 // Per-device status word.  Kernels OR flags in; bl_sync_status reads and clears.
-enum : unsigned int { kDevTimeout = 1u, kDevNonFinite = 2u, kDevBadWorkspace = 4u };
+enum : unsigned int { kDevTimeout = 1u, kDevNonFinite = 2u, kDevBadWorkspace = 4u, kDevRange = 8u };
 __device__ unsigned int g_status = 0u;
 
 __device__ __forceinline__ void raise_status(unsigned int f) { atomicOr(&g_status, f); }

@@ -1,0 +1,478 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+// "ultragraph-1bit 0.12.0" (PyPI): a cached step gives what the full forward
+// gives.  Row b: softmax(scale q_b K^T) V over the visible tokens of sequence b.
+//
+// Bound by memory: every visible key and value is read once, 4 D bytes per token
+// and key head, for 4 D operations per query head.  So
+//   - the visible 64-token tiles of all sequences and key heads form one line that
+//     is cut into equal parts, one per CTA (two CTAs an SM): ragged batches and a
+//     single long sequence load every SM alike;
+//   - tiles arrive by 16-byte asynchronous copies, kPaStages in flight, the page of
+//     each row looked up two tiles ahead; rows that are not visible are filled with
+//     zeros instead of being read;
+//   - the scores are taken transposed, S^T = K q^T (keys are the 16-row side of the
+//     m16n8k16 matrix instruction, the group's query heads its 8 columns), and so is
+//     O^T = V^T P^T: a group of up to 8 heads shares each tile's one trip through
+//     shared memory.  The tensor pipe is far from its limit at 8 columns, and
+//     tcgen05's tiles (at least 64 rows of one operand, 8 columns of the other, but
+//     staged through tensor memory with its own waits) would add latency and no rate;
+//   - P keeps float32's precision: it is split into terms of the cache's type (three
+//     bfloat16 terms of 8 bits, two float16 terms of 11), each its own product;
+//   - each warp keeps the running maximum and sum of its own 16 keys per tile, so the
+//     loop has one barrier; warps are joined when a head ends, CTAs by the last one
+//     to finish (a counter per head part, reset by it), in the order of the line.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_common.cuh"
+
+namespace bl {
+
+constexpr int kPaThreads = 128, kPaTile = 64, kPaStages = 3;
+constexpr int kPaCtas = 296;                         // two for each of B200's 148 SMs
+constexpr float kPaLow = -1e30f;                     // below every finite scaled score that matters
+
+struct PaArgs {
+  const void *q, *k, *v;
+  const int32_t *table, *lens;
+  int64_t ldt, pages, B;
+  int Hq, Hkv, D, page, window, sinks;
+  float scale_log2;
+  void* out;
+  unsigned int* count;      // [kPaCtas]
+  float* part;              // [2 kPaCtas][8 NT][DP + 2]
+  int group, chunks;        // query heads per key head; ceil(group / (8 NT))
+  uint32_t page_magic, page_shift;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <typename T> __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <> __device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile with rows of DP elements; the
+// xor spreads the 8 rows that one ldmatrix phase reads over all banks.
+template <int DP> __device__ __forceinline__ uint32_t pa_off(int r, int c) {
+  const int x = DP >= 64 ? (r & 7) : ((r >> 1) & 3);
+  return uint32_t(r * DP * 2 + ((c ^ x) << 4));
+}
+
+// The visible tiles of a sequence of `len` tokens: `lead` of them from tile 0, the
+// others from tile `from` on.
+struct PaTiles {
+  int lead, from, n;
+};
+__device__ __forceinline__ PaTiles pa_tiles(int len, int window, int sinks) {
+  PaTiles t;
+  const int all = (len + kPaTile - 1) / kPaTile;
+  t.lead = 0;
+  t.from = 0;
+  if (window != 0 && len > window) {
+    const int ws = len - window;
+    t.lead = (min(sinks, ws) + kPaTile - 1) / kPaTile;
+    t.from = max(t.lead, ws / kPaTile);
+  }
+  t.n = t.lead + all - t.from;
+  return t;
+}
+__device__ __forceinline__ int pa_len(const PaArgs& a, int64_t b, bool& range) {
+  const int n = a.lens[b];
+  const int64_t most = a.ldt * a.page;
+  if (n < 0 || n > most) range = true;
+  return n < 0 ? 0 : n > most ? int(most) : n;
+}
+
+template <typename T, int DP, int NT>
+struct PaCfg {
+  static constexpr int kTileBytes = kPaTile * DP * 2;
+  static constexpr int kStage = 2 * kTileBytes;
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kJoin = kHeads * DP * 4;
+  static constexpr int kSmem = kPaStages * kStage + kJoin;
+};
+
+// Position in the line of tiles: sequence b, key head and chunk (item), tile t of it.
+struct PaAt {
+  int64_t b, flat;          // flat: line index of the item's first tile
+  int item, t, len;         // item = hk * chunks + chunk
+  PaTiles tiles;
+};
+
+template <typename T, int DP, int NT, typename OutT>
+__global__ void __launch_bounds__(kPaThreads, 2)
+paged_attn_kernel(const PaArgs a) {
+  using C = PaCfg<T, DP, NT>;
+  extern __shared__ __align__(128) unsigned char pa_smem[];
+  unsigned char* smem = pa_smem;
+  __shared__ int64_t s_row[2][kPaTile];          // element offset of each row's head data, -1: not visible
+  __shared__ float s_m[4][C::kHeads], s_l[4][C::kHeads];
+  __shared__ int64_t s_scan[4];
+  __shared__ int64_t s_find[2];                  // sequence of this CTA's first tile, line index of its first tile
+  __shared__ unsigned int s_last;
+  constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
+  constexpr float kShift = std::is_same<T, __half>::value ? 14.f : 0.f;   // keeps float16 terms of small probabilities normal
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = smem_u32(smem);
+  float* join = reinterpret_cast<float*>(smem + kPaStages * C::kStage);
+  const int items = a.Hkv * a.chunks;
+  bool range = false, bad = false;
+
+  // the line: total tiles, this CTA's part, and the sequence where it begins
+  int64_t total = 0;
+  for (int64_t b = tid; b < a.B; b += kPaThreads) total += pa_tiles(pa_len(a, b, range), a.window, a.sinks).n;
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) s_scan[warp] = total;
+  __syncthreads();
+  total = (s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3]) * items;
+  const int64_t ctas = min(int64_t(gridDim.x), total);
+  // rows without tokens are nobody's tiles: zeros from the CTAs in turn
+  for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (pa_len(a, b, range) == 0)
+      for (int i = tid; i < a.Hq * a.D; i += kPaThreads) static_cast<OutT*>(a.out)[b * a.Hq * a.D + i] = from_f32<OutT>(0.f);
+  if (range) raise_status(kDevRange);
+  if (int64_t(blockIdx.x) >= ctas) return;
+  const int64_t lo = int64_t(blockIdx.x) * total / ctas, hi = (int64_t(blockIdx.x) + 1) * total / ctas;
+  {
+    int64_t before = 0;                              // line tiles of the sequences before this round's
+    for (int64_t b0 = 0; b0 < a.B; b0 += kPaThreads) {
+      const int64_t b = b0 + tid;
+      const int64_t n = b < a.B ? int64_t(pa_tiles(pa_len(a, b, range), a.window, a.sinks).n) * items : 0;
+      int64_t x = n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = x;
+      __syncthreads();
+      int64_t first = before + x - n;
+      for (int w = 0; w < warp; ++w) first += s_scan[w];
+      if (n > 0 && first <= lo && lo < first + n) {
+        s_find[0] = b;
+        s_find[1] = first;
+      }
+      before += s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
+      if (before > lo) break;
+    }
+    __syncthreads();
+  }
+
+  auto enter = [&](PaAt& p, int64_t b, int64_t first, int64_t x) {   // line index x, in sequence b whose tiles begin at first
+    p.b = b;
+    p.len = pa_len(a, b, range);
+    p.tiles = pa_tiles(p.len, a.window, a.sinks);
+    p.item = int((x - first) / p.tiles.n);
+    p.flat = first + int64_t(p.item) * p.tiles.n;
+    p.t = int(x - p.flat);
+  };
+  auto advance = [&](PaAt& p) {                                      // to the next tile of the line
+    if (++p.t < p.tiles.n) return;
+    p.t = 0;
+    p.flat += p.tiles.n;
+    if (++p.item < items) return;
+    p.item = 0;
+    do {
+      if (++p.b >= a.B) return;
+      p.len = pa_len(a, p.b, range);
+      p.tiles = pa_tiles(p.len, a.window, a.sinks);
+    } while (p.tiles.n == 0);
+  };
+  // thread tid < 64: where row tid of p's tile is
+  auto locate = [&](const PaAt& p) -> int64_t {
+    const int t = p.t < p.tiles.lead ? p.t : p.t - p.tiles.lead + p.tiles.from;
+    const int j = t * kPaTile + tid;
+    if (!(j < p.len && sees(p.len - 1, j, a.window, a.sinks))) return -1;
+    const uint32_t n = a.page == 1 ? uint32_t(j) : __umulhi(uint32_t(j), a.page_magic) >> a.page_shift;
+    const int64_t page = a.table[p.b * a.ldt + n];
+    if (page < 0 || page >= a.pages) {
+      range = true;
+      return -1;
+    }
+    return ((page * a.Hkv + p.item / a.chunks) * a.page + (j - int(n) * a.page)) * int64_t(a.D);
+  };
+  const int row_chunks = a.D >> 3;
+  auto issue = [&](int stage, int buf) {
+    const uint32_t kd = base + stage * C::kStage, vd = kd + C::kTileBytes;
+    for (int i = tid; i < kPaTile * row_chunks; i += kPaThreads) {
+      const int r = i / row_chunks, c = i - r * row_chunks;
+      const int64_t off = s_row[buf][r];
+      const int n = off < 0 ? 0 : 16;
+      const int64_t e = off < 0 ? 0 : off + 8 * c;
+      const uint32_t d = pa_off<DP>(r, c);
+      cp_async16(kd + d, static_cast<const T*>(a.k) + e, n);
+      cp_async16(vd + d, static_cast<const T*>(a.v) + e, n);
+    }
+  };
+
+  if (a.D < DP) {                                    // columns past D: zeros, never written again
+    for (int i = tid; i < kPaStages * C::kStage / 16; i += kPaThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+
+  PaAt cur, load;
+  enter(cur, s_find[0], s_find[1], lo);
+  load = cur;
+  const int n = int(hi - lo);                        // tiles of this CTA
+  int located = 0;                                   // tiles whose rows are known
+  auto next_rows = [&]() {
+    if (located < n) {
+      if (tid < kPaTile) s_row[located & 1][tid] = locate(load);
+      ++located;
+      advance(load);
+    }
+  };
+  next_rows();
+  for (int s = 0; s < kPaStages - 1; ++s) {
+    next_rows();
+    __syncthreads();
+    if (s < n) issue(s, s & 1);
+    cp_async_commit();
+    __syncthreads();
+  }
+
+  // per-lane state: heads 2 (lane % 4) + {0, 1} of each 8
+  float m[NT][2], l[NT][2], o[DP / 16][NT][4];
+  uint32_t qf[DP / 16][NT][2];
+  const int hpair = (lane & 3) * 2;
+  auto begin_item = [&]() {
+    const int hk = cur.item / a.chunks, ch = cur.item - hk * a.chunks;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int hg = ch * C::kHeads + u * 8 + (lane >> 2);      // head in the group: the B operand's column
+      const T* q = static_cast<const T*>(a.q) + (cur.b * a.Hq + int64_t(hk) * a.group + hg) * a.D;
+#pragma unroll
+      for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int d = ks * 16 + half * 8 + hpair;
+          qf[ks][u][half] = hg < a.group && d < a.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+        }
+      m[u][0] = m[u][1] = kPaLow;
+      l[u][0] = l[u][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][u][e] = 0.f;
+    }
+  };
+  begin_item();
+  int seg_first = cur.t;                             // first tile of this segment within the item
+
+  for (int it = 0; it < n; ++it) {
+    cp_async_wait<kPaStages - 2>();
+    __syncthreads();
+    if (it + kPaStages - 1 < n) issue((it + kPaStages - 1) % kPaStages, (it + kPaStages - 1) & 1);
+    cp_async_commit();
+    // rows of tile it + kPaStages: into the buffer that tile it + kPaStages - 2 used (issued before this barrier)
+    next_rows();
+
+    const uint32_t ks_base = base + (it % kPaStages) * C::kStage, vs_base = ks_base + C::kTileBytes;
+    const int r0 = warp * 16;
+    float s[NT][4];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < DP / 16; ++ks) {
+      uint32_t f[4];
+      ldsm4(f, ks_base + pa_off<DP>(r0 + (lane & 15), 2 * ks + (lane >> 4)));
+#pragma unroll
+      for (int u = 0; u < NT; ++u) mma16816<T>(s[u], f, qf[ks][u][0], qf[ks][u][1]);
+    }
+    const int tile = cur.t < cur.tiles.lead ? cur.t : cur.t - cur.tiles.lead + cur.tiles.from;
+    const int j = tile * kPaTile + r0 + (lane >> 2);
+    const bool v0 = j < cur.len && sees(cur.len - 1, j, a.window, a.sinks);
+    const bool v1 = j + 8 < cur.len && sees(cur.len - 1, j + 8, a.window, a.sinks);
+    uint32_t pf[NT][kTerms][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x0 = v0 ? s[u][e] * a.scale_log2 : -INFINITY, x1 = v1 ? s[u][2 + e] * a.scale_log2 : -INFINITY;
+        float t = fmaxf(x0, x1);
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        if (t > m[u][e]) {                           // the same for the eight lanes of a column
+          const float f = exp2_approx(m[u][e] - t);
+          m[u][e] = t;
+          l[u][e] *= f;
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) {
+            o[i][u][e] *= f;
+            o[i][u][2 + e] *= f;
+          }
+        }
+        s[u][e] = exp2_approx(x0 - m[u][e] + kShift);
+        s[u][2 + e] = exp2_approx(x1 - m[u][e] + kShift);
+        l[u][e] += s[u][e] + s[u][2 + e];
+      }
+#pragma unroll
+      for (int k = 0; k < kTerms; ++k) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t w = pack2<T>(s[u][2 * half], s[u][2 * half + 1]);
+          const float2 back = unpack2<T>(w);
+          s[u][2 * half] -= back.x;
+          s[u][2 * half + 1] -= back.y;
+          pf[u][k][half] = movm_t(w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      uint32_t f[4];
+      ldsm4_t(f, vs_base + pa_off<DP>(r0 + (lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) mma16816<T>(o[i][u], f, pf[u][k][0], pf[u][k][1]);
+    }
+
+    const bool item_ends = cur.t + 1 == cur.tiles.n;
+    if (item_ends || it + 1 == n) {
+      // join the warps: statistics first, then O in the order of the warps
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = l[u][e];
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          if (lane < 4) {
+            s_m[warp][u * 8 + hpair + e] = m[u][e];
+            s_l[warp][u * 8 + hpair + e] = x;
+          }
+        }
+      __syncthreads();
+      float f[NT][2];
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = u * 8 + hpair + e;
+          const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+          f[u][e] = exp2_approx(m[u][e] - top);
+        }
+      for (int w = 0; w < 4; ++w) {
+        if (w == warp) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float* d = join + (u * 8 + hpair + (e & 1)) * DP + i * 16 + (lane >> 2) + 8 * (e >> 1);
+                const float x = o[i][u][e] * f[u][e & 1];
+                *d = w == 0 ? x : *d + x;
+              }
+        }
+        __syncthreads();
+      }
+      const int hk = cur.item / a.chunks, ch = cur.item - hk * a.chunks;
+      const int nh = min(C::kHeads, a.group - ch * C::kHeads);       // live heads
+      OutT* out = static_cast<OutT*>(a.out) + (cur.b * a.Hq + int64_t(hk) * a.group + ch * C::kHeads) * a.D;
+      if (item_ends && seg_first == 0) {                             // the whole item is this CTA's
+        for (int i = tid; i < nh * a.D; i += kPaThreads) {
+          const int h = i / a.D, d = i - h * a.D;
+          const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+          float sum = 0.f;
+          for (int w = 0; w < 4; ++w) sum = fmaf(s_l[w][h], exp2_approx(s_m[w][h] - top), sum);
+          const float r = join[h * DP + d] / sum;
+          if (!(fabsf(r) < INFINITY)) bad = true;
+          out[i] = from_f32<OutT>(r);
+        }
+      } else {
+        // its part to the workspace: slot 0 of the CTA if the item began before it, slot 1 if it goes on
+        float* part = a.part + (2 * int64_t(blockIdx.x) + (seg_first == 0 ? 1 : 0)) * C::kHeads * (DP + 2);
+        for (int i = tid; i < nh * DP; i += kPaThreads) __stcg(part + (i / DP) * (DP + 2) + i % DP, join[i]);
+        for (int h = tid; h < nh; h += kPaThreads) {
+          const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+          float sum = 0.f;
+          for (int w = 0; w < 4; ++w) sum = fmaf(s_l[w][h], exp2_approx(s_m[w][h] - top), sum);
+          __stcg(part + h * (DP + 2) + DP, top);
+          __stcg(part + h * (DP + 2) + DP + 1, sum);
+        }
+        __threadfence();
+        __syncthreads();
+        // CTAs of the item: those that hold its first and its last tile, and all between
+        const int64_t c0 = ((cur.flat + 1) * ctas + total - 1) / total - 1;
+        const int64_t c1 = ((cur.flat + cur.tiles.n) * ctas + total - 1) / total - 1;
+        if (tid == 0) {
+          const unsigned int before = atomicAdd(a.count + c0, 1u);
+          s_last = before == unsigned(c1 - c0);
+          if (s_last) a.count[c0] = 0u;
+          if (before > unsigned(c1 - c0)) raise_status(kDevBadWorkspace);
+          __threadfence();
+        }
+        __syncthreads();
+        if (s_last) {
+          constexpr int kStride = C::kHeads * (DP + 2);
+          for (int i = tid; i < nh * a.D; i += kPaThreads) {
+            const int h = i / a.D, d = i - h * a.D;
+            float top = kPaLow, sum = 0.f, x = 0.f;
+            for (int64_t c = c0; c <= c1; ++c) {
+              const float* p = a.part + (2 * c + (c == c0 ? 1 : 0)) * kStride + h * (DP + 2);
+              const float pm = __ldcg(p + DP), pl = __ldcg(p + DP + 1), px = __ldcg(p + d);
+              const float t = fmaxf(top, pm), f0 = exp2_approx(top - t), f1 = exp2_approx(pm - t);
+              sum = fmaf(sum, f0, pl * f1);
+              x = fmaf(x, f0, px * f1);
+              top = t;
+            }
+            const float r = x / sum;
+            if (!(fabsf(r) < INFINITY)) bad = true;
+            out[i] = from_f32<OutT>(r);
+          }
+        }
+      }
+      __syncthreads();                                               // join, s_m free again
+      if (it + 1 < n) {
+        advance(cur);
+        begin_item();
+        seg_first = 0;
+      }
+    } else {
+      advance(cur);
+    }
+  }
+  if (bad) raise_status(kDevNonFinite);
+  if (range) raise_status(kDevRange);
+}
+
+}  // namespace bl

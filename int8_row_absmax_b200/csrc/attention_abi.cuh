@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn.cuh"
+#include "attn_fwd.cuh"
 #include "paged_attn.cuh"
 #include "qk_rope.cuh"
 
@@ -138,11 +139,44 @@ AttnArgs attn_args(const bl_attn_call* c) {
   return a;
 }
 
+// 16-bit rows [tokens, heads, D] as boxes of 128 tokens x 64 elements of one head,
+// 128-byte swizzle; elements past D and tokens past the buffer read as zero.
+bool make_map_rows(CUtensorMap* map, bool f16, const void* base, int64_t ld, int heads, int D, int64_t tokens) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(ld) * 2};
+  const cuuint32_t box[3] = {64u, 1u, 128u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int DP>
+bl_status launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
+  constexpr bool f16 = std::is_same<T, __half>::value;
+  AttnMaps maps;
+  if (!make_map_rows(&maps.q, f16, a.q, a.ldq, a.Hq, a.D, a.Tq)) return BL_ERR_CUDA;
+  if (a.Tk > 0) {
+    if (!make_map_rows(&maps.k, f16, a.k, a.ldk, a.Hkv, a.D, a.Tk) ||
+        !make_map_rows(&maps.v, f16, a.v, a.ldv, a.Hkv, a.D, a.Tk))
+      return BL_ERR_CUDA;
+  } else {
+    maps.k = maps.v = maps.q;                            // no keys: never loaded from
+  }
+  constexpr int smem = AfCfg<DP>::kSmem;
+  if (cudaFuncSetAttribute(attn_fwd_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return BL_ERR_CUDA;
+  const bool two = (a.Hq / a.Hkv) % 2 == 0;
+  const int64_t grid = int64_t(two ? a.Hq / 2 : a.Hq) * a.B * ceil_div(a.max_q, two ? 128 : 256);
+  if (!int32_max(grid)) return BL_ERR_UNSUPPORTED;
+  attn_fwd_kernel<T, DP><<<unsigned(grid), kAfThreads, smem, st>>>(maps, a);
+  return launch_status();
+}
 template <typename T>
 bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
-  attn_simple_kernel<T><<<dim3(unsigned(ceil_div(a.max_q, kSimpleWarps)), unsigned(a.Hq), unsigned(a.B)),
-                          32 * kSimpleWarps, 0, st>>>(a);
-  return launch_status();
+  return a.D <= 64 ? launch_attn_fwd<T, 64>(a, st) : launch_attn_fwd<T, 128>(a, st);
 }
 
 template <typename T>

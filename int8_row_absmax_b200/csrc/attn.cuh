@@ -3,6 +3,8 @@
 // 2", section "attention, as graph ops": softmax(Q K^T / sqrt(d) + mask) V).
 #pragma once
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace bl {
@@ -37,62 +39,6 @@ __device__ __forceinline__ bool load_seq(const AttnArgs& a, int b, Seq& s, bool 
 }
 
 constexpr int kSimpleWarps = 4;
-
-// One warp per query row and head, 32 keys a turn.
-template <typename T>
-__global__ void __launch_bounds__(32 * kSimpleWarps)
-attn_simple_kernel(const AttnArgs a) {
-  __shared__ float sq[kSimpleWarps][128];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Seq s;
-  if (!load_seq(a, blockIdx.z, s, false)) return;
-  const int i = blockIdx.x * kSimpleWarps + w, h = blockIdx.y;
-  if (i >= s.nq) return;
-  const int hk = h / (a.Hq / a.Hkv), p = i + s.nk - s.nq;
-  const T* q = static_cast<const T*>(a.q) + int64_t(s.q0 + i) * a.ldq + int64_t(h) * a.D;
-  for (int d = lane; d < a.D; d += 32) sq[w][d] = to_f32(q[d]);
-  __syncwarp();
-  const float c = a.scale * kLog2e;
-  float top = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 <= p; j0 += 32) {
-    const int j = j0 + lane;
-    const bool see = j < s.nk && sees(p, j, a.window, a.sinks);
-    if (!__any_sync(0xffffffffu, see)) continue;
-    float x = -INFINITY;
-    if (see) {
-      const T* k = static_cast<const T*>(a.k) + int64_t(s.k0 + j) * a.ldk + int64_t(hk) * a.D;
-      float t = 0.f;
-      for (int d = 0; d < a.D; ++d) t = fmaf(sq[w][d], to_f32(k[d]), t);
-      x = t * c;
-    }
-    const float m = fmaxf(top, warp_max(x));
-    const float e = see ? exp2_approx(x - m) : 0.f;
-    const float f = exp2_approx(top - m);
-    sum *= f;
-    for (int u = 0; u < 4; ++u) o[u] *= f;
-    top = m;
-    sum += e;
-    for (int t = 0; t < 32 && j0 + t < s.nk; ++t) {
-      const float pt = __shfl_sync(0xffffffffu, e, t);
-      if (pt == 0.f) continue;
-      const T* v = static_cast<const T*>(a.v) + int64_t(s.k0 + j0 + t) * a.ldv + int64_t(hk) * a.D;
-      for (int u = 0; u < 4; ++u)
-        if (lane + 32 * u < a.D) o[u] = fmaf(pt, to_f32(v[lane + 32 * u]), o[u]);
-    }
-  }
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  T* out = static_cast<T*>(a.out) + (int64_t(s.q0 + i) * a.Hq + h) * a.D;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  bool bad = !(sum < INFINITY);
-  for (int u = 0; u < 4; ++u)
-    if (lane + 32 * u < a.D) {
-      const float r = o[u] * inv;
-      if (!(fabsf(r) < INFINITY)) bad = true;
-      out[lane + 32 * u] = from_f32<T>(r);
-    }
-  if (bad) raise_status(kDevNonFinite);
-  if (a.lse && lane == 0) a.lse[int64_t(h) * a.Tq + s.q0 + i] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-}
 
 // delta = rowsum(dO O): one warp per row and head.
 template <typename T>

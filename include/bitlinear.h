@@ -467,7 +467,7 @@ typedef struct {
   int32_t Hq, Hkv, D;
   const void *q, *k, *v;      /* [Tq, Hq, D], [Tk, Hkv, D], [Tk, Hkv, D]; heads D apart, 16-byte aligned */
   int64_t ldq, ldk, ldv;      /* elements between tokens, multiples of 8 */
-  int64_t Tq, Tk;             /* rows of the buffers (< 2^31) */
+  int64_t Tq, Tk;             /* rows of the buffers (< 2^30) */
   const int32_t *cu_q, *cu_k; /* [B + 1], not falling, within 0 .. Tq and 0 .. Tk */
   int32_t B;
   int32_t max_q, max_k;       /* at least the longest Lq and Lk (max_k: the backward only) */

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn.cuh"
+#include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
 #include "paged_attn.cuh"
 #include "qk_rope.cuh"
@@ -12,6 +13,7 @@ namespace bl {
 namespace {
 
 constexpr int kAttnMaxD = 128, kRopeMaxD = 256;
+constexpr int64_t kAttnMaxRows = int64_t(1) << 30;      // sums of two positions stay within 31 bits
 
 bool half_type(bl_dtype t) { return t == BL_T_F16 || t == BL_T_BF16; }
 bool any_type(bl_dtype t) { return t == BL_T_F32 || half_type(t); }
@@ -100,13 +102,13 @@ bl_status check_attn(const bl_attn_call* c) {
   if (!c || !half_type(c->t)) return BL_ERR_INVALID_ARG;
   if (c->Hq < 1 || c->Hkv < 1 || c->Hq > 65535 || c->Hq % c->Hkv != 0) return BL_ERR_INVALID_ARG;
   if (c->D < 8 || c->D % 8 != 0 || c->D > kAttnMaxD) return BL_ERR_INVALID_ARG;
-  if (c->Tq < 0 || c->Tk < 0 || !int32_max(c->Tq) || !int32_max(c->Tk)) return BL_ERR_INVALID_ARG;
+  if (c->Tq < 0 || c->Tk < 0 || c->Tq >= kAttnMaxRows || c->Tk >= kAttnMaxRows) return BL_ERR_INVALID_ARG;
   if (c->B < 0 || c->B > 65535 || c->max_q < 0 || c->max_k < 0 || c->window < 0 || c->sinks < 0) return BL_ERR_INVALID_ARG;
   if (!std::isfinite(c->scale) || !(c->scale > 0.f)) return BL_ERR_INVALID_ARG;
-  if (c->B == 0 || c->Tq == 0) return BL_OK;
-  if (!c->q || !c->cu_q || !c->cu_k || (c->Tk > 0 && (!c->k || !c->v))) return BL_ERR_INVALID_ARG;
+  if (c->B == 0 || (c->Tq == 0 && c->Tk == 0)) return BL_OK;
+  if ((c->Tq > 0 && !c->q) || !c->cu_q || !c->cu_k || (c->Tk > 0 && (!c->k || !c->v))) return BL_ERR_INVALID_ARG;
   const int64_t wq = int64_t(c->Hq) * c->D, wk = int64_t(c->Hkv) * c->D;
-  if (c->ldq < wq || (c->Tk > 0 && (c->ldk < wk || c->ldv < wk))) return BL_ERR_INVALID_ARG;
+  if ((c->Tq > 0 && c->ldq < wq) || (c->Tk > 0 && (c->ldk < wk || c->ldv < wk))) return BL_ERR_INVALID_ARG;
   if (c->ldq % 8 != 0 || c->ldk % 8 != 0 || c->ldv % 8 != 0) return BL_ERR_ALIGNMENT;
   if (!is_aligned(c->q, 16) || !is_aligned(c->k, 16) || !is_aligned(c->v, 16) || !is_aligned(c->cu_q, 4) ||
       !is_aligned(c->cu_k, 4))
@@ -133,7 +135,7 @@ AttnArgs attn_args(const bl_attn_call* c) {
   a.B = c->B;
   a.max_q = c->max_q;
   a.max_k = c->max_k;
-  a.window = c->window;
+  a.window = c->window >= c->Tk ? 0 : c->window;         // no window at all, then
   a.sinks = c->sinks;
   a.scale = c->scale;
   return a;
@@ -179,16 +181,41 @@ bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
   return a.D <= 64 ? launch_attn_fwd<T, 64>(a, st) : launch_attn_fwd<T, 128>(a, st);
 }
 
-template <typename T>
-bl_status run_attn_backward(const AttnArgs& a, cudaStream_t st) {
-  attn_delta_kernel<T><<<unsigned(ceil_div(a.Tq * a.Hq, 4)), 128, 0, st>>>(a);
-  if (a.max_q > 0)
-    attn_dq_simple_kernel<T><<<dim3(unsigned(ceil_div(a.max_q, kSimpleWarps)), unsigned(a.Hq), unsigned(a.B)),
-                               32 * kSimpleWarps, 0, st>>>(a);
-  if (a.max_k > 0)
-    attn_dkv_simple_kernel<T><<<dim3(unsigned(ceil_div(a.max_k, kSimpleWarps)), unsigned(a.Hkv), unsigned(a.B)),
-                                32 * kSimpleWarps, 0, st>>>(a);
+// The backward's workspace: the two norms (float16), then delta [Hq, Tq].
+constexpr size_t kAbNormBytes = 256;
+
+template <typename T, int DP>
+bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
+  constexpr bool f16 = std::is_same<T, __half>::value;
+  AttnBwdMaps maps;
+  const bool queries = a.Tq > 0, keys = a.Tk > 0;
+  if (queries && (!make_map_rows(&maps.q, f16, a.q, a.ldq, a.Hq, a.D, a.Tq) ||
+                  !make_map_rows(&maps.dout, f16, a.dout, int64_t(a.Hq) * a.D, a.Hq, a.D, a.Tq)))
+    return BL_ERR_CUDA;
+  if (keys && (!make_map_rows(&maps.k, f16, a.k, a.ldk, a.Hkv, a.D, a.Tk) ||
+               !make_map_rows(&maps.v, f16, a.v, a.ldv, a.Hkv, a.D, a.Tk)))
+    return BL_ERR_CUDA;
+  if (!queries) maps.q = maps.dout = maps.k;             // never loaded from
+  if (!keys) maps.k = maps.v = maps.q;
+  if (cudaFuncSetAttribute(attn_dkv_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, AbCfg<DP>::kDkvSmem) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(attn_dq_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, AbCfg<DP>::kDqSmem) !=
+          cudaSuccess)
+    return BL_ERR_CUDA;
+  const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
+  if (!int32_max(gq) || !int32_max(gk)) return BL_ERR_UNSUPPORTED;
+  if (f16 && cudaMemsetAsync(norms, 0, 8, st) != cudaSuccess) return BL_ERR_CUDA;
+  if (queries) {
+    const int64_t rows = a.Tq * a.Hq;
+    attn_delta_kernel<T, DP><<<grid_for(rows, 256 / (DP / 8), 8), 256, 0, st>>>(a, norms);
+  }
+  if (queries && gq > 0) attn_dq_kernel<T, DP><<<unsigned(gq), kAbThreads, AbCfg<DP>::kDqSmem, st>>>(maps, a, norms);
+  if (keys && gk > 0) attn_dkv_kernel<T, DP><<<unsigned(gk), kAbThreads, AbCfg<DP>::kDkvSmem, st>>>(maps, a, norms);
   return launch_status();
+}
+template <typename T>
+bl_status run_attn_backward(const AttnArgs& a, float* norms, cudaStream_t st) {
+  return a.D <= 64 ? launch_attn_bwd<T, 64>(a, norms, st) : launch_attn_bwd<T, 128>(a, norms, st);
 }
 
 // ---- paged attention ----------------------------------------------------------------
@@ -335,16 +362,16 @@ bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStre
 }
 
 size_t bl_attention_backward_workspace_size(const bl_attn_call* call) {
-  if (check_attn(call) != BL_OK || call->B == 0 || call->Tq == 0) return 0;
-  return align_up(size_t(call->Tq) * size_t(call->Hq) * 4);
+  if (check_attn(call) != BL_OK || call->B == 0) return 0;
+  return kAbNormBytes + align_up(size_t(call->Tq) * size_t(call->Hq) * 4);
 }
 
 bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
                                 void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, cudaStream_t stream) {
   bl_status st = check_attn(call);
   if (st != BL_OK) return st;
-  if (call->B == 0 || call->Tq == 0) return BL_OK;
-  if (!out || !lse || !dout || !dq || (call->Tk > 0 && (!dk || !dv))) return BL_ERR_INVALID_ARG;
+  if (call->B == 0 || (call->Tq == 0 && call->Tk == 0)) return BL_OK;
+  if ((call->Tq > 0 && (!out || !lse || !dout || !dq)) || (call->Tk > 0 && (!dk || !dv))) return BL_ERR_INVALID_ARG;
   if (!is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(dout, 16) || !is_aligned(dq, 16) ||
       !is_aligned(dk, 16) || !is_aligned(dv, 16))
     return BL_ERR_ALIGNMENT;
@@ -357,8 +384,10 @@ bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.delta = static_cast<float*>(ws);
-  return call->t == BL_T_F16 ? run_attn_backward<__half>(a, stream) : run_attn_backward<__nv_bfloat16>(a, stream);
+  float* norms = static_cast<float*>(ws);
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + kAbNormBytes);
+  return call->t == BL_T_F16 ? run_attn_backward<__half>(a, norms, stream)
+                             : run_attn_backward<__nv_bfloat16>(a, norms, stream);
 }
 
 size_t bl_paged_attention_workspace_size(int64_t B, int Hq, const bl_kv_pages* cache) {

@@ -1,0 +1,610 @@
+// Gradients of attention over packed sequences on the tensor cores.
+//
+// With the scores' log-sum-exp from the forward, per pair of a query and a key it sees
+//   P = 2^(c S - lse'),  dP = dO V^T,  dS = P (dP - delta),  delta = rowsum(dO O),
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
+// Two kernels, so that every sum has a fixed order and no atomics:
+//   attn_dkv_kernel   one CTA per 128 keys of a key head; walks the query blocks that see
+//     them, for each head of the group, with the transposed products (keys are the rows):
+//     S^T = K Q^T and dP^T = V dO^T into tensor memory, P^T and dS^T written back over
+//     them in the inputs' type, dV += P^T dO and dK += dS^T Q with the accumulators in
+//     tensor memory throughout: 4 matrix products a block;
+//   attn_dq_kernel    one CTA per 128 queries of a head; S, dP, dQ += dS K: 3 products.
+// Seven products for the formula's five: recomputing S and dP costs 40% more matrix work
+// than one kernel would, whose dQ would have to be summed across CTAs (atomics in float32,
+// whose order changes the result, or a turn-taking between CTAs).
+//
+// Eight softmax warps share a block, a thread half a row (64 columns): while they form P
+// the tensor core runs dK of the block before and dP of this one, while they form dS it
+// runs dV and the next S.  Bound: 512 cycles per product and block at D = 128, against
+// 1024 cycles of exponentials.
+//
+// float16: P is stored 2^14 times larger and dS 2^k times, k from the largest norms of
+// the rows of dO and V (|dP - delta| <= 2 |dO| |V|), so that neither leaves the normal
+// numbers; bfloat16 needs neither.
+#pragma once
+
+#include "attn_fwd.cuh"
+
+namespace bl {
+
+constexpr int kAbThreads = 320;                        // 8 softmax warps, MMA warp, TMA warp
+constexpr float kNoRow = 1e30f;                        // a log-sum-exp that makes every P zero
+
+struct alignas(64) AttnBwdMaps {
+  CUtensorMap q, k, v, dout;
+};
+
+template <int DP>
+struct AbCfg {
+  static constexpr int kTile = 128 * DP * 2;
+  static constexpr int kDkvSmem = 6 * kTile + 2048 + 1024;   // K, V, two stages of Q and dO, lse and delta of each
+  static constexpr int kDqSmem = 7 * kTile + 1024;           // Q, dO, three K, two V
+};
+
+template <typename T> __device__ __forceinline__ constexpr float p_scale_log2() { return std::is_same<T, __half>::value ? 14.f : 0.f; }
+
+// 2^k for dS (float16), from the largest squared row norms of dO and V.
+template <typename T> __device__ __forceinline__ float ds_scale(const float* norms) {
+  if (!std::is_same<T, __half>::value) return 1.f;
+  const float most = 2.02f * sqrtf(norms[0]) * sqrtf(norms[1]);
+  if (!(most > 0.f && most < INFINITY)) return 1.f;
+  return exp2f(fminf(fmaxf(floorf(log2f(32768.f / most)), -100.f), 100.f));
+}
+
+// Whether key row r is one that some query of its sequence may see.
+__device__ __forceinline__ bool seen_key(const AttnArgs& a, int r) {
+  if (r < a.cu_k[0] || r >= a.cu_k[a.B]) return false;
+  if (a.window == 0) return true;
+  int lo = 0, hi = a.B;                                 // cu_k[lo] <= r < cu_k[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.cu_k[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  const int j = r - a.cu_k[lo], off = (a.cu_k[lo + 1] - a.cu_k[lo]) - (a.cu_q[lo + 1] - a.cu_q[lo]);
+  return j < a.sinks || j > off - a.window;
+}
+
+// delta[h, row] = sum dO O, one group of DP / 8 lanes a row; for float16 also the largest
+// squared norms of the rows of dO and V (order does not matter to a maximum).
+template <typename T, int DP>
+__global__ void __launch_bounds__(256)
+attn_delta_kernel(const AttnArgs a, float* norms) {
+  constexpr int kLanes = DP / 8, kRows = 256 / kLanes;
+  const int u = threadIdx.x % kLanes, in = threadIdx.x / kLanes;
+  const bool on = 8 * u < a.D;
+  float top_o = 0.f, top_v = 0.f;
+  const int64_t rows = a.Tq * a.Hq, step = int64_t(gridDim.x) * kRows;
+  auto sum = [&](float x) {
+    for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < rows; r0 += step) {
+    const int64_t r = r0 + in;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (on && r < rows) {
+      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + r * a.D + 8 * u);
+      y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + r * a.D + 8 * u);
+    }
+    float d = 0.f, n = 0.f;
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = unpack2<T>(xs[i]), g = unpack2<T>(ys[i]);
+      d = fmaf(p.x, g.x, fmaf(p.y, g.y, d));
+      n = fmaf(g.x, g.x, fmaf(g.y, g.y, n));
+    }
+    d = sum(d);
+    if (std::is_same<T, __half>::value) {
+      n = sum(n);
+      const int64_t q = r / a.Hq;
+      if (q >= a.cu_q[0] && q < a.cu_q[a.B] && n < INFINITY) top_o = fmaxf(top_o, n);
+    }
+    if (u == 0 && r < rows) a.delta[(r % a.Hq) * a.Tq + r / a.Hq] = d;
+  }
+  if (std::is_same<T, __half>::value) {
+    const int64_t vr = a.Tk * a.Hkv;
+    for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < vr; r0 += step) {
+      const int64_t r = r0 + in;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (on && r < vr)
+        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + (r / a.Hkv) * a.ldv + (r % a.Hkv) * a.D + 8 * u);
+      float n = 0.f;
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack2<T>(xs[i]);
+        n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
+      }
+      n = sum(n);
+      if (n < INFINITY && n > top_v && seen_key(a, int(r / a.Hkv))) top_v = n;
+    }
+    top_o = warp_max(top_o);
+    top_v = warp_max(top_v);
+    if ((threadIdx.x & 31) == 0) {                      // squares: not negative, so their bits are ordered
+      atomicMax(reinterpret_cast<unsigned int*>(norms), __float_as_uint(top_o));
+      atomicMax(reinterpret_cast<unsigned int*>(norms + 1), __float_as_uint(top_v));
+    }
+  }
+}
+
+// D (128 x DP) += P B as mma_pv, with P's columns of rows 64.. at +64 (each half of the
+// softmax warps writes over the columns that it has read itself).
+template <typename T, int DP>
+__device__ __forceinline__ void mma_pv_halves(uint32_t d, uint32_t p, uint32_t b, bool acc) {
+  constexpr uint32_t idesc = umma_idesc_16<T>(128, DP, true);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    umma_f16_ts(d, p + uint32_t(k / 4) * 64u + uint32_t(k % 4) * 8u, umma_desc_mn_sw128(b + uint32_t(k) * 2048u), idesc,
+                acc || k > 0 ? 1u : 0u);
+}
+
+// A row of an accumulator, times f, to 16-bit memory (D elements); false if not finite.
+template <typename T, int DP>
+__device__ __forceinline__ bool store_row(uint32_t taddr, T* out, int D, float f, bool store, bool zero) {
+  bool good = true;
+#pragma unroll 1
+  for (int u = 0; u < DP / 32; ++u) {
+    uint32_t o[32];
+    __syncwarp();
+    tmem_ld32(taddr + u * 32, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      if (!store || u * 32 + e >= D) break;
+      uint32_t y[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const float f0 = zero ? 0.f : __uint_as_float(o[e + 2 * z]) * f, f1 = zero ? 0.f : __uint_as_float(o[e + 2 * z + 1]) * f;
+        if (!(fabsf(f0) + fabsf(f1) < INFINITY)) good = false;
+        y[z] = pack2<T>(f0, f1);
+      }
+      *reinterpret_cast<uint4*>(out + u * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  return good;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kAbThreads, 1)
+attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const float* norms) {
+  using C = AbCfg<DP>;
+  extern __shared__ unsigned char ab_smem[];
+  __shared__ uint64_t kv_full, full[2], empty[2], s_full, dp_full, p_ready, ds_ready, drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_err;
+  constexpr int kBoxes = DP / 64;
+  volatile int* err = &s_err;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // the work: key heads fastest, early key blocks (which most queries see) first
+  const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
+  const int j0 = rest / a.B * 128, group = a.Hq / a.Hkv;
+  Seq s;
+  if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) return;
+  const int off = s.nk - s.nq;
+  // query blocks that see these keys: rows from `first` to `last`
+  const int first = max(0, j0 - off) / 128;
+  const int last = a.window == 0 || j0 < a.sinks ? s.nq - 1 : min(s.nq - 1, j0 + 126 + a.window - off);
+  const int per = last < 0 || j0 - off > last ? 0 : last / 128 + 1 - first;   // blocks of one head
+  const int n = per * group;
+
+  const uint32_t base = (smem_u32(ab_smem) + 1023u) & ~1023u;
+  unsigned char* smem = ab_smem + (base - smem_u32(ab_smem));
+  float* rows = reinterpret_cast<float*>(smem + 6 * C::kTile);          // [2 stages][lse, delta][128]
+  if (tid == 0) {
+    s_err = 0;
+    mbar_init(&kv_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&dp_full, 1);
+    mbar_init(&p_ready, 8);
+    mbar_init(&ds_ready, 8);
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;                                         // S, dP, dV, dK: 128 columns each
+
+  if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(&kv_full, 2 * C::kTile);
+      tma_rows(smem, &maps.k, kBoxes, hk, s.k0 + j0, &kv_full);
+      tma_rows(smem + C::kTile, &maps.v, kBoxes, hk, s.k0 + j0, &kv_full);
+    }
+    int it = 0;
+    for (; it < n; ++it) {
+      const int st = it & 1, h = hk * group + it / per, i0 = (first + it % per) * 128;
+      if (it >= 2 && !mbar_wait(&empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+      if (__any_sync(0xffffffffu, *err)) break;
+      for (int u = lane; u < 128; u += 32) {
+        const bool in = i0 + u < s.nq;
+        const int64_t at = int64_t(h) * a.Tq + s.q0 + i0 + u;
+        const float l = in ? a.lse[at] : -INFINITY;
+        rows[st * 256 + u] = l == -INFINITY ? kNoRow : l * kLog2e - p_scale_log2<T>();
+        rows[st * 256 + 128 + u] = in ? a.delta[at] : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[st], 2 * C::kTile);
+        unsigned char* q = smem + (2 + 2 * st) * C::kTile;
+        tma_rows(q, &maps.q, kBoxes, h, s.q0 + i0, &full[st]);
+        tma_rows(q + C::kTile, &maps.dout, kBoxes, h, s.q0 + i0, &full[st]);
+      }
+    }
+    if (*err && n > 0) {                                                // leave no copy in flight behind
+      mbar_wait(&kv_full, 0u);
+      for (int i = max(0, it - 2); i < it; ++i) mbar_wait(&full[i & 1], uint32_t(i / 2) & 1u);
+    }
+  } else if (warp == 8) {
+    const uint32_t S = tmem, dP = tmem + 128, dV = tmem + 256, dK = tmem + 384;
+    auto q_at = [&](int it) { return base + uint32_t((2 + 2 * (it & 1)) * C::kTile); };
+    auto wait_q = [&](int it) {
+      if (!mbar_wait(&full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
+      tc_fence_after();
+      const int i0 = (first + it % per) * 128;
+      if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) {                      // rows of no query of the sequence
+        unsigned char* q = smem + (2 + 2 * (it & 1)) * C::kTile;
+        zero_rows(q, kBoxes, s.nq - i0, 128, lane);
+        zero_rows(q + C::kTile, kBoxes, s.nq - i0, 128, lane);
+      }
+    };
+    if (n > 0) {
+      if (!mbar_wait(&kv_full, 0u)) *err = 1;
+      wait_q(0);
+      if (lane == 0 && !*err) {
+        mma_qk<T, DP>(S, base, q_at(0));
+        umma_commit(&s_full);
+        mma_qk<T, DP>(dP, base + C::kTile, q_at(0) + C::kTile);
+        umma_commit(&dp_full);
+      }
+      __syncwarp();
+    }
+    for (int it = 0; it < n && !__any_sync(0xffffffffu, *err); ++it) {
+      const bool more = it + 1 < n;
+      if (!mbar_wait(&p_ready, uint32_t(it) & 1u)) *err = 1;
+      tc_fence_after();
+      if (lane == 0 && !*err) mma_pv_halves<T, DP>(dV, S, q_at(it) + C::kTile, it > 0);
+      if (more) {
+        wait_q(it + 1);
+        if (lane == 0 && !*err) {
+          mma_qk<T, DP>(S, base, q_at(it + 1));                         // in order behind the product that reads P
+          umma_commit(&s_full);
+        }
+      }
+      __syncwarp();
+      if (!mbar_wait(&ds_ready, uint32_t(it) & 1u)) *err = 1;
+      tc_fence_after();
+      if (lane == 0 && !*err) {
+        mma_pv_halves<T, DP>(dK, dP, q_at(it), it > 0);
+        umma_commit(&empty[it & 1]);
+        if (more) {
+          mma_qk<T, DP>(dP, base + C::kTile, q_at(it + 1) + C::kTile);
+          umma_commit(&dp_full);
+        }
+      }
+      __syncwarp();
+    }
+    if (lane == 0) umma_commit(&drain);
+    __syncwarp();
+  } else {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane, j = j0 + row;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t S = tmem + lanes + half * 64, dP = S + 128;
+    const float c = a.scale * kLog2e;
+    const float mult = ds_scale<T>(norms), f = mult * exp2f(-p_scale_log2<T>());
+    bool fine = true;
+    for (int it = 0; it < n; ++it) {
+      const int i0 = (first + it % per) * 128;
+      const float4* lse = reinterpret_cast<const float4*>(rows + (it & 1) * 256 + half * 64);
+      const float4* del = lse + 32;
+      fine = mbar_wait(&full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait(&s_full, uint32_t(it) & 1u) && !*err;
+      if (__any_sync(0xffffffffu, !fine)) {
+        *err = 1;
+        break;
+      }
+      tc_fence_after();
+      float p[64];
+      uint32_t w[32];
+      tmem_ld32(S, reinterpret_cast<uint32_t*>(p));
+      tmem_ld32(S + 32, reinterpret_cast<uint32_t*>(p) + 32);
+      tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const float4 l = lse[u];
+        p[4 * u] = exp2_approx(fmaf(p[4 * u], c, -l.x));
+        p[4 * u + 1] = exp2_approx(fmaf(p[4 * u + 1], c, -l.y));
+        p[4 * u + 2] = exp2_approx(fmaf(p[4 * u + 2], c, -l.z));
+        p[4 * u + 3] = exp2_approx(fmaf(p[4 * u + 3], c, -l.w));
+      }
+      // some key of the block is not seen by some query of the block
+      const bool masked = i0 + off < j0 + 127 || (a.window != 0 && i0 + 127 + off >= j0 + a.window && j0 + 128 > a.sinks);
+      if (masked) {
+        const int bot = j - off - i0 - half * 64;
+        const int top = a.window == 0 || j < a.sinks ? 128 : j + a.window - off - i0 - half * 64;
+#pragma unroll
+        for (int u = 0; u < 64; ++u)
+          if (u < bot || u >= top) p[u] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 32; ++u) w[u] = pack2<T>(p[2 * u], p[2 * u + 1]);
+      tmem_st32(S, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready);
+
+      fine = mbar_wait(&dp_full, uint32_t(it) & 1u) && !*err;
+      if (__any_sync(0xffffffffu, !fine)) {
+        *err = 1;
+        break;
+      }
+      tc_fence_after();
+      float d[64];
+      tmem_ld32(dP, reinterpret_cast<uint32_t*>(d));
+      tmem_ld32(dP + 32, reinterpret_cast<uint32_t*>(d) + 32);
+      tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const float4 e = del[u];
+        d[4 * u] = p[4 * u] * (d[4 * u] - e.x);
+        d[4 * u + 1] = p[4 * u + 1] * (d[4 * u + 1] - e.y);
+        d[4 * u + 2] = p[4 * u + 2] * (d[4 * u + 2] - e.z);
+        d[4 * u + 3] = p[4 * u + 3] * (d[4 * u + 3] - e.w);
+      }
+      if (masked) {                                                     // zero whatever V holds there
+#pragma unroll
+        for (int u = 0; u < 64; ++u)
+          if (p[u] == 0.f) d[u] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 32; ++u)
+        w[u] = std::is_same<T, __half>::value ? pack2<T>(d[2 * u] * f, d[2 * u + 1] * f) : pack2<T>(d[2 * u], d[2 * u + 1]);
+      tmem_st32(dP, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_ready);                            // (lse and delta of the stage have been read, too)
+    }
+  }
+
+  // every product done: warps 0..3 store dV, warps 4..7 dK
+  __syncthreads();
+  bool good = !*err;
+  if (warp == 8) {
+    if (!mbar_wait(&drain, 0u)) *err = 1;
+    __syncwarp();
+    if (*err && lane == 0) raise_status(kDevTimeout);
+  }
+  __syncthreads();
+  good = !*err;
+  tc_fence_after();
+  if (warp < 8 && good) {
+    const int row = (warp & 3) * 32 + lane, j = j0 + row;
+    const bool keys = warp >= 4;
+    const uint32_t acc = tmem + (uint32_t((warp & 3) * 32) << 16) + (keys ? 384 : 256);
+    const float f = keys ? a.scale / ds_scale<T>(norms) : exp2f(-p_scale_log2<T>());
+    T* out = static_cast<T*>(keys ? a.dk : a.dv) + (int64_t(s.k0 + j) * a.Hkv + hk) * a.D;
+    if (!store_row<T, DP>(acc, out, a.D, f, j < s.nk, n == 0) && j < s.nk) raise_status(kDevNonFinite);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kAbThreads, 1)
+attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const float* norms) {
+  using C = AbCfg<DP>;
+  extern __shared__ unsigned char ab_smem[];
+  __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_ready, drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_err;
+  constexpr int kBoxes = DP / 64;
+  volatile int* err = &s_err;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int nblk = (a.max_q + 127) / 128;
+  const int h = int(blockIdx.x % unsigned(a.Hq)), rest = int(blockIdx.x / unsigned(a.Hq));
+  const int i0 = (nblk - 1 - rest / a.B) * 128, hk = h / (a.Hq / a.Hkv);
+  Seq s;
+  if (!load_seq(a, rest % a.B, s, true) || i0 >= s.nq) return;
+  const int off = s.nk - s.nq;
+  const Blocks blocks = key_blocks(i0 + off, min(i0 + 128, s.nq) - 1 + off, a.window, a.sinks);
+  const int n = blocks.n;
+
+  const uint32_t base = (smem_u32(ab_smem) + 1023u) & ~1023u;
+  unsigned char* smem = ab_smem + (base - smem_u32(ab_smem));
+  if (tid == 0) {
+    s_err = 0;
+    mbar_init(&q_full, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+    }
+    mbar_init(&dp_full, 1);
+    mbar_init(&ds_ready, 8);
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;                                         // S0, S1, dP, dQ: 128 columns each
+
+  if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(&q_full, 2 * C::kTile);
+      tma_rows(smem, &maps.q, kBoxes, h, s.q0 + i0, &q_full);
+      tma_rows(smem + C::kTile, &maps.dout, kBoxes, h, s.q0 + i0, &q_full);
+      int it = 0;
+      for (; it < n; ++it) {
+        const int ks = it % 3, vs = it & 1, j0 = blocks.at(it);
+        if (it >= 3 && !mbar_wait(&k_empty[ks], uint32_t(it / 3 - 1) & 1u)) *err = 1;
+        if (it >= 2 && !mbar_wait(&v_empty[vs], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+        if (*err) break;
+        mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+        tma_rows(smem + (2 + ks) * C::kTile, &maps.k, kBoxes, hk, s.k0 + j0, &k_full[ks]);
+        mbar_arrive_expect_tx(&v_full[vs], C::kTile);
+        tma_rows(smem + (5 + vs) * C::kTile, &maps.v, kBoxes, hk, s.k0 + j0, &v_full[vs]);
+      }
+      if (*err) {                                                       // leave no copy in flight behind
+        mbar_wait(&q_full, 0u);
+        for (int i = max(0, it - 3); i < it; ++i) mbar_wait(&k_full[i % 3], uint32_t(i / 3) & 1u);
+        for (int i = max(0, it - 2); i < it; ++i) mbar_wait(&v_full[i & 1], uint32_t(i / 2) & 1u);
+      }
+    }
+  } else if (warp == 8) {
+    const uint32_t dP = tmem + 256, dQ = tmem + 384;
+    auto k_at = [&](int it) { return base + uint32_t((2 + it % 3) * C::kTile); };
+    auto issue_s = [&](int it) {
+      if (!mbar_wait(&k_full[it % 3], uint32_t(it / 3) & 1u)) *err = 1;
+      tc_fence_after();
+      zero_dead_keys(smem + (2 + it % 3) * C::kTile, kBoxes, blocks.at(it), s, a.window, a.sinks, a.Tk, lane);
+      if (lane == 0 && !*err) {
+        mma_qk<T, DP>(tmem + (it & 1) * 128, base, k_at(it));
+        umma_commit(&s_full[it & 1]);
+      }
+      __syncwarp();
+    };
+    auto issue_dp = [&](int it) {
+      if (!mbar_wait(&v_full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
+      tc_fence_after();
+      if (lane == 0 && !*err) {
+        mma_qk<T, DP>(dP, base + C::kTile, base + uint32_t((5 + (it & 1)) * C::kTile));
+        umma_commit(&dp_full);
+        umma_commit(&v_empty[it & 1]);
+      }
+      __syncwarp();
+    };
+    if (n > 0) {
+      if (!mbar_wait(&q_full, 0u)) *err = 1;
+      issue_s(0);
+      issue_dp(0);
+      if (n > 1) issue_s(1);
+    }
+    for (int it = 0; it < n && !__any_sync(0xffffffffu, *err); ++it) {
+      if (!mbar_wait(&ds_ready, uint32_t(it) & 1u)) *err = 1;
+      tc_fence_after();
+      if (it + 1 < n) issue_dp(it + 1);                                 // dP of this block has been read
+      if (lane == 0 && !*err) {
+        mma_pv_halves<T, DP>(dQ, tmem + (it & 1) * 128, k_at(it), it > 0);
+        umma_commit(&k_empty[it % 3]);
+      }
+      __syncwarp();
+      if (it + 2 < n) issue_s(it + 2);                                  // in order behind the product that reads dS
+    }
+    if (lane == 0) umma_commit(&drain);
+    __syncwarp();
+  } else {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane, i = i0 + row;
+    const int pos = i < s.nq ? i + off : -1, lo = a.window ? pos - a.window + 1 : 0;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t dP = tmem + lanes + 256 + half * 64;
+    const float c = a.scale * kLog2e;
+    float lse = kNoRow, delta = 0.f;
+    if (i < s.nq) {
+      const float l = a.lse[int64_t(h) * a.Tq + s.q0 + i];
+      lse = l == -INFINITY ? kNoRow : l * kLog2e;
+      delta = a.delta[int64_t(h) * a.Tq + s.q0 + i];
+    }
+    const float mult = ds_scale<T>(norms);
+    bool fine = true;
+    for (int it = 0; it < n; ++it) {
+      const int j0 = blocks.at(it);
+      const uint32_t S = tmem + lanes + (it & 1) * 128 + half * 64;
+      fine = mbar_wait(&s_full[it & 1], uint32_t(it / 2) & 1u) && !*err;
+      if (__any_sync(0xffffffffu, !fine)) {
+        *err = 1;
+        break;
+      }
+      tc_fence_after();
+      float p[64];
+      tmem_ld32(S, reinterpret_cast<uint32_t*>(p));
+      tmem_ld32(S + 32, reinterpret_cast<uint32_t*>(p) + 32);
+      tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 64; ++u) p[u] = exp2_approx(fmaf(p[u], c, -lse));
+      // a key of the block is not seen by some row of the tile
+      const bool masked = j0 + 127 > i0 + off ||
+                          (a.window != 0 && j0 <= min(i0 + 128, s.nq) - 1 + off - a.window && j0 + 128 > a.sinks);
+      if (masked) {
+        const int top = pos - j0 - half * 64, bot = lo - j0 - half * 64, lead = a.window ? a.sinks - j0 - half * 64 : 0;
+#pragma unroll
+        for (int u = 0; u < 64; ++u)
+          if (u > top || (u < bot && u >= lead)) p[u] = 0.f;
+      }
+      fine = mbar_wait(&dp_full, uint32_t(it) & 1u) && !*err;
+      if (__any_sync(0xffffffffu, !fine)) {
+        *err = 1;
+        break;
+      }
+      tc_fence_after();
+      float d[64];
+      uint32_t w[32];
+      tmem_ld32(dP, reinterpret_cast<uint32_t*>(d));
+      tmem_ld32(dP + 32, reinterpret_cast<uint32_t*>(d) + 32);
+      tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 64; ++u) d[u] = p[u] * (d[u] - delta);
+      if (masked) {                                                     // zero whatever V holds there
+#pragma unroll
+        for (int u = 0; u < 64; ++u)
+          if (p[u] == 0.f) d[u] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 32; ++u)
+        w[u] = std::is_same<T, __half>::value ? pack2<T>(d[2 * u] * mult, d[2 * u + 1] * mult) : pack2<T>(d[2 * u], d[2 * u + 1]);
+      tmem_st32(S, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_ready);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 8) {
+    if (!mbar_wait(&drain, 0u)) *err = 1;
+    __syncwarp();
+    if (*err && lane == 0) raise_status(kDevTimeout);
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp < 4 && !*err) {
+    const int row = warp * 32 + lane, i = i0 + row;
+    T* out = static_cast<T*>(a.dq) + (int64_t(s.q0 + i) * a.Hq + h) * a.D;
+    const uint32_t acc = tmem + (uint32_t(warp * 32) << 16) + 384;
+    if (!store_row<T, DP>(acc, out, a.D, a.scale / ds_scale<T>(norms), i < s.nq, n == 0) && i < s.nq) raise_status(kDevNonFinite);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace bl

@@ -221,7 +221,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
         umma_commit(&kv_empty[0]);
       }
     }
-    for (int j = 0; j < blocks.n && !*err; ++j) {
+    for (int j = 0; j < blocks.n && !__any_sync(0xffffffffu, *err); ++j) {
       const int j0 = blocks.at(j), nv = 2 * j + 1, nk = 2 * j + 2;
       const uint32_t v = wait_kv(nv);
       zero_dead_keys(ring + (nv % kAfRing) * C::kTile, kBoxes, j0, s, a.window, a.sinks, a.Tk, lane);

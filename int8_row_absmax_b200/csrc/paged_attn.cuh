@@ -213,28 +213,39 @@ paged_attn_kernel(const PaArgs a) {
       p.tiles = pa_tiles(p.len, a.window, a.sinks);
     } while (p.tiles.n == 0);
   };
-  // thread tid < 64: where row tid of p's tile is
-  auto locate = [&](const PaAt& p) -> int64_t {
+  // thread tid < 64 looks up where row tid of a tile is, in two steps so that the page
+  // number's way from memory overlaps a tile's work
+  int64_t pend_in = 0;                               // the row's place within its page's head, -1: not visible
+  int pend_page = 0;
+  auto look_up = [&](const PaAt& p) {
     const int t = p.t < p.tiles.lead ? p.t : p.t - p.tiles.lead + p.tiles.from;
     const int j = t * kPaTile + tid;
-    if (!(j < p.len && sees(p.len - 1, j, a.window, a.sinks))) return -1;
+    pend_in = -1;
+    if (!(j < p.len && sees(p.len - 1, j, a.window, a.sinks))) return;
     const uint32_t n = a.page == 1 ? uint32_t(j) : __umulhi(uint32_t(j), a.page_magic) >> a.page_shift;
-    const int64_t page = a.table[p.b * a.ldt + n];
-    if (page < 0 || page >= a.pages) {
+    pend_in = int64_t(p.item / a.chunks) * a.page + (j - int(n) * a.page);
+    pend_page = a.table[p.b * a.ldt + n];
+  };
+  auto place = [&]() -> int64_t {
+    if (pend_in < 0) return -1;
+    if (pend_page < 0 || pend_page >= a.pages) {
       range = true;
       return -1;
     }
-    return ((page * a.Hkv + p.item / a.chunks) * a.page + (j - int(n) * a.page)) * int64_t(a.D);
+    return (int64_t(pend_page) * a.Hkv * a.page + pend_in) * a.D;
   };
-  const int row_chunks = a.D >> 3;
+  constexpr int kRowChunks = DP / 8, kRowStep = kPaThreads / kRowChunks;
+  const int my_chunk = tid % kRowChunks, my_row = tid / kRowChunks;
   auto issue = [&](int stage, int buf) {
+    if (8 * my_chunk >= a.D) return;
     const uint32_t kd = base + stage * C::kStage, vd = kd + C::kTileBytes;
-    for (int i = tid; i < kPaTile * row_chunks; i += kPaThreads) {
-      const int r = i / row_chunks, c = i - r * row_chunks;
+#pragma unroll
+    for (int i = 0; i < kPaTile / kRowStep; ++i) {
+      const int r = my_row + i * kRowStep;
       const int64_t off = s_row[buf][r];
       const int n = off < 0 ? 0 : 16;
-      const int64_t e = off < 0 ? 0 : off + 8 * c;
-      const uint32_t d = pa_off<DP>(r, c);
+      const int64_t e = off < 0 ? 0 : off + 8 * my_chunk;
+      const uint32_t d = pa_off<DP>(r, my_chunk);
       cp_async16(kd + d, static_cast<const T*>(a.k) + e, n);
       cp_async16(vd + d, static_cast<const T*>(a.v) + e, n);
     }
@@ -249,14 +260,22 @@ paged_attn_kernel(const PaArgs a) {
   enter(cur, s_find[0], s_find[1], lo);
   load = cur;
   const int n = int(hi - lo);                        // tiles of this CTA
-  int located = 0;                                   // tiles whose rows are known
-  auto next_rows = [&]() {
-    if (located < n) {
-      if (tid < kPaTile) s_row[located & 1][tid] = locate(load);
-      ++located;
+  int looked = 0, located = 0;                       // tiles whose rows are asked for, and known
+  auto ask = [&]() {
+    if (looked < n) {
+      if (tid < kPaTile) look_up(load);
+      ++looked;
       advance(load);
     }
   };
+  auto next_rows = [&]() {                           // writes down the rows asked for last, asks for the next
+    if (located < n) {
+      if (tid < kPaTile) s_row[located & 1][tid] = place();
+      ++located;
+    }
+    ask();
+  };
+  ask();
   next_rows();
   for (int s = 0; s < kPaStages - 1; ++s) {
     next_rows();
@@ -359,9 +378,14 @@ paged_attn_kernel(const PaArgs a) {
       uint32_t f[4];
       ldsm4_t(f, vs_base + pa_off<DP>(r0 + (lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+      for (int u = 0; u < NT; ++u) {
+        // a fresh accumulator: the matrix unit truncates its sums, which would add up over the tiles
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < kTerms; ++k) mma16816<T>(o[i][u], f, pf[u][k][0], pf[u][k][1]);
+        for (int k = kTerms - 1; k >= 0; --k) mma16816<T>(y, f, pf[u][k][0], pf[u][k][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][u][e] += y[e];
+      }
     }
 
     const bool item_ends = cur.t + 1 == cur.tiles.n;

@@ -129,15 +129,12 @@ attn_delta_kernel(const AttnArgs a, float* norms) {
   }
 }
 
-// D (128 x DP) += P B as mma_pv, with P's columns of rows 64.. at +64 (each half of the
-// softmax warps writes over the columns that it has read itself).
+// D (128 x DP) += P B over 128 rows of B, with P's columns of rows 64.. at +64 (each half
+// of the softmax warps writes over the columns that it has read itself).
 template <typename T, int DP>
 __device__ __forceinline__ void mma_pv_halves(uint32_t d, uint32_t p, uint32_t b, bool acc) {
-  constexpr uint32_t idesc = umma_idesc_16<T>(128, DP, true);
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    umma_f16_ts(d, p + uint32_t(k / 4) * 64u + uint32_t(k % 4) * 8u, umma_desc_mn_sw128(b + uint32_t(k) * 2048u), idesc,
-                acc || k > 0 ? 1u : 0u);
+  mma_pv_half<T, DP>(d, p, b, acc);
+  mma_pv_half<T, DP>(d, p + 64, b + 8192, true);
 }
 
 // A row of an accumulator, times f, to 16-bit memory (D elements); false if not finite.
@@ -225,7 +222,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     int it = 0;
     for (; it < n; ++it) {
       const int st = it & 1, h = hk * group + it / per, i0 = (first + it % per) * 128;
-      if (it >= 2 && !mbar_wait(&empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+      if (it >= 2 && !mbar_wait_near(&empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
       if (__any_sync(0xffffffffu, *err)) break;
       for (int u = lane; u < 128; u += 32) {
         const bool in = i0 + u < s.nq;
@@ -243,14 +240,14 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       }
     }
     if (*err && n > 0) {                                                // leave no copy in flight behind
-      mbar_wait(&kv_full, 0u);
-      for (int i = max(0, it - 2); i < it; ++i) mbar_wait(&full[i & 1], uint32_t(i / 2) & 1u);
+      mbar_wait_near(&kv_full, 0u);
+      for (int i = max(0, it - 2); i < it; ++i) mbar_wait_near(&full[i & 1], uint32_t(i / 2) & 1u);
     }
   } else if (warp == 8) {
     const uint32_t S = tmem, dP = tmem + 128, dV = tmem + 256, dK = tmem + 384;
     auto q_at = [&](int it) { return base + uint32_t((2 + 2 * (it & 1)) * C::kTile); };
     auto wait_q = [&](int it) {
-      if (!mbar_wait(&full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
+      if (!mbar_wait_near(&full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
       tc_fence_after();
       const int i0 = (first + it % per) * 128;
       if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) {                      // rows of no query of the sequence
@@ -260,7 +257,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       }
     };
     if (n > 0) {
-      if (!mbar_wait(&kv_full, 0u)) *err = 1;
+      if (!mbar_wait_near(&kv_full, 0u)) *err = 1;
       wait_q(0);
       if (lane == 0 && !*err) {
         mma_qk<T, DP>(S, base, q_at(0));
@@ -272,7 +269,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     }
     for (int it = 0; it < n && !__any_sync(0xffffffffu, *err); ++it) {
       const bool more = it + 1 < n;
-      if (!mbar_wait(&p_ready, uint32_t(it) & 1u)) *err = 1;
+      if (!mbar_wait_near(&p_ready, uint32_t(it) & 1u)) *err = 1;
       tc_fence_after();
       if (lane == 0 && !*err) mma_pv_halves<T, DP>(dV, S, q_at(it) + C::kTile, it > 0);
       if (more) {
@@ -283,7 +280,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
         }
       }
       __syncwarp();
-      if (!mbar_wait(&ds_ready, uint32_t(it) & 1u)) *err = 1;
+      if (!mbar_wait_near(&ds_ready, uint32_t(it) & 1u)) *err = 1;
       tc_fence_after();
       if (lane == 0 && !*err) {
         mma_pv_halves<T, DP>(dK, dP, q_at(it), it > 0);
@@ -308,7 +305,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       const int i0 = (first + it % per) * 128;
       const float4* lse = reinterpret_cast<const float4*>(rows + (it & 1) * 256 + half * 64);
       const float4* del = lse + 32;
-      fine = mbar_wait(&full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait(&s_full, uint32_t(it) & 1u) && !*err;
+      fine = mbar_wait_near(&full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait_near(&s_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -344,7 +341,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready);
 
-      fine = mbar_wait(&dp_full, uint32_t(it) & 1u) && !*err;
+      fine = mbar_wait_near(&dp_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -382,7 +379,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   __syncthreads();
   bool good = !*err;
   if (warp == 8) {
-    if (!mbar_wait(&drain, 0u)) *err = 1;
+    if (!mbar_wait_near(&drain, 0u)) *err = 1;
     __syncwarp();
     if (*err && lane == 0) raise_status(kDevTimeout);
   }
@@ -462,8 +459,8 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       int it = 0;
       for (; it < n; ++it) {
         const int ks = it % 3, vs = it & 1, j0 = blocks.at(it);
-        if (it >= 3 && !mbar_wait(&k_empty[ks], uint32_t(it / 3 - 1) & 1u)) *err = 1;
-        if (it >= 2 && !mbar_wait(&v_empty[vs], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+        if (it >= 3 && !mbar_wait_near(&k_empty[ks], uint32_t(it / 3 - 1) & 1u)) *err = 1;
+        if (it >= 2 && !mbar_wait_near(&v_empty[vs], uint32_t(it / 2 - 1) & 1u)) *err = 1;
         if (*err) break;
         mbar_arrive_expect_tx(&k_full[ks], C::kTile);
         tma_rows(smem + (2 + ks) * C::kTile, &maps.k, kBoxes, hk, s.k0 + j0, &k_full[ks]);
@@ -471,16 +468,16 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
         tma_rows(smem + (5 + vs) * C::kTile, &maps.v, kBoxes, hk, s.k0 + j0, &v_full[vs]);
       }
       if (*err) {                                                       // leave no copy in flight behind
-        mbar_wait(&q_full, 0u);
-        for (int i = max(0, it - 3); i < it; ++i) mbar_wait(&k_full[i % 3], uint32_t(i / 3) & 1u);
-        for (int i = max(0, it - 2); i < it; ++i) mbar_wait(&v_full[i & 1], uint32_t(i / 2) & 1u);
+        mbar_wait_near(&q_full, 0u);
+        for (int i = max(0, it - 3); i < it; ++i) mbar_wait_near(&k_full[i % 3], uint32_t(i / 3) & 1u);
+        for (int i = max(0, it - 2); i < it; ++i) mbar_wait_near(&v_full[i & 1], uint32_t(i / 2) & 1u);
       }
     }
   } else if (warp == 8) {
     const uint32_t dP = tmem + 256, dQ = tmem + 384;
     auto k_at = [&](int it) { return base + uint32_t((2 + it % 3) * C::kTile); };
     auto issue_s = [&](int it) {
-      if (!mbar_wait(&k_full[it % 3], uint32_t(it / 3) & 1u)) *err = 1;
+      if (!mbar_wait_near(&k_full[it % 3], uint32_t(it / 3) & 1u)) *err = 1;
       tc_fence_after();
       zero_dead_keys(smem + (2 + it % 3) * C::kTile, kBoxes, blocks.at(it), s, a.window, a.sinks, a.Tk, lane);
       if (lane == 0 && !*err) {
@@ -490,7 +487,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       __syncwarp();
     };
     auto issue_dp = [&](int it) {
-      if (!mbar_wait(&v_full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
+      if (!mbar_wait_near(&v_full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
       tc_fence_after();
       if (lane == 0 && !*err) {
         mma_qk<T, DP>(dP, base + C::kTile, base + uint32_t((5 + (it & 1)) * C::kTile));
@@ -500,13 +497,13 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       __syncwarp();
     };
     if (n > 0) {
-      if (!mbar_wait(&q_full, 0u)) *err = 1;
+      if (!mbar_wait_near(&q_full, 0u)) *err = 1;
       issue_s(0);
       issue_dp(0);
       if (n > 1) issue_s(1);
     }
     for (int it = 0; it < n && !__any_sync(0xffffffffu, *err); ++it) {
-      if (!mbar_wait(&ds_ready, uint32_t(it) & 1u)) *err = 1;
+      if (!mbar_wait_near(&ds_ready, uint32_t(it) & 1u)) *err = 1;
       tc_fence_after();
       if (it + 1 < n) issue_dp(it + 1);                                 // dP of this block has been read
       if (lane == 0 && !*err) {
@@ -535,7 +532,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
     for (int it = 0; it < n; ++it) {
       const int j0 = blocks.at(it);
       const uint32_t S = tmem + lanes + (it & 1) * 128 + half * 64;
-      fine = mbar_wait(&s_full[it & 1], uint32_t(it / 2) & 1u) && !*err;
+      fine = mbar_wait_near(&s_full[it & 1], uint32_t(it / 2) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -556,7 +553,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
         for (int u = 0; u < 64; ++u)
           if (u > top || (u < bot && u >= lead)) p[u] = 0.f;
       }
-      fine = mbar_wait(&dp_full, uint32_t(it) & 1u) && !*err;
+      fine = mbar_wait_near(&dp_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -587,7 +584,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
 
   __syncthreads();
   if (warp == 8) {
-    if (!mbar_wait(&drain, 0u)) *err = 1;
+    if (!mbar_wait_near(&drain, 0u)) *err = 1;
     __syncwarp();
     if (*err && lane == 0) raise_status(kDevTimeout);
   }

@@ -50,20 +50,31 @@ template <typename T> __host__ __device__ constexpr uint32_t umma_idesc_16(int m
   const uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
   return (1u << 4) | (fmt << 7) | (fmt << 10) | (mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
+// The issuing warp stays whole: every lane computes the (uniform) operands and one elected
+// lane issues.  Behind a branch on the lane, the operands' way into the uniform registers
+// that the instruction reads took about 90 cycles per product.
 __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// A value that every lane of the warp holds, known to be uniform.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // MN-major operand: rows (contraction index) of 128 bytes with 128-byte swizzle, 8-row
 // groups 1024 bytes apart; the next 64 columns a box of 128 rows further.
 __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t addr) {
@@ -80,12 +91,12 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint32_t a, uint32_t b) {
     umma_f16(d, umma_desc_k_sw128(a + off), umma_desc_k_sw128(b + off), idesc, k > 0 ? 1u : 0u);
   }
 }
-// D (128 x DP) += P B over 128 rows of B: P in tensor memory, B MN-major in shared memory.
+// D (128 x DP) += P B over 64 rows of B: P in tensor memory, B MN-major in shared memory.
 template <typename T, int DP>
-__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_pv_half(uint32_t d, uint32_t p, uint32_t b, bool acc) {
   constexpr uint32_t idesc = umma_idesc_16<T>(128, DP, true);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
+  for (int k = 0; k < 4; ++k)
     umma_f16_ts(d, p + uint32_t(k) * 8u, umma_desc_mn_sw128(b + uint32_t(k) * 2048u), idesc, acc || k > 0 ? 1u : 0u);
 }
 
@@ -130,13 +141,13 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   using C = AfCfg<DP>;
   extern __shared__ unsigned char af_smem[];
-  __shared__ uint64_t q_full, kv_full[kAfRing], kv_empty[kAfRing], s_full[2], p_full[2], o_full[2], drain;
+  __shared__ uint64_t q_full, kv_full[kAfRing], kv_empty[kAfRing], s_full[2], p_full[2][2], o_full[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_err;
   constexpr int kBoxes = DP / 64;
   constexpr float kShift = std::is_same<T, __half>::value ? 7.f : 0.f;
   volatile int* err = &s_err;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   // the work: heads (or a pair of them) fastest, long row blocks first
   const int group = a.Hq / a.Hkv;
@@ -147,6 +158,10 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   const int i0 = (nblk - 1 - rest / a.B) * rows;
   Seq s;
   if (!load_seq(a, rest % a.B, s, false) || i0 >= s.nq) return;
+  s.q0 = uniform(s.q0);
+  s.nq = uniform(s.nq);
+  s.k0 = uniform(s.k0);
+  s.nk = uniform(s.nk);
   const int off = s.nk - s.nq;
   const int h0 = two ? 2 * unit : unit, hk = h0 / group;
   const int r1 = two ? i0 : i0 + 128;                  // first row of tile 1
@@ -168,7 +183,8 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[t][0], 4);
+      mbar_init(&p_full[t][1], 4);
       mbar_init(&o_full[t], 1);
     }
     fence_mbar_init();
@@ -180,7 +196,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;                        // S0, S1, O0, O1: 128 columns each
+  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                        // S0, S1, O0, O1: 128 columns each
   unsigned char* ring = smem + 2 * C::kTile;
 
   if (warp == 9) {
@@ -191,68 +207,72 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
       int n = 0;
       for (; n < 2 * blocks.n; ++n) {                  // K of block 0, V of block 0, K of block 1, ...
         const int st = n % kAfRing;
-        if (n >= kAfRing && !mbar_wait(&kv_empty[st], uint32_t(n / kAfRing - 1) & 1u)) *err = 1;
+        if (n >= kAfRing && !mbar_wait_near(&kv_empty[st], uint32_t(n / kAfRing - 1) & 1u)) *err = 1;
         if (*err) break;
         mbar_arrive_expect_tx(&kv_full[st], C::kTile);
         tma_rows(ring + st * C::kTile, (n & 1) ? &maps.v : &maps.k, kBoxes, hk, s.k0 + blocks.at(n >> 1), &kv_full[st]);
       }
       if (*err) {                                      // leave no copy in flight behind
-        mbar_wait(&q_full, 0u);
-        for (int i = max(0, n - kAfRing); i < n; ++i) mbar_wait(&kv_full[i % kAfRing], uint32_t(i / kAfRing) & 1u);
+        mbar_wait_near(&q_full, 0u);
+        for (int i = max(0, n - kAfRing); i < n; ++i) mbar_wait_near(&kv_full[i % kAfRing], uint32_t(i / kAfRing) & 1u);
       }
     }
   } else if (warp == 8) {
-    auto wait_kv = [&](int n) {
-      if (!mbar_wait(&kv_full[n % kAfRing], uint32_t(n / kAfRing) & 1u)) *err = 1;
+    bool good = true;                                    // the same in every lane
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (good && __any_sync(0xffffffffu, !mbar_wait_near(bar, uint32_t(parity) & 1u))) {
+        good = false;
+        *err = 1;
+      }
       tc_fence_after();
+    };
+    auto wait_kv = [&](int n) {
+      wait(&kv_full[n % kAfRing], n / kAfRing);
       return base + uint32_t((2 + n % kAfRing) * C::kTile);
     };
     int cnt[2] = {0, 0};
     if (blocks.n > 0) {
-      if (!mbar_wait(&q_full, 0u)) *err = 1;
+      wait(&q_full, 0);
       const uint32_t k = wait_kv(0);
-      if (lane == 0 && !*err) {
+      if (good) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (active(t ? r1 : i0, blocks.at(0))) {
             mma_qk<T, DP>(tmem + t * 128, base + t * C::kTile, k);
-            umma_commit(&s_full[t]);
+            umma_commit_warp(&s_full[t]);
           }
-        umma_commit(&kv_empty[0]);
+        umma_commit_warp(&kv_empty[0]);
       }
     }
-    for (int j = 0; j < blocks.n && !__any_sync(0xffffffffu, *err); ++j) {
+    for (int j = 0; j < blocks.n && good; ++j) {
       const int j0 = blocks.at(j), nv = 2 * j + 1, nk = 2 * j + 2;
       const uint32_t v = wait_kv(nv);
       zero_dead_keys(ring + (nv % kAfRing) * C::kTile, kBoxes, j0, s, a.window, a.sinks, a.Tk, lane);
       const bool more = j + 1 < blocks.n;
-      uint32_t k = 0;
+      const int j1 = more ? blocks.at(j + 1) : 0;
+      const uint32_t k = more ? wait_kv(nk) : 0;         // loaded long since: not on the way from P to the next S
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int r = t ? r1 : i0;
         if (active(r, j0)) {
-          if (!mbar_wait(&p_full[t], uint32_t(cnt[t]) & 1u)) *err = 1;
-          tc_fence_after();
-          if (lane == 0 && !*err) {
-            mma_pv<T, DP>(tmem + 256 + t * 128, tmem + t * 128, v, cnt[t] > 0);
-            umma_commit(&o_full[t]);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            wait(&p_full[t][part], cnt[t]);
+            if (good)
+              mma_pv_half<T, DP>(tmem + 256 + t * 128, tmem + t * 128 + part * 32, v + part * 8192, cnt[t] > 0 || part > 0);
           }
+          umma_commit_warp(&o_full[t]);
           ++cnt[t];
         }
-        if (more && t == 0) k = wait_kv(nk);
-        if (more && lane == 0 && !*err && active(r, blocks.at(j + 1))) {
+        if (more && good && active(r, j1)) {
           mma_qk<T, DP>(tmem + t * 128, base + t * C::kTile, k);   // in order behind the product that reads P
-          umma_commit(&s_full[t]);
+          umma_commit_warp(&s_full[t]);
         }
-        __syncwarp();
       }
-      if (lane == 0) {
-        umma_commit(&kv_empty[nv % kAfRing]);
-        if (more) umma_commit(&kv_empty[nk % kAfRing]);
-      }
+      umma_commit_warp(&kv_empty[nv % kAfRing]);
+      if (more) umma_commit_warp(&kv_empty[nk % kAfRing]);
     }
-    if (lane == 0) umma_commit(&drain);
-    __syncwarp();
+    umma_commit_warp(&drain);
   } else {
     const int t = warp >> 2, row = (warp & 3) * 32 + lane, r = t ? r1 : i0, i = r + row;
     const int h = two ? h0 + t : h0;
@@ -267,7 +287,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
     for (int j = 0; j < blocks.n && r < s.nq; ++j) {
       const int j0 = blocks.at(j);
       if (!active(r, j0)) continue;
-      fine = mbar_wait(&s_full[t], uint32_t(cnt) & 1u) && !*err;
+      fine = mbar_wait_near(&s_full[t], uint32_t(cnt) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -285,17 +305,21 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
         for (int u = 0; u < 128; ++u)
           if (u > top || (u < bot && u >= lead)) x[u] = -INFINITY;
       }
-      float mx = fmaxf(x[0], x[1]);
+      float top4[4] = {x[0], x[1], x[2], x[3]};          // four chains: one would be 64 dependent steps
 #pragma unroll
-      for (int u = 2; u < 128; u += 2) mx = fmaxf(fmaxf(x[u], x[u + 1]), mx);
-      mx *= c;
+      for (int u = 4; u < 124; u += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(x[u + 2 * e], x[u + 2 * e + 1]), top4[e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top4[e] = fmaxf(x[124 + e], top4[e]);
+      const float mx = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;
       if (cnt == 0) {
         m = fmaxf(mx, kLow);
       } else if (__any_sync(0xffffffffu, mx > m + kAfLazy)) {
         const float up = fmaxf(mx, m), f = exp2_approx(m - up);
         m = up;
         l *= f;
-        fine = mbar_wait(&o_full[t], uint32_t(cnt - 1) & 1u);
+        fine = mbar_wait_near(&o_full[t], uint32_t(cnt - 1) & 1u);
         if (__any_sync(0xffffffffu, !fine)) {
           *err = 1;
           break;
@@ -312,24 +336,28 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
         }
       }
       const float sub = kShift - m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int u = 0; u < 128; u += 2) {
-        const float e0 = exp2_approx(fmaf(x[u], c, sub)), e1 = exp2_approx(fmaf(x[u + 1], c, sub));
-        sum[(u >> 1) & 3] += e0 + e1;
-        w[u >> 1] = pack2<T>(e0, e1);
+      for (int part = 0; part < 2; ++part) {             // the tensor core starts on the first 64 keys meanwhile
+#pragma unroll
+        for (int u = part * 64; u < part * 64 + 64; u += 2) {
+          const float2 y = fma2(make_float2(x[u], x[u + 1]), make_float2(c, c), make_float2(sub, sub));
+          const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          sum[(u >> 1) & 1] = add2(sum[(u >> 1) & 1], e);
+          w[u >> 1] = pack2<T>(e.x, e.y);
+        }
+        tmem_st32(st + part * 32, w + part * 32);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][part]);
       }
-      tmem_st32(st, w);
-      tmem_st32(st + 32, w + 32);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
       ++cnt;
     }
     if (fine && cnt > 0) {
-      fine = mbar_wait(&o_full[t], uint32_t(cnt - 1) & 1u) && !*err;
+      fine = mbar_wait_near(&o_full[t], uint32_t(cnt - 1) & 1u) && !*err;
       if (!fine) *err = 1;
       tc_fence_after();
     }
@@ -370,7 +398,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
 
   __syncthreads();
   if (warp == 8) {
-    const bool drained = mbar_wait(&drain, 0u);
+    const bool drained = mbar_wait_near(&drain, 0u);
     if ((!drained || *err) && lane == 0) raise_status(kDevTimeout);
     __syncwarp();
     tc_fence_after();

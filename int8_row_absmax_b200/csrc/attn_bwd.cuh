@@ -173,13 +173,17 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   __shared__ int s_err;
   constexpr int kBoxes = DP / 64;
   volatile int* err = &s_err;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   // the work: key heads fastest, early key blocks (which most queries see) first
   const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
   const int j0 = rest / a.B * 128, group = a.Hq / a.Hkv;
   Seq s;
   if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) return;
+  s.q0 = uniform(s.q0);
+  s.nq = uniform(s.nq);
+  s.k0 = uniform(s.k0);
+  s.nk = uniform(s.nk);
   const int off = s.nk - s.nq;
   // query blocks that see these keys: rows from `first` to `last`
   const int first = max(0, j0 - off) / 128;
@@ -211,7 +215,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;                                         // S, dP, dV, dK: 128 columns each
+  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                                         // S, dP, dV, dK: 128 columns each
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
@@ -244,11 +248,18 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       for (int i = max(0, it - 2); i < it; ++i) mbar_wait_near(&full[i & 1], uint32_t(i / 2) & 1u);
     }
   } else if (warp == 8) {
+    bool good = true;                                                   // the same in every lane
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (good && __any_sync(0xffffffffu, !mbar_wait_near(bar, uint32_t(parity) & 1u))) {
+        good = false;
+        *err = 1;
+      }
+      tc_fence_after();
+    };
     const uint32_t S = tmem, dP = tmem + 128, dV = tmem + 256, dK = tmem + 384;
     auto q_at = [&](int it) { return base + uint32_t((2 + 2 * (it & 1)) * C::kTile); };
     auto wait_q = [&](int it) {
-      if (!mbar_wait_near(&full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
-      tc_fence_after();
+      wait(&full[it & 1], it / 2);
       const int i0 = (first + it % per) * 128;
       if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) {                      // rows of no query of the sequence
         unsigned char* q = smem + (2 + 2 * (it & 1)) * C::kTile;
@@ -257,43 +268,37 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       }
     };
     if (n > 0) {
-      if (!mbar_wait_near(&kv_full, 0u)) *err = 1;
+      wait(&kv_full, 0);
       wait_q(0);
-      if (lane == 0 && !*err) {
+      if (good) {
         mma_qk<T, DP>(S, base, q_at(0));
-        umma_commit(&s_full);
+        umma_commit_warp(&s_full);
         mma_qk<T, DP>(dP, base + C::kTile, q_at(0) + C::kTile);
-        umma_commit(&dp_full);
+        umma_commit_warp(&dp_full);
       }
-      __syncwarp();
     }
-    for (int it = 0; it < n && !__any_sync(0xffffffffu, *err); ++it) {
+    for (int it = 0; it < n && good; ++it) {
       const bool more = it + 1 < n;
-      if (!mbar_wait_near(&p_ready, uint32_t(it) & 1u)) *err = 1;
-      tc_fence_after();
-      if (lane == 0 && !*err) mma_pv_halves<T, DP>(dV, S, q_at(it) + C::kTile, it > 0);
-      if (more) {
-        wait_q(it + 1);
-        if (lane == 0 && !*err) {
+      if (more) wait_q(it + 1);                                         // loaded long since
+      wait(&p_ready, it);
+      if (good) {
+        mma_pv_halves<T, DP>(dV, S, q_at(it) + C::kTile, it > 0);
+        if (more) {
           mma_qk<T, DP>(S, base, q_at(it + 1));                         // in order behind the product that reads P
-          umma_commit(&s_full);
+          umma_commit_warp(&s_full);
         }
       }
-      __syncwarp();
-      if (!mbar_wait_near(&ds_ready, uint32_t(it) & 1u)) *err = 1;
-      tc_fence_after();
-      if (lane == 0 && !*err) {
+      wait(&ds_ready, it);
+      if (good) {
         mma_pv_halves<T, DP>(dK, dP, q_at(it), it > 0);
-        umma_commit(&empty[it & 1]);
+        umma_commit_warp(&empty[it & 1]);
         if (more) {
           mma_qk<T, DP>(dP, base + C::kTile, q_at(it + 1) + C::kTile);
-          umma_commit(&dp_full);
+          umma_commit_warp(&dp_full);
         }
       }
-      __syncwarp();
     }
-    if (lane == 0) umma_commit(&drain);
-    __syncwarp();
+    umma_commit_warp(&drain);
   } else {
     const int half = warp >> 2, row = (warp & 3) * 32 + lane, j = j0 + row;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -412,13 +417,17 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
   __shared__ int s_err;
   constexpr int kBoxes = DP / 64;
   volatile int* err = &s_err;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   const int nblk = (a.max_q + 127) / 128;
   const int h = int(blockIdx.x % unsigned(a.Hq)), rest = int(blockIdx.x / unsigned(a.Hq));
   const int i0 = (nblk - 1 - rest / a.B) * 128, hk = h / (a.Hq / a.Hkv);
   Seq s;
   if (!load_seq(a, rest % a.B, s, true) || i0 >= s.nq) return;
+  s.q0 = uniform(s.q0);
+  s.nq = uniform(s.nq);
+  s.k0 = uniform(s.k0);
+  s.nk = uniform(s.nk);
   const int off = s.nk - s.nq;
   const Blocks blocks = key_blocks(i0 + off, min(i0 + 128, s.nq) - 1 + off, a.window, a.sinks);
   const int n = blocks.n;
@@ -449,7 +458,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;                                         // S0, S1, dP, dQ: 128 columns each
+  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                                         // S0, S1, dP, dQ: 128 columns each
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
@@ -474,47 +483,56 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       }
     }
   } else if (warp == 8) {
+    bool good = true;                                                   // the same in every lane
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (good && __any_sync(0xffffffffu, !mbar_wait_near(bar, uint32_t(parity) & 1u))) {
+        good = false;
+        *err = 1;
+      }
+      tc_fence_after();
+    };
     const uint32_t dP = tmem + 256, dQ = tmem + 384;
     auto k_at = [&](int it) { return base + uint32_t((2 + it % 3) * C::kTile); };
-    auto issue_s = [&](int it) {
-      if (!mbar_wait_near(&k_full[it % 3], uint32_t(it / 3) & 1u)) *err = 1;
-      tc_fence_after();
+    auto wait_k = [&](int it) {
+      wait(&k_full[it % 3], it / 3);
       zero_dead_keys(smem + (2 + it % 3) * C::kTile, kBoxes, blocks.at(it), s, a.window, a.sinks, a.Tk, lane);
-      if (lane == 0 && !*err) {
-        mma_qk<T, DP>(tmem + (it & 1) * 128, base, k_at(it));
-        umma_commit(&s_full[it & 1]);
-      }
-      __syncwarp();
+    };
+    auto issue_s = [&](int it) {
+      if (!good) return;
+      mma_qk<T, DP>(tmem + (it & 1) * 128, base, k_at(it));
+      umma_commit_warp(&s_full[it & 1]);
     };
     auto issue_dp = [&](int it) {
-      if (!mbar_wait_near(&v_full[it & 1], uint32_t(it / 2) & 1u)) *err = 1;
-      tc_fence_after();
-      if (lane == 0 && !*err) {
-        mma_qk<T, DP>(dP, base + C::kTile, base + uint32_t((5 + (it & 1)) * C::kTile));
-        umma_commit(&dp_full);
-        umma_commit(&v_empty[it & 1]);
-      }
-      __syncwarp();
+      if (!good) return;
+      mma_qk<T, DP>(dP, base + C::kTile, base + uint32_t((5 + (it & 1)) * C::kTile));
+      umma_commit_warp(&dp_full);
+      umma_commit_warp(&v_empty[it & 1]);
     };
     if (n > 0) {
-      if (!mbar_wait_near(&q_full, 0u)) *err = 1;
+      wait(&q_full, 0);
+      wait_k(0);
       issue_s(0);
+      wait(&v_full[0], 0);
       issue_dp(0);
-      if (n > 1) issue_s(1);
-    }
-    for (int it = 0; it < n && !__any_sync(0xffffffffu, *err); ++it) {
-      if (!mbar_wait_near(&ds_ready, uint32_t(it) & 1u)) *err = 1;
-      tc_fence_after();
-      if (it + 1 < n) issue_dp(it + 1);                                 // dP of this block has been read
-      if (lane == 0 && !*err) {
-        mma_pv_halves<T, DP>(dQ, tmem + (it & 1) * 128, k_at(it), it > 0);
-        umma_commit(&k_empty[it % 3]);
+      if (n > 1) {
+        wait_k(1);
+        issue_s(1);
       }
-      __syncwarp();
-      if (it + 2 < n) issue_s(it + 2);                                  // in order behind the product that reads dS
     }
-    if (lane == 0) umma_commit(&drain);
-    __syncwarp();
+    for (int it = 0; it < n && good; ++it) {
+      if (it + 1 < n) wait(&v_full[(it + 1) & 1], (it + 1) / 2);        // loaded long since
+      wait(&ds_ready, it);
+      if (it + 1 < n) issue_dp(it + 1);                                 // dP of this block has been read
+      if (good) {
+        mma_pv_halves<T, DP>(dQ, tmem + (it & 1) * 128, k_at(it), it > 0);
+        umma_commit_warp(&k_empty[it % 3]);
+      }
+      if (it + 2 < n) {
+        wait_k(it + 2);
+        issue_s(it + 2);                                                // in order behind the product that reads dS
+      }
+    }
+    umma_commit_warp(&drain);
   } else {
     const int half = warp >> 2, row = (warp & 3) * 32 + lane, i = i0 + row;
     const int pos = i < s.nq ? i + off : -1, lo = a.window ? pos - a.window + 1 : 0;

@@ -133,8 +133,8 @@ attn_delta_kernel(const AttnArgs a, float* norms) {
 // of the softmax warps writes over the columns that it has read itself).
 template <typename T, int DP>
 __device__ __forceinline__ void mma_pv_halves(uint32_t d, uint32_t p, uint32_t b, bool acc) {
-  mma_pv_half<T, DP>(d, p, b, acc);
-  mma_pv_half<T, DP>(d, p + 64, b + 8192, true);
+  mma_pv_part<T, DP, 64>(d, p, b, acc);
+  mma_pv_part<T, DP, 64>(d, p + 64, b + 8192, true);
 }
 
 // A row of an accumulator, times f, to 16-bit memory (D elements); false if not finite.
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const float* norms) {
   using C = AbCfg<DP>;
   extern __shared__ unsigned char ab_smem[];
-  __shared__ uint64_t kv_full, full[2], empty[2], s_full, dp_full, p_ready, ds_ready, drain;
+  __shared__ uint64_t kv_full, q_full[2], q_empty[2], g_full[2], g_empty[2], s_full, dp_full, p_ready, ds_ready, drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_err;
   constexpr int kBoxes = DP / 64;
@@ -198,8 +198,10 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     s_err = 0;
     mbar_init(&kv_full, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&g_full[i], 1);
+      mbar_init(&g_empty[i], 1);
     }
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
@@ -223,29 +225,49 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       tma_rows(smem, &maps.k, kBoxes, hk, s.k0 + j0, &kv_full);
       tma_rows(smem + C::kTile, &maps.v, kBoxes, hk, s.k0 + j0, &kv_full);
     }
+    // a block's lse and delta are asked for while the block before waits for its stage
+    float l[4], e[4];
+    auto ask = [&](int it) {
+      const int h = hk * group + it / per, i0 = (first + it % per) * 128;
+      const int64_t at = int64_t(h) * a.Tq + s.q0 + i0 + lane;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = i0 + lane + 32 * u < s.nq;
+        l[u] = in ? a.lse[at + 32 * u] : -INFINITY;
+        e[u] = in ? a.delta[at + 32 * u] : 0.f;
+      }
+    };
+    if (n > 0) ask(0);
     int it = 0;
     for (; it < n; ++it) {
       const int st = it & 1, h = hk * group + it / per, i0 = (first + it % per) * 128;
-      if (it >= 2 && !mbar_wait_near(&empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+      unsigned char* q = smem + (2 + 2 * st) * C::kTile;
+      // dO's place is free before Q's: after dV, not after dK of two blocks ago
+      if (it >= 2 && !mbar_wait_near(&g_empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
       if (__any_sync(0xffffffffu, *err)) break;
-      for (int u = lane; u < 128; u += 32) {
-        const bool in = i0 + u < s.nq;
-        const int64_t at = int64_t(h) * a.Tq + s.q0 + i0 + u;
-        const float l = in ? a.lse[at] : -INFINITY;
-        rows[st * 256 + u] = l == -INFINITY ? kNoRow : l * kLog2e - p_scale_log2<T>();
-        rows[st * 256 + 128 + u] = in ? a.delta[at] : 0.f;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&g_full[st], C::kTile);
+        tma_rows(q + C::kTile, &maps.dout, kBoxes, h, s.q0 + i0, &g_full[st]);
+      }
+      if (it >= 2 && !mbar_wait_near(&q_empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        rows[st * 256 + lane + 32 * u] = l[u] == -INFINITY ? kNoRow : fmaf(l[u], kLog2e, -p_scale_log2<T>());
+        rows[st * 256 + 128 + lane + 32 * u] = e[u];
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_expect_tx(&full[st], 2 * C::kTile);
-        unsigned char* q = smem + (2 + 2 * st) * C::kTile;
-        tma_rows(q, &maps.q, kBoxes, h, s.q0 + i0, &full[st]);
-        tma_rows(q + C::kTile, &maps.dout, kBoxes, h, s.q0 + i0, &full[st]);
+        mbar_arrive_expect_tx(&q_full[st], C::kTile);
+        tma_rows(q, &maps.q, kBoxes, h, s.q0 + i0, &q_full[st]);
       }
+      if (it + 1 < n) ask(it + 1);
     }
     if (*err && n > 0) {                                                // leave no copy in flight behind
       mbar_wait_near(&kv_full, 0u);
-      for (int i = max(0, it - 2); i < it; ++i) mbar_wait_near(&full[i & 1], uint32_t(i / 2) & 1u);
+      for (int i = max(0, it - 2); i < it; ++i) {
+        mbar_wait_near(&q_full[i & 1], uint32_t(i / 2) & 1u);
+        mbar_wait_near(&g_full[i & 1], uint32_t(i / 2) & 1u);
+      }
     }
   } else if (warp == 8) {
     bool good = true;                                                   // the same in every lane
@@ -258,14 +280,18 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     };
     const uint32_t S = tmem, dP = tmem + 128, dV = tmem + 256, dK = tmem + 384;
     auto q_at = [&](int it) { return base + uint32_t((2 + 2 * (it & 1)) * C::kTile); };
-    auto wait_q = [&](int it) {
-      wait(&full[it & 1], it / 2);
+    // rows of no query of the sequence must not meet P's and dS's zeros
+    auto trim = [&](unsigned char* tile, int it) {
       const int i0 = (first + it % per) * 128;
-      if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) {                      // rows of no query of the sequence
-        unsigned char* q = smem + (2 + 2 * (it & 1)) * C::kTile;
-        zero_rows(q, kBoxes, s.nq - i0, 128, lane);
-        zero_rows(q + C::kTile, kBoxes, s.nq - i0, 128, lane);
-      }
+      if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) zero_rows(tile, kBoxes, s.nq - i0, 128, lane);
+    };
+    auto wait_q = [&](int it) {
+      wait(&q_full[it & 1], it / 2);
+      trim(smem + (2 + 2 * (it & 1)) * C::kTile, it);
+    };
+    auto wait_g = [&](int it) {
+      wait(&g_full[it & 1], it / 2);
+      trim(smem + (3 + 2 * (it & 1)) * C::kTile, it);
     };
     if (n > 0) {
       wait(&kv_full, 0);
@@ -273,17 +299,23 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       if (good) {
         mma_qk<T, DP>(S, base, q_at(0));
         umma_commit_warp(&s_full);
+      }
+      wait_g(0);
+      if (good) {
         mma_qk<T, DP>(dP, base + C::kTile, q_at(0) + C::kTile);
         umma_commit_warp(&dp_full);
       }
     }
     for (int it = 0; it < n && good; ++it) {
       const bool more = it + 1 < n;
-      if (more) wait_q(it + 1);                                         // loaded long since
       wait(&p_ready, it);
       if (good) {
         mma_pv_halves<T, DP>(dV, S, q_at(it) + C::kTile, it > 0);
-        if (more) {
+        umma_commit_warp(&g_empty[it & 1]);
+      }
+      if (more) {
+        wait_q(it + 1);
+        if (good) {
           mma_qk<T, DP>(S, base, q_at(it + 1));                         // in order behind the product that reads P
           umma_commit_warp(&s_full);
         }
@@ -291,8 +323,11 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       wait(&ds_ready, it);
       if (good) {
         mma_pv_halves<T, DP>(dK, dP, q_at(it), it > 0);
-        umma_commit_warp(&empty[it & 1]);
-        if (more) {
+        umma_commit_warp(&q_empty[it & 1]);
+      }
+      if (more) {
+        wait_g(it + 1);
+        if (good) {
           mma_qk<T, DP>(dP, base + C::kTile, q_at(it + 1) + C::kTile);
           umma_commit_warp(&dp_full);
         }
@@ -310,7 +345,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       const int i0 = (first + it % per) * 128;
       const float4* lse = reinterpret_cast<const float4*>(rows + (it & 1) * 256 + half * 64);
       const float4* del = lse + 32;
-      fine = mbar_wait_near(&full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait_near(&s_full, uint32_t(it) & 1u) && !*err;
+      fine = mbar_wait_near(&q_full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait_near(&s_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;

@@ -27,6 +27,7 @@ namespace bl {
 
 constexpr int kAfThreads = 320;                        // 2 x 4 softmax warps, MMA warp, TMA warp
 constexpr int kAfRing = 4;                             // K and V tiles in flight
+constexpr int kAfParts = 2;                            // parts in which a row of P is handed over
 constexpr float kAfLazy = 8.f;                         // log2 of the growth that is let pass
 constexpr float kLow = -1e30f;                         // a row maximum before anything is seen
 
@@ -91,12 +92,12 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint32_t a, uint32_t b) {
     umma_f16(d, umma_desc_k_sw128(a + off), umma_desc_k_sw128(b + off), idesc, k > 0 ? 1u : 0u);
   }
 }
-// D (128 x DP) += P B over 64 rows of B: P in tensor memory, B MN-major in shared memory.
-template <typename T, int DP>
-__device__ __forceinline__ void mma_pv_half(uint32_t d, uint32_t p, uint32_t b, bool acc) {
+// D (128 x DP) += P B over kRows rows of B: P in tensor memory, B MN-major in shared memory.
+template <typename T, int DP, int kRows>
+__device__ __forceinline__ void mma_pv_part(uint32_t d, uint32_t p, uint32_t b, bool acc) {
   constexpr uint32_t idesc = umma_idesc_16<T>(128, DP, true);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < kRows / 16; ++k)
     umma_f16_ts(d, p + uint32_t(k) * 8u, umma_desc_mn_sw128(b + uint32_t(k) * 2048u), idesc, acc || k > 0 ? 1u : 0u);
 }
 
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   using C = AfCfg<DP>;
   extern __shared__ unsigned char af_smem[];
-  __shared__ uint64_t q_full, kv_full[kAfRing], kv_empty[kAfRing], s_full[2], p_full[2][2], o_full[2], drain;
+  __shared__ uint64_t q_full, kv_full[kAfRing], kv_empty[kAfRing], s_full[2], p_full[2][kAfParts], o_full[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_err;
   constexpr int kBoxes = DP / 64;
@@ -183,8 +184,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t][0], 4);
-      mbar_init(&p_full[t][1], 4);
+      for (int i = 0; i < kAfParts; ++i) mbar_init(&p_full[t][i], 4);
       mbar_init(&o_full[t], 1);
     }
     fence_mbar_init();
@@ -256,10 +256,11 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
         const int r = t ? r1 : i0;
         if (active(r, j0)) {
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
+          for (int part = 0; part < kAfParts; ++part) {
             wait(&p_full[t][part], cnt[t]);
             if (good)
-              mma_pv_half<T, DP>(tmem + 256 + t * 128, tmem + t * 128 + part * 32, v + part * 8192, cnt[t] > 0 || part > 0);
+              mma_pv_part<T, DP, 128 / kAfParts>(tmem + 256 + t * 128, tmem + t * 128 + part * (64 / kAfParts),
+                                                 v + part * (16384 / kAfParts), cnt[t] > 0 || part > 0);
           }
           umma_commit_warp(&o_full[t]);
           ++cnt[t];
@@ -338,9 +339,10 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
       const float sub = kShift - m;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {             // the tensor core starts on the first 64 keys meanwhile
+      for (int part = 0; part < kAfParts; ++part) {      // the tensor core starts on the first keys meanwhile
+        constexpr int kKeys = 128 / kAfParts;
 #pragma unroll
-        for (int u = part * 64; u < part * 64 + 64; u += 2) {
+        for (int u = part * kKeys; u < (part + 1) * kKeys; u += 2) {
           const float2 y = fma2(make_float2(x[u], x[u + 1]), make_float2(c, c), make_float2(sub, sub));
           const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
           sum[(u >> 1) & 1] = add2(sum[(u >> 1) & 1], e);

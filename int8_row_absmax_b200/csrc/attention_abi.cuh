@@ -3,6 +3,8 @@
 // helpers it uses.
 #pragma once
 
+#include <atomic>
+
 #include "attn.cuh"
 #include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
@@ -18,6 +20,19 @@ constexpr int64_t kAttnMaxRows = int64_t(1) << 30;      // sums of two positions
 bool half_type(bl_dtype t) { return t == BL_T_F16 || t == BL_T_BF16; }
 bool any_type(bl_dtype t) { return t == BL_T_F32 || half_type(t); }
 bool int32_max(int64_t v) { return v < (int64_t(1) << 31); }
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device and kernel (the call
+// costs about a microsecond, as much as the rest of a small call's host work).
+template <typename K>
+bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
 
 // ---- norms and rotation ----------------------------------------------------------
 bl_status check_rows(const bl_qkv_rows* r, bool values) {
@@ -168,8 +183,8 @@ bl_status launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
     maps.k = maps.v = maps.q;                            // no keys: never loaded from
   }
   constexpr int smem = AfCfg<DP>::kSmem;
-  if (cudaFuncSetAttribute(attn_fwd_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return BL_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(attn_fwd_kernel<T, DP>, smem, done)) return BL_ERR_CUDA;
   const bool two = (a.Hq / a.Hkv) % 2 == 0;
   const int64_t grid = int64_t(two ? a.Hq / 2 : a.Hq) * a.B * ceil_div(a.max_q, two ? 128 : 256);
   if (!int32_max(grid)) return BL_ERR_UNSUPPORTED;
@@ -197,10 +212,9 @@ bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
     return BL_ERR_CUDA;
   if (!queries) maps.q = maps.dout = maps.k;             // never loaded from
   if (!keys) maps.k = maps.v = maps.q;
-  if (cudaFuncSetAttribute(attn_dkv_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, AbCfg<DP>::kDkvSmem) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(attn_dq_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, AbCfg<DP>::kDqSmem) !=
-          cudaSuccess)
+  static std::atomic<uint64_t> done_kv{0}, done_q{0};
+  if (!allow_smem(attn_dkv_kernel<T, DP>, AbCfg<DP>::kDkvSmem, done_kv) ||
+      !allow_smem(attn_dq_kernel<T, DP>, AbCfg<DP>::kDqSmem, done_q))
     return BL_ERR_CUDA;
   const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
   if (!int32_max(gq) || !int32_max(gk)) return BL_ERR_UNSUPPORTED;
@@ -221,17 +235,16 @@ bl_status run_attn_backward(const AttnArgs& a, float* norms, cudaStream_t st) {
 // ---- paged attention ----------------------------------------------------------------
 int paged_pad(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 int paged_nt(int Hq, int Hkv) { return Hq / Hkv <= 8 ? 1 : 2; }
-constexpr size_t kPaCountBytes = 2048;
-static_assert(kPaCtas * 4 <= kPaCountBytes, "counters fit");
+constexpr size_t kPaCountBytes = 4096;
+static_assert(kPaMaxCtas * 4 <= kPaCountBytes, "counters fit");
 
 template <typename T, int DP, int NT, typename OutT>
 bl_status launch_paged(const PaArgs& a, cudaStream_t st) {
   constexpr int smem = PaCfg<T, DP, NT>::kSmem;
-  if (cudaFuncSetAttribute(paged_attn_kernel<T, DP, NT, OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return BL_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(paged_attn_kernel<T, DP, NT, OutT>, smem, done)) return BL_ERR_CUDA;
   const int64_t most = a.B * a.Hkv * a.chunks * ceil_div(a.ldt * a.page, kPaTile);
-  const int64_t grid = most < 1 ? 1 : most < kPaCtas ? most : kPaCtas;
+  const int64_t grid = most < 1 ? 1 : most < PaCfg<T, DP, NT>::kCtas ? most : PaCfg<T, DP, NT>::kCtas;
   paged_attn_kernel<T, DP, NT, OutT><<<unsigned(grid), kPaThreads, smem, st>>>(a);
   return launch_status();
 }
@@ -393,7 +406,7 @@ bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const
 size_t bl_paged_attention_workspace_size(int64_t B, int Hq, const bl_kv_pages* cache) {
   if (!cache || B < 1 || Hq < 1 || cache->Hkv < 1 || Hq % cache->Hkv != 0 || cache->D < 8 || cache->D > kAttnMaxD) return 0;
   const int heads = 8 * paged_nt(Hq, cache->Hkv);
-  return kPaCountBytes + align_up(size_t(2 * kPaCtas) * size_t(heads) * size_t(paged_pad(cache->D) + 2) * 4);
+  return kPaCountBytes + align_up(size_t(2 * kPaMaxCtas) * size_t(heads) * size_t(paged_pad(cache->D) + 2) * 4);
 }
 
 bl_status bl_paged_attention(const void* q, int64_t B, int Hq, const bl_kv_pages* cache, const int32_t* table,

@@ -6,9 +6,10 @@
 // Bound by memory: every visible key and value is read once, 4 D bytes per token
 // and key head, for 4 D operations per query head.  So
 //   - the visible 64-token tiles of all sequences and key heads form one line that
-//     is cut into equal parts, one per CTA (two CTAs an SM): ragged batches and a
+//     is cut into equal parts, one per CTA (three or four CTAs an SM: a tile's
+//     chain of products, exchanges and exponentials is long, other warps fill it): ragged batches and a
 //     single long sequence load every SM alike;
-//   - tiles arrive by 16-byte asynchronous copies, kPaStages in flight, the page of
+//   - tiles arrive by 16-byte asynchronous copies, kStages in flight, the page of
 //     each row looked up two tiles ahead; rows that are not visible are filled with
 //     zeros instead of being read;
 //   - the scores are taken transposed, S^T = K q^T (keys are the 16-row side of the
@@ -30,8 +31,8 @@
 
 namespace bl {
 
-constexpr int kPaThreads = 128, kPaTile = 64, kPaStages = 3;
-constexpr int kPaCtas = 296;                         // two for each of B200's 148 SMs
+constexpr int kPaThreads = 128, kPaTile = 64;
+constexpr int kPaMaxCtas = 148 * 4;                  // planned for B200's 148 SMs
 constexpr float kPaLow = -1e30f;                     // below every finite scaled score that matters
 
 struct PaArgs {
@@ -41,8 +42,8 @@ struct PaArgs {
   int Hq, Hkv, D, page, window, sinks;
   float scale_log2;
   void* out;
-  unsigned int* count;      // [kPaCtas]
-  float* part;              // [2 kPaCtas][8 NT][DP + 2]
+  unsigned int* count;      // [kPaMaxCtas]
+  float* part;              // [2 kPaMaxCtas][8 NT][DP + 2]
   int group, chunks;        // query heads per key head; ceil(group / (8 NT))
   uint32_t page_magic, page_shift;
 };
@@ -123,8 +124,11 @@ struct PaCfg {
   static constexpr int kTileBytes = kPaTile * DP * 2;
   static constexpr int kStage = 2 * kTileBytes;
   static constexpr int kHeads = 8 * NT;
+  static constexpr int kPerSm = DP == 128 ? 3 : 4;     // CTAs an SM
+  static constexpr int kStages = DP == 128 ? 2 : 3;
+  static constexpr int kCtas = 148 * kPerSm;
   static constexpr int kJoin = kHeads * DP * 4;
-  static constexpr int kSmem = kPaStages * kStage + kJoin;
+  static constexpr int kSmem = kStages * kStage + kJoin;
 };
 
 // Position in the line of tiles: sequence b, key head and chunk (item), tile t of it.
@@ -135,12 +139,12 @@ struct PaAt {
 };
 
 template <typename T, int DP, int NT, typename OutT>
-__global__ void __launch_bounds__(kPaThreads, 2)
+__global__ void __launch_bounds__(kPaThreads, NT == 1 ? PaCfg<T, DP, NT>::kPerSm : 2)
 paged_attn_kernel(const PaArgs a) {
   using C = PaCfg<T, DP, NT>;
   extern __shared__ __align__(128) unsigned char pa_smem[];
   unsigned char* smem = pa_smem;
-  __shared__ int64_t s_row[2][kPaTile];          // element offset of each row's head data, -1: not visible
+  __shared__ int64_t s_row[C::kStages][kPaTile]; // element offset of each row's head data, -1: not visible
   __shared__ float s_m[4][C::kHeads], s_l[4][C::kHeads];
   __shared__ int64_t s_scan[4];
   __shared__ int64_t s_find[2];                  // sequence of this CTA's first tile, line index of its first tile
@@ -149,31 +153,18 @@ paged_attn_kernel(const PaArgs a) {
   constexpr float kShift = std::is_same<T, __half>::value ? 14.f : 0.f;   // keeps float16 terms of small probabilities normal
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = smem_u32(smem);
-  float* join = reinterpret_cast<float*>(smem + kPaStages * C::kStage);
+  float* join = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
   const int items = a.Hkv * a.chunks;
   bool range = false, bad = false;
 
   // the line: total tiles, this CTA's part, and the sequence where it begins
-  int64_t total = 0;
-  for (int64_t b = tid; b < a.B; b += kPaThreads) total += pa_tiles(pa_len(a, b, range), a.window, a.sinks).n;
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) s_scan[warp] = total;
-  __syncthreads();
-  total = (s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3]) * items;
-  const int64_t ctas = min(int64_t(gridDim.x), total);
-  // rows without tokens are nobody's tiles: zeros from the CTAs in turn
-  for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (pa_len(a, b, range) == 0)
-      for (int i = tid; i < a.Hq * a.D; i += kPaThreads) static_cast<OutT*>(a.out)[b * a.Hq * a.D + i] = from_f32<OutT>(0.f);
-  if (range) raise_status(kDevRange);
-  if (int64_t(blockIdx.x) >= ctas) return;
-  const int64_t lo = int64_t(blockIdx.x) * total / ctas, hi = (int64_t(blockIdx.x) + 1) * total / ctas;
+  int64_t total = 0, ctas = 0, lo = 0, hi = 0;
   {
-    int64_t before = 0;                              // line tiles of the sequences before this round's
-    for (int64_t b0 = 0; b0 < a.B; b0 += kPaThreads) {
-      const int64_t b = b0 + tid;
-      const int64_t n = b < a.B ? int64_t(pa_tiles(pa_len(a, b, range), a.window, a.sinks).n) * items : 0;
-      int64_t x = n;
+    const int64_t rounds = ceil_div(a.B, kPaThreads);
+    int64_t n = 0, x = 0, before = 0;                // of sequence b: line tiles, and up to it within the round
+    auto scan = [&](int64_t b) {                     // returns the round's tiles
+      n = b < a.B ? int64_t(pa_tiles(pa_len(a, b, range), a.window, a.sinks).n) * items : 0;
+      x = n;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
@@ -181,16 +172,38 @@ paged_attn_kernel(const PaArgs a) {
       __syncthreads();
       if (lane == 31) s_scan[warp] = x;
       __syncthreads();
-      int64_t first = before + x - n;
-      for (int w = 0; w < warp; ++w) first += s_scan[w];
-      if (n > 0 && first <= lo && lo < first + n) {
-        s_find[0] = b;
-        s_find[1] = first;
+      for (int w = 0; w < warp; ++w) x += s_scan[w];
+      return s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
+    };
+    for (int64_t r = 0; r < rounds; ++r) total += scan(r * kPaThreads + tid);
+    ctas = min(int64_t(gridDim.x), total);
+    if (int64_t(blockIdx.x) < ctas) {
+      lo = int64_t(blockIdx.x) * total / ctas;
+      hi = (int64_t(blockIdx.x) + 1) * total / ctas;
+      for (int64_t r = 0; r < rounds; ++r) {
+        const int64_t sum = rounds == 1 ? total : scan(r * kPaThreads + tid);
+        const int64_t first = before + x - n;
+        if (n > 0 && first <= lo && lo < first + n) {
+          s_find[0] = r * kPaThreads + tid;
+          s_find[1] = first;
+        }
+        before += sum;
+        if (before > lo) break;
       }
-      before += s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
-      if (before > lo) break;
+      __syncthreads();
     }
-    __syncthreads();
+  }
+  // rows without tokens are nobody's tiles: zeros, from the CTAs in turn
+  auto empty_rows = [&]() {
+    for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
+      if (pa_len(a, b, range) == 0)
+        for (int i = tid; i < a.Hq * a.D; i += kPaThreads)
+          static_cast<OutT*>(a.out)[b * a.Hq * a.D + i] = from_f32<OutT>(0.f);
+    if (range) raise_status(kDevRange);
+  };
+  if (int64_t(blockIdx.x) >= ctas) {
+    empty_rows();
+    return;
   }
 
   auto enter = [&](PaAt& p, int64_t b, int64_t first, int64_t x) {   // line index x, in sequence b whose tiles begin at first
@@ -213,36 +226,42 @@ paged_attn_kernel(const PaArgs a) {
       p.tiles = pa_tiles(p.len, a.window, a.sinks);
     } while (p.tiles.n == 0);
   };
-  // thread tid < 64 looks up where row tid of a tile is, in two steps so that the page
+  // Thread tid looks up where row tid % 64 of a tile is, in two steps so that the page
   // number's way from memory overlaps a tile's work
-  int64_t pend_in = 0;                               // the row's place within its page's head, -1: not visible
-  int pend_page = 0;
-  auto look_up = [&](const PaAt& p) {
-    const int t = p.t < p.tiles.lead ? p.t : p.t - p.tiles.lead + p.tiles.from;
-    const int j = t * kPaTile + tid;
-    pend_in = -1;
-    if (!(j < p.len && sees(p.len - 1, j, a.window, a.sinks))) return;
-    const uint32_t n = a.page == 1 ? uint32_t(j) : __umulhi(uint32_t(j), a.page_magic) >> a.page_shift;
-    pend_in = int64_t(p.item / a.chunks) * a.page + (j - int(n) * a.page);
-    pend_page = a.table[p.b * a.ldt + n];
+  struct Pending {
+    int64_t in;                                      // the row's place within its page, -1: not visible
+    int page;
   };
-  auto place = [&]() -> int64_t {
-    if (pend_in < 0) return -1;
-    if (pend_page < 0 || pend_page >= a.pages) {
-      range = true;
-      return -1;
+  auto look_up = [&](const PaAt& p) {
+    Pending d;
+    d.in = -1;
+    d.page = 0;
+    const int t = p.t < p.tiles.lead ? p.t : p.t - p.tiles.lead + p.tiles.from;
+    const int j = t * kPaTile + (tid & (kPaTile - 1));
+    if (j < p.len && sees(p.len - 1, j, a.window, a.sinks)) {
+      const uint32_t n = a.page == 1 ? uint32_t(j) : __umulhi(uint32_t(j), a.page_magic) >> a.page_shift;
+      d.in = int64_t(p.item / a.chunks) * a.page + (j - int(n) * a.page);
+      d.page = a.table[p.b * a.ldt + n];
     }
-    return (int64_t(pend_page) * a.Hkv * a.page + pend_in) * a.D;
+    return d;
+  };
+  auto place = [&](const Pending& d, int tile) {
+    int64_t off = -1;
+    if (d.in >= 0) {
+      if (d.page < 0 || d.page >= a.pages) range = true;
+      else off = (int64_t(d.page) * a.Hkv * a.page + d.in) * a.D;
+    }
+    s_row[tile % C::kStages][tid & (kPaTile - 1)] = off;
   };
   constexpr int kRowChunks = DP / 8, kRowStep = kPaThreads / kRowChunks;
   const int my_chunk = tid % kRowChunks, my_row = tid / kRowChunks;
-  auto issue = [&](int stage, int buf) {
+  auto issue = [&](int stage) {
     if (8 * my_chunk >= a.D) return;
     const uint32_t kd = base + stage * C::kStage, vd = kd + C::kTileBytes;
 #pragma unroll
     for (int i = 0; i < kPaTile / kRowStep; ++i) {
       const int r = my_row + i * kRowStep;
-      const int64_t off = s_row[buf][r];
+      const int64_t off = s_row[stage][r];
       const int n = off < 0 ? 0 : 16;
       const int64_t e = off < 0 ? 0 : off + 8 * my_chunk;
       const uint32_t d = pa_off<DP>(r, my_chunk);
@@ -252,7 +271,7 @@ paged_attn_kernel(const PaArgs a) {
   };
 
   if (a.D < DP) {                                    // columns past D: zeros, never written again
-    for (int i = tid; i < kPaStages * C::kStage / 16; i += kPaThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < C::kStages * C::kStage / 16; i += kPaThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
 
@@ -260,30 +279,27 @@ paged_attn_kernel(const PaArgs a) {
   enter(cur, s_find[0], s_find[1], lo);
   load = cur;
   const int n = int(hi - lo);                        // tiles of this CTA
-  int looked = 0, located = 0;                       // tiles whose rows are asked for, and known
-  auto ask = [&]() {
-    if (looked < n) {
-      if (tid < kPaTile) look_up(load);
-      ++looked;
-      advance(load);
+  // the first tiles' rows all at once (threads 0..63 the even ones, 64..127 the odd ones)
+  {
+    Pending d[(C::kStages + 1) / 2];
+#pragma unroll
+    for (int t = 0; t < C::kStages; ++t) {
+      if (t < n && (tid / kPaTile) == (t & 1)) d[t / 2] = look_up(load);
+      if (t < n) advance(load);
     }
-  };
-  auto next_rows = [&]() {                           // writes down the rows asked for last, asks for the next
-    if (located < n) {
-      if (tid < kPaTile) s_row[located & 1][tid] = place();
-      ++located;
-    }
-    ask();
-  };
-  ask();
-  next_rows();
-  for (int s = 0; s < kPaStages - 1; ++s) {
-    next_rows();
-    __syncthreads();
-    if (s < n) issue(s, s & 1);
-    cp_async_commit();
-    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < C::kStages; ++t)
+      if (t < n && (tid / kPaTile) == (t & 1)) place(d[t / 2], t);
   }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < C::kStages - 1; ++t) {
+    if (t < n) issue(t);
+    cp_async_commit();
+  }
+  Pending next;                                      // of tile kStages, then of those after it
+  next.in = -1;
+  if (tid < kPaTile && C::kStages < n) next = look_up(load);
 
   // per-lane state: heads 2 (lane % 4) + {0, 1} of each 8
   float m[NT][2], l[NT][2], o[DP / 16][NT][4];
@@ -314,14 +330,18 @@ paged_attn_kernel(const PaArgs a) {
   int seg_first = cur.t;                             // first tile of this segment within the item
 
   for (int it = 0; it < n; ++it) {
-    cp_async_wait<kPaStages - 2>();
+    cp_async_wait<C::kStages - 2>();
     __syncthreads();
-    if (it + kPaStages - 1 < n) issue((it + kPaStages - 1) % kPaStages, (it + kPaStages - 1) & 1);
+    if (it + C::kStages - 1 < n) issue((it + C::kStages - 1) % C::kStages);
     cp_async_commit();
-    // rows of tile it + kPaStages: into the buffer that tile it + kPaStages - 2 used (issued before this barrier)
-    next_rows();
+    // the rows of tile it + kStages, asked for a tile ago, into the place of tile it's
+    if (it + C::kStages < n) {
+      if (tid < kPaTile) place(next, it + C::kStages);
+      advance(load);
+      if (tid < kPaTile && it + C::kStages + 1 < n) next = look_up(load);
+    }
 
-    const uint32_t ks_base = base + (it % kPaStages) * C::kStage, vs_base = ks_base + C::kTileBytes;
+    const uint32_t ks_base = base + (it % C::kStages) * C::kStage, vs_base = ks_base + C::kTileBytes;
     const int r0 = warp * 16;
     float s[NT][4];
 #pragma unroll
@@ -471,13 +491,24 @@ paged_attn_kernel(const PaArgs a) {
           for (int i = tid; i < nh * a.D; i += kPaThreads) {
             const int h = i / a.D, d = i - h * a.D;
             float top = kPaLow, sum = 0.f, x = 0.f;
-            for (int64_t c = c0; c <= c1; ++c) {
-              const float* p = a.part + (2 * c + (c == c0 ? 1 : 0)) * kStride + h * (DP + 2);
-              const float pm = __ldcg(p + DP), pl = __ldcg(p + DP + 1), px = __ldcg(p + d);
-              const float t = fmaxf(top, pm), f0 = exp2_approx(top - t), f1 = exp2_approx(pm - t);
-              sum = fmaf(sum, f0, pl * f1);
-              x = fmaf(x, f0, px * f1);
-              top = t;
+            for (int64_t c = c0; c <= c1; c += 8) {                  // eight parts' loads in flight
+              float pm[8], pl[8], px[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int64_t at = min(c + e, c1);
+                const float* p = a.part + (2 * at + (at == c0 ? 1 : 0)) * kStride + h * (DP + 2);
+                pm[e] = __ldcg(p + DP);
+                pl[e] = __ldcg(p + DP + 1);
+                px[e] = __ldcg(p + d);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (c + e <= c1) {
+                  const float t = fmaxf(top, pm[e]), f0 = exp2_approx(top - t), f1 = exp2_approx(pm[e] - t);
+                  sum = fmaf(sum, f0, pl[e] * f1);
+                  x = fmaf(x, f0, px[e] * f1);
+                  top = t;
+                }
             }
             const float r = x / sum;
             if (!(fabsf(r) < INFINITY)) bad = true;
@@ -496,7 +527,7 @@ paged_attn_kernel(const PaArgs a) {
     }
   }
   if (bad) raise_status(kDevNonFinite);
-  if (range) raise_status(kDevRange);
+  empty_rows();
 }
 
 }  // namespace bl

@@ -96,12 +96,18 @@ bl_status launch_norm_rope(const QrArgs& a, cudaStream_t st) {
 }
 
 // CTAs of the backward (and rows of its partial sums): planned for 148 SMs.
-constexpr int kQrBackCtas = 148 * 4;
+constexpr int kQrBackCtas = 148 * 2;
 int rows_back_grid(const bl_qkv_rows* r) {
   int lanes = 1;
   while (lanes < r->D / 8) lanes *= 2;
   const int64_t g = ceil_div(r->M * (r->Hq + 2 * int64_t(r->Hkv)), int64_t(kQrThreads / lanes));
   return int(g < 1 ? 1 : g < kQrBackCtas ? g : kQrBackCtas);
+}
+
+template <typename T>
+void launch_rows_back(const QrArgs& a, bool two, int grid, int smem, cudaStream_t st) {
+  if (two) qk_norm_rope_backward_kernel<T, 2><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
+  else qk_norm_rope_backward_kernel<T, 1><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
 }
 
 bl_status check_cache(const bl_kv_pages* c) {
@@ -352,12 +358,11 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
   a.lddk = lddk;
   a.lddv = lddv;
   const int smem = (kQrThreads / a.lanes) * 2 * a.D * 4;       // at most 16 KB
-  const void* fn = t == BL_T_F32   ? reinterpret_cast<const void*>(qk_norm_rope_backward_kernel<float>)
-                   : t == BL_T_F16 ? reinterpret_cast<const void*>(qk_norm_rope_backward_kernel<__half>)
-                                   : reinterpret_cast<const void*>(qk_norm_rope_backward_kernel<__nv_bfloat16>);
-  void* args[] = {&a};
-  if (cudaLaunchKernel(fn, dim3(unsigned(grid)), dim3(kQrThreads), args, size_t(smem), stream) != cudaSuccess)
-    return BL_ERR_CUDA;
+  // two heads an item once that fills the SMs, one where latency counts
+  const bool two = rows->M * ceil_div(rows->Hq + 2 * int64_t(rows->Hkv), 2) >= int64_t(grid) * (kQrThreads / a.lanes) * 2;
+  if (t == BL_T_F32) launch_rows_back<float>(a, two, grid, smem, stream);
+  else if (t == BL_T_F16) launch_rows_back<__half>(a, two, grid, smem, stream);
+  else launch_rows_back<__nv_bfloat16>(a, two, grid, smem, stream);
   if (a.part) gain_sum_kernel<<<unsigned(ceil_div(2 * a.D, 32)), 256, 0, stream>>>(a.part, grid, a.D, dgq, dgk);
   return launch_status();
 }

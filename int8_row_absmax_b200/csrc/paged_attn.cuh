@@ -43,7 +43,7 @@ struct PaArgs {
   float scale_log2;
   void* out;
   unsigned int* count;      // [kPaMaxCtas]
-  float* part;              // [2 kPaMaxCtas][8 NT][DP + 2]
+  float* part;              // [2 kPaMaxCtas][8 NT DP of O, then 8 NT pairs of maximum and sum]
   int group, chunks;        // query heads per key head; ceil(group / (8 NT))
   uint32_t page_magic, page_shift;
 };
@@ -127,7 +127,7 @@ struct PaCfg {
   static constexpr int kPerSm = DP == 128 ? 3 : 4;     // CTAs an SM
   static constexpr int kStages = DP == 128 ? 2 : 3;
   static constexpr int kCtas = 148 * kPerSm;
-  static constexpr int kJoin = kHeads * DP * 4;
+  static constexpr int kJoin = kHeads * DP * 4 > kPaThreads * 16 ? kHeads * DP * 4 : kPaThreads * 16;   // O, or a float4 a thread
   static constexpr int kSmem = kStages * kStage + kJoin;
 };
 
@@ -147,7 +147,9 @@ paged_attn_kernel(const PaArgs a) {
   __shared__ int64_t s_row[C::kStages][kPaTile]; // element offset of each row's head data, -1: not visible
   __shared__ float s_m[4][C::kHeads], s_l[4][C::kHeads];
   __shared__ int64_t s_scan[4];
-  __shared__ int64_t s_find[2];                  // sequence of this CTA's first tile, line index of its first tile
+  __shared__ int64_t s_find[3];                  // sequence of this CTA's first tile, line index of its first tile, its length
+  __shared__ int s_empty;                        // whether a sequence has no tokens
+  __shared__ float2 s_join[kPaThreads];
   __shared__ unsigned int s_last;
   constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
   constexpr float kShift = std::is_same<T, __half>::value ? 14.f : 0.f;   // keeps float16 terms of small probabilities normal
@@ -162,8 +164,11 @@ paged_attn_kernel(const PaArgs a) {
   {
     const int64_t rounds = ceil_div(a.B, kPaThreads);
     int64_t n = 0, x = 0, before = 0;                // of sequence b: line tiles, and up to it within the round
+    int len = 0;
+    if (tid == 0) s_empty = 0;
     auto scan = [&](int64_t b) {                     // returns the round's tiles
-      n = b < a.B ? int64_t(pa_tiles(pa_len(a, b, range), a.window, a.sinks).n) * items : 0;
+      len = b < a.B ? pa_len(a, b, range) : 0;
+      n = int64_t(pa_tiles(len, a.window, a.sinks).n) * items;
       x = n;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -171,6 +176,7 @@ paged_attn_kernel(const PaArgs a) {
       }
       __syncthreads();
       if (lane == 31) s_scan[warp] = x;
+      if (b < a.B && n == 0) s_empty = 1;
       __syncthreads();
       for (int w = 0; w < warp; ++w) x += s_scan[w];
       return s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
@@ -186,6 +192,7 @@ paged_attn_kernel(const PaArgs a) {
         if (n > 0 && first <= lo && lo < first + n) {
           s_find[0] = r * kPaThreads + tid;
           s_find[1] = first;
+          s_find[2] = len;
         }
         before += sum;
         if (before > lo) break;
@@ -195,7 +202,7 @@ paged_attn_kernel(const PaArgs a) {
   }
   // rows without tokens are nobody's tiles: zeros, from the CTAs in turn
   auto empty_rows = [&]() {
-    for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
+    for (int64_t b = blockIdx.x; s_empty && b < a.B; b += gridDim.x)
       if (pa_len(a, b, range) == 0)
         for (int i = tid; i < a.Hq * a.D; i += kPaThreads)
           static_cast<OutT*>(a.out)[b * a.Hq * a.D + i] = from_f32<OutT>(0.f);
@@ -206,9 +213,9 @@ paged_attn_kernel(const PaArgs a) {
     return;
   }
 
-  auto enter = [&](PaAt& p, int64_t b, int64_t first, int64_t x) {   // line index x, in sequence b whose tiles begin at first
+  auto enter = [&](PaAt& p, int64_t b, int64_t first, int len, int64_t x) {   // line index x, in sequence b whose tiles begin at first
     p.b = b;
-    p.len = pa_len(a, b, range);
+    p.len = len;
     p.tiles = pa_tiles(p.len, a.window, a.sinks);
     p.item = int((x - first) / p.tiles.n);
     p.flat = first + int64_t(p.item) * p.tiles.n;
@@ -276,7 +283,7 @@ paged_attn_kernel(const PaArgs a) {
   }
 
   PaAt cur, load;
-  enter(cur, s_find[0], s_find[1], lo);
+  enter(cur, s_find[0], s_find[1], int(s_find[2]), lo);
   load = cur;
   const int n = int(hi - lo);                        // tiles of this CTA
   // the first tiles' rows all at once (threads 0..63 the even ones, 64..127 the odd ones)
@@ -465,13 +472,13 @@ paged_attn_kernel(const PaArgs a) {
       } else {
         // its part to the workspace: slot 0 of the CTA if the item began before it, slot 1 if it goes on
         float* part = a.part + (2 * int64_t(blockIdx.x) + (seg_first == 0 ? 1 : 0)) * C::kHeads * (DP + 2);
-        for (int i = tid; i < nh * DP; i += kPaThreads) __stcg(part + (i / DP) * (DP + 2) + i % DP, join[i]);
+        for (int i = tid; i < nh * DP / 4; i += kPaThreads)
+          __stcg(reinterpret_cast<float4*>(part) + i, reinterpret_cast<const float4*>(join)[i]);
         for (int h = tid; h < nh; h += kPaThreads) {
           const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
           float sum = 0.f;
           for (int w = 0; w < 4; ++w) sum = fmaf(s_l[w][h], exp2_approx(s_m[w][h] - top), sum);
-          __stcg(part + h * (DP + 2) + DP, top);
-          __stcg(part + h * (DP + 2) + DP + 1, sum);
+          __stcg(reinterpret_cast<float2*>(part + C::kHeads * DP) + h, make_float2(top, sum));
         }
         __threadfence();
         __syncthreads();
@@ -487,32 +494,63 @@ paged_attn_kernel(const PaArgs a) {
         }
         __syncthreads();
         if (s_last) {
+          // a thread takes four columns of every `groups`-th part, eight parts' loads in flight; then
+          // the groups are joined through shared memory
           constexpr int kStride = C::kHeads * (DP + 2);
-          for (int i = tid; i < nh * a.D; i += kPaThreads) {
-            const int h = i / a.D, d = i - h * a.D;
-            float top = kPaLow, sum = 0.f, x = 0.f;
-            for (int64_t c = c0; c <= c1; c += 8) {                  // eight parts' loads in flight
-              float pm[8], pl[8], px[8];
+          const int cols = nh * DP / 4, parts = int(c1 - c0) + 1;
+          const int groups = min(kPaThreads / min(cols, kPaThreads), parts);
+          for (int col0 = 0; col0 < cols; col0 += kPaThreads) {
+            const int col = col0 + (groups > 1 ? tid % cols : tid), g = groups > 1 ? tid / cols : 0;
+            const bool on = col < cols && g < groups;
+            const int h = col * 4 / DP;
+            float top = kPaLow, sum = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = g; on && k < parts; k += 8 * groups) {
+              float2 ps[8];
+              float4 px[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const int64_t at = min(c + e, c1);
-                const float* p = a.part + (2 * at + (at == c0 ? 1 : 0)) * kStride + h * (DP + 2);
-                pm[e] = __ldcg(p + DP);
-                pl[e] = __ldcg(p + DP + 1);
-                px[e] = __ldcg(p + d);
+                const int64_t at = c0 + min(k + e * groups, parts - 1);
+                const float* p = a.part + (2 * at + (at == c0 ? 1 : 0)) * kStride;
+                ps[e] = __ldcg(reinterpret_cast<const float2*>(p + C::kHeads * DP) + h);
+                px[e] = __ldcg(reinterpret_cast<const float4*>(p) + col);
               }
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (c + e <= c1) {
-                  const float t = fmaxf(top, pm[e]), f0 = exp2_approx(top - t), f1 = exp2_approx(pm[e] - t);
-                  sum = fmaf(sum, f0, pl[e] * f1);
-                  x = fmaf(x, f0, px[e] * f1);
+                if (k + e * groups < parts) {
+                  const float t = fmaxf(top, ps[e].x), f0 = exp2_approx(top - t), f1 = exp2_approx(ps[e].x - t);
+                  sum = fmaf(sum, f0, ps[e].y * f1);
+                  x = make_float4(fmaf(x.x, f0, px[e].x * f1), fmaf(x.y, f0, px[e].y * f1), fmaf(x.z, f0, px[e].z * f1),
+                                  fmaf(x.w, f0, px[e].w * f1));
                   top = t;
                 }
             }
-            const float r = x / sum;
-            if (!(fabsf(r) < INFINITY)) bad = true;
-            out[i] = from_f32<OutT>(r);
+            __syncthreads();
+            if (on && g > 0) {
+              reinterpret_cast<float4*>(join)[tid] = x;
+              s_join[tid] = make_float2(top, sum);
+            }
+            __syncthreads();
+            if (on && g == 0) {
+              for (int o = 1; o < groups; ++o) {
+                const float4 y = reinterpret_cast<const float4*>(join)[o * cols + col];
+                const float2 ys = s_join[o * cols + col];
+                const float t = fmaxf(top, ys.x), f0 = exp2_approx(top - t), f1 = exp2_approx(ys.x - t);
+                sum = fmaf(sum, f0, ys.y * f1);
+                x = make_float4(fmaf(x.x, f0, y.x * f1), fmaf(x.y, f0, y.y * f1), fmaf(x.z, f0, y.z * f1),
+                                fmaf(x.w, f0, y.w * f1));
+                top = t;
+              }
+              const int d = col * 4 - h * DP;
+              if (d < a.D) {
+                const float r[4] = {x.x / sum, x.y / sum, x.z / sum, x.w / sum};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (!(fabsf(r[e]) < INFINITY)) bad = true;
+                  out[h * a.D + d + e] = from_f32<OutT>(r[e]);
+                }
+              }
+            }
           }
         }
       }

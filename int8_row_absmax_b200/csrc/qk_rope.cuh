@@ -110,12 +110,20 @@ qk_norm_rope_kernel(const QrArgs a) {
   bool bad = false, range = false;
   // whole warps take every turn together: the shuffles need all lanes
   const int64_t first = int64_t(blockIdx.x) * per_block, mine = threadIdx.x / lanes;
+  // the token, its position and slot are asked for an item ahead: the table's row follows the position
+  int64_t m_next = 0, c_next = 0, p_next = 0, at_next = -1;
+  auto ask = [&](int64_t i) {
+    if (i >= items) return;
+    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
+    p_next = a.R ? a.pos[m_next] : 0;
+    if (kAppend) at_next = a.slots[m_next];
+  };
+  ask(first + mine);
   for (int64_t base = first; base < items; base += step) {
     const int64_t i = base + mine;
     const bool live = i < items;
-    int64_t m = 0, c = 0;
-    split_index(live ? i : 0, chunks, items < (int64_t(1) << 31), m, c);
-    const int h0 = int(c) * kHeads;
+    const int64_t m = m_next, p = p_next, at = at_next;
+    const int h0 = int(c_next) * kHeads;
     float4 x[kHeads], y[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
@@ -129,20 +137,19 @@ qk_norm_rope_kernel(const QrArgs a) {
       x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (value ? 8 * u : lo)));
       y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (value ? 8 * u + 4 : hi)));
     }
-    const int64_t p = live && a.R ? a.pos[m] : 0;
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
-    if (!ok) range = true;
+    if (live && !ok) range = true;
     float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turned && ok) {
       cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
       sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
     }
-    int64_t at = 0, page = 0, in = 0;
+    ask(i + step);
+    int64_t page = 0, in = 0;
     bool store = true;
     if (kAppend) {
-      at = live ? a.slots[m] : -1;
-      store = at >= 0 && at < a.nslots;
-      if (at >= a.nslots) range = true;
+      store = live && at >= 0 && at < a.nslots;
+      if (live && at >= a.nslots) range = true;
       split_index(store ? at : 0, a.page, a.nslots < (int64_t(1) << 31), page, in);
     }
 #pragma unroll
@@ -189,79 +196,95 @@ qk_norm_rope_kernel(const QrArgs a) {
 // The gradient.  A group of lanes keeps the same columns throughout, so the gains'
 // gradients stay in its registers until the end; then the CTA adds its groups in
 // order and writes one partial row, and gain_sum_kernel adds those in order.
-template <typename T>
-__global__ void __launch_bounds__(kQrThreads)
+template <typename T, int kHeads>
+__global__ void __launch_bounds__(kQrThreads, 2)
 qk_norm_rope_backward_kernel(const QrArgs a) {
   extern __shared__ float sums[];                    // [per_block, 2, D]
   const int lanes = a.lanes, u = threadIdx.x & (lanes - 1), grp = threadIdx.x / lanes;
   const int per_block = kQrThreads / lanes;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t items = a.M * heads, step = int64_t(gridDim.x) * per_block;
+  const int heads = a.Hq + 2 * a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
+  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * per_block;
   const bool on = u < (a.D >> 3), turned = on && u < (a.R >> 3), split = turned && !a.interleaved;
   const int lo = on ? (split ? 4 * u : 8 * u) : 0, hi = on ? (split ? (a.R >> 1) + 4 * u : 8 * u + 4) : 0;
   const float inv_d = 1.f / float(a.D);
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f), one = make_float4(1.f, 1.f, 1.f, 1.f);
+  const float4 gq0 = a.gq ? *reinterpret_cast<const float4*>(a.gq + lo) : one;
+  const float4 gq1 = a.gq ? *reinterpret_cast<const float4*>(a.gq + hi) : one;
+  const float4 gk0 = a.gk ? *reinterpret_cast<const float4*>(a.gk + lo) : one;
+  const float4 gk1 = a.gk ? *reinterpret_cast<const float4*>(a.gk + hi) : one;
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
   bool bad = false, range = false;
+  int64_t m_next = 0, c_next = 0, p_next = 0;        // asked for an item ahead: the table's row follows the position
+  auto ask = [&](int64_t i) {
+    if (i >= items) return;
+    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
+    p_next = a.R ? a.pos[m_next] : 0;
+  };
+  ask(int64_t(blockIdx.x) * per_block + grp);
   for (int64_t base = int64_t(blockIdx.x) * per_block; base < items; base += step) {
     const int64_t i = base + grp;
     const bool live = i < items;
-    int64_t m = 0, hh = 0;
-    split_index(live ? i : 0, heads, items < (int64_t(1) << 31), m, hh);
-    const int h = int(hh);
-    const bool value = h >= a.Hq + a.Hkv, query = h < a.Hq;
-    float4 x = zero, y = zero, e = zero, f = zero;
-    const int64_t p = live && a.R ? a.pos[m] : 0;
+    const int64_t m = m_next, p = p_next;
+    const int h0 = int(c_next) * kHeads;
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
-    if (!ok) range = true;
+    if (live && !ok) range = true;
     const bool work = live && on && ok;
-    if (work) {
+    float4 x[kHeads], y[kHeads], e[kHeads], f[kHeads];
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      const int h = h0 + j;
+      const bool value = h >= a.Hq + a.Hkv, query = h < a.Hq;
+      x[j] = y[j] = e[j] = f[j] = zero;
+      if (!work || h >= heads) continue;
       const T* d = query ? static_cast<const T*>(a.dq) + (m * a.Hq + h) * a.D
-                         : static_cast<const T*>(value ? a.dv : a.dk) + (m * a.Hkv + (h - a.Hq) % a.Hkv) * a.D;
-      e = ld4(d + (value ? 8 * u : lo));
-      f = ld4(d + (value ? 8 * u + 4 : hi));
-      if (!value) {
-        const float* row = query ? a.q + m * a.ldq + int64_t(h) * a.D : a.k + m * a.ldk + int64_t(h - a.Hq) * a.D;
-        x = ld_stream_f4(reinterpret_cast<const float4*>(row + lo));
-        y = ld_stream_f4(reinterpret_cast<const float4*>(row + hi));
-        if (turned) {
-          const float4 c = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
-          float4 s = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
-          s = make_float4(-s.x, -s.y, -s.z, -s.w);
-          rotate(e, f, c, s, a.interleaved != 0);
-        }
+                         : static_cast<const T*>(value ? a.dv : a.dk) + (m * a.Hkv + (value ? h - a.Hq - a.Hkv : h - a.Hq)) * a.D;
+      e[j] = ld4(d + (value ? 8 * u : lo));
+      f[j] = ld4(d + (value ? 8 * u + 4 : hi));
+      if (value) continue;
+      const float* row = query ? a.q + m * a.ldq + int64_t(h) * a.D : a.k + m * a.ldk + int64_t(h - a.Hq) * a.D;
+      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + lo));
+      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + hi));
+    }
+    float4 cs = one, sn = zero;
+    if (work && turned) {
+      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
+      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
+      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
+    }
+    ask(i + step);
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      const int h = h0 + j;
+      const bool value = h >= a.Hq + a.Hkv, query = h < a.Hq;
+      if (turned && !value) rotate(e[j], f[j], cs, sn, a.interleaved != 0);
+      const float ss = head_sum(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)), lanes);
+      const float r = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
+      x[j] = scale4(x[j], r);
+      y[j] = scale4(y[j], r);
+      const float4 px = mul4(e[j], x[j]), py = mul4(f[j], y[j]);          // dg terms
+      const float4 ge = mul4(e[j], query ? gq0 : gk0), gf = mul4(f[j], query ? gq1 : gk1);
+      const float t = head_sum(dot4(ge, x[j], dot4(gf, y[j], 0.f)), lanes) * inv_d;
+      if (!work || h >= heads) continue;
+      if (value) {
+        float* out = a.dxv + m * a.lddv + int64_t(h - a.Hq - a.Hkv) * a.D;
+        *reinterpret_cast<float4*>(out + 8 * u) = e[j];
+        *reinterpret_cast<float4*>(out + 8 * u + 4) = f[j];
+        continue;
+      }
+      if (!(ss <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
+      float* out = query ? a.dxq + m * a.lddq + int64_t(h) * a.D : a.dxk + m * a.lddk + int64_t(h - a.Hq) * a.D;
+      *reinterpret_cast<float4*>(out + lo) = make_float4(r * fmaf(-x[j].x, t, ge.x), r * fmaf(-x[j].y, t, ge.y),
+                                                         r * fmaf(-x[j].z, t, ge.z), r * fmaf(-x[j].w, t, ge.w));
+      *reinterpret_cast<float4*>(out + hi) = make_float4(r * fmaf(-y[j].x, t, gf.x), r * fmaf(-y[j].y, t, gf.y),
+                                                         r * fmaf(-y[j].z, t, gf.z), r * fmaf(-y[j].w, t, gf.w));
+      if (query) {
+        sq0 = make_float4(sq0.x + px.x, sq0.y + px.y, sq0.z + px.z, sq0.w + px.w);
+        sq1 = make_float4(sq1.x + py.x, sq1.y + py.y, sq1.z + py.z, sq1.w + py.w);
+      } else {
+        sk0 = make_float4(sk0.x + px.x, sk0.y + px.y, sk0.z + px.z, sk0.w + px.w);
+        sk1 = make_float4(sk1.x + py.x, sk1.y + py.y, sk1.z + py.z, sk1.w + py.w);
       }
     }
-    const float ss = head_sum(dot4(x, x, dot4(y, y, 0.f)), lanes);
-    const float r = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
-    x = scale4(x, r);
-    y = scale4(y, r);
-    const float4 px = mul4(e, x), py = mul4(f, y);                // dg terms
-    const float* g = query ? a.gq : a.gk;
-    float4 ge = e, gf = f;
-    if (g && on && !value) {
-      ge = mul4(e, *reinterpret_cast<const float4*>(g + lo));
-      gf = mul4(f, *reinterpret_cast<const float4*>(g + hi));
-    }
-    const float t = head_sum(dot4(ge, x, dot4(gf, y, 0.f)), lanes) * inv_d;
-    if (!work) continue;
-    float* out;
-    if (value) {
-      out = a.dxv + m * a.lddv + int64_t(h - a.Hq - a.Hkv) * a.D;
-      *reinterpret_cast<float4*>(out + 8 * u) = e;
-      *reinterpret_cast<float4*>(out + 8 * u + 4) = f;
-      continue;
-    }
-    if (!(ss <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
-    out = query ? a.dxq + m * a.lddq + int64_t(h) * a.D : a.dxk + m * a.lddk + int64_t(h - a.Hq) * a.D;
-    *reinterpret_cast<float4*>(out + lo) = make_float4(r * fmaf(-x.x, t, ge.x), r * fmaf(-x.y, t, ge.y),
-                                                       r * fmaf(-x.z, t, ge.z), r * fmaf(-x.w, t, ge.w));
-    *reinterpret_cast<float4*>(out + hi) = make_float4(r * fmaf(-y.x, t, gf.x), r * fmaf(-y.y, t, gf.y),
-                                                       r * fmaf(-y.z, t, gf.z), r * fmaf(-y.w, t, gf.w));
-    float4& s0 = query ? sq0 : sk0;
-    float4& s1 = query ? sq1 : sk1;
-    s0 = make_float4(s0.x + px.x, s0.y + px.y, s0.z + px.z, s0.w + px.w);
-    s1 = make_float4(s1.x + py.x, s1.y + py.y, s1.z + py.z, s1.w + py.w);
   }
   if (bad) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
@@ -287,8 +310,17 @@ gain_sum_kernel(const float* __restrict__ part, int rows, int D, float* __restri
   __shared__ float s[8][32];
   const int c = threadIdx.x & 31, sl = threadIdx.x >> 5, d = blockIdx.x * 32 + c;
   float v = 0.f;
-  if (d < 2 * D)
-    for (int r = sl; r < rows; r += 8) v += part[int64_t(r) * 2 * D + d];
+  if (d < 2 * D) {
+    int r = sl;
+    for (; r + 56 < rows; r += 64) {                   // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = part[int64_t(r + 8 * e) * 2 * D + d];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v += x[e];
+    }
+    for (; r < rows; r += 8) v += part[int64_t(r) * 2 * D + d];
+  }
   s[sl][c] = v;
   __syncthreads();
   if (sl == 0 && d < 2 * D) {

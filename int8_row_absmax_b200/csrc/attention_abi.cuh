@@ -77,37 +77,60 @@ QrArgs rows_args(const bl_qkv_rows* r) {
   a.gk = r->gk;
   a.eps = r->eps;
   a.page = 1;
-  a.lanes = 1;
-  while (a.lanes < r->D / 8) a.lanes *= 2;
   return a;
 }
 
+// Lanes that share a head: the power of two from 4 to 32 that covers D / 8.
+int rows_lanes(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+
 // Four heads an item once that still fills the SMs (eight loads in flight a
 // thread), one head an item below, where latency counts.
+template <typename T, bool kAppend, int kLanes>
+void launch_rows(const QrArgs& a, cudaStream_t st) {
+  constexpr int kPerBlock = kQrThreads / kLanes;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int64_t many = a.M * ceil_div(heads, 4);
+  if (many >= int64_t(num_sms()) * 4 * kPerBlock)
+    qk_norm_rope_kernel<T, kAppend, 4, kLanes><<<grid_for(many, kPerBlock, 16), kQrThreads, 0, st>>>(a);
+  else
+    qk_norm_rope_kernel<T, kAppend, 1, kLanes><<<grid_for(a.M * heads, kPerBlock, 16), kQrThreads, 0, st>>>(a);
+}
 template <typename T, bool kAppend>
 bl_status launch_norm_rope(const QrArgs& a, cudaStream_t st) {
-  const int per_block = kQrThreads / a.lanes, heads = a.Hq + 2 * a.Hkv;
-  const int64_t many = a.M * ceil_div(heads, 4);
-  if (many >= int64_t(num_sms()) * 4 * per_block)
-    qk_norm_rope_kernel<T, kAppend, 4><<<grid_for(many, per_block, 16), kQrThreads, 0, st>>>(a);
-  else
-    qk_norm_rope_kernel<T, kAppend, 1><<<grid_for(a.M * heads, per_block, 16), kQrThreads, 0, st>>>(a);
+  switch (rows_lanes(a.D)) {
+    case 4: launch_rows<T, kAppend, 4>(a, st); break;
+    case 8: launch_rows<T, kAppend, 8>(a, st); break;
+    case 16: launch_rows<T, kAppend, 16>(a, st); break;
+    default: launch_rows<T, kAppend, 32>(a, st); break;
+  }
   return launch_status();
 }
 
 // CTAs of the backward (and rows of its partial sums): planned for 148 SMs.
 constexpr int kQrBackCtas = 148 * 2;
 int rows_back_grid(const bl_qkv_rows* r) {
-  int lanes = 1;
-  while (lanes < r->D / 8) lanes *= 2;
-  const int64_t g = ceil_div(r->M * (r->Hq + 2 * int64_t(r->Hkv)), int64_t(kQrThreads / lanes));
+  const int64_t g = ceil_div(r->M * (r->Hq + 2 * int64_t(r->Hkv)), int64_t(kQrThreads / rows_lanes(r->D)));
   return int(g < 1 ? 1 : g < kQrBackCtas ? g : kQrBackCtas);
 }
 
+// Two heads an item once that fills the SMs, one where latency counts.
+template <typename T, int kLanes>
+void launch_rows_back(const QrArgs& a, int grid, cudaStream_t st) {
+  constexpr int kPerBlock = kQrThreads / kLanes;
+  const int smem = kPerBlock * 2 * a.D * 4;            // at most 16 KB
+  if (a.M * ceil_div(a.Hq + 2 * int64_t(a.Hkv), 2) >= int64_t(grid) * kPerBlock * 2)
+    qk_norm_rope_backward_kernel<T, 2, kLanes><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
+  else
+    qk_norm_rope_backward_kernel<T, 1, kLanes><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
+}
 template <typename T>
-void launch_rows_back(const QrArgs& a, bool two, int grid, int smem, cudaStream_t st) {
-  if (two) qk_norm_rope_backward_kernel<T, 2><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
-  else qk_norm_rope_backward_kernel<T, 1><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
+void launch_norm_rope_back(const QrArgs& a, int grid, cudaStream_t st) {
+  switch (rows_lanes(a.D)) {
+    case 4: launch_rows_back<T, 4>(a, grid, st); break;
+    case 8: launch_rows_back<T, 8>(a, grid, st); break;
+    case 16: launch_rows_back<T, 16>(a, grid, st); break;
+    default: launch_rows_back<T, 32>(a, grid, st); break;
+  }
 }
 
 bl_status check_cache(const bl_kv_pages* c) {
@@ -357,12 +380,9 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
   a.lddq = lddq;
   a.lddk = lddk;
   a.lddv = lddv;
-  const int smem = (kQrThreads / a.lanes) * 2 * a.D * 4;       // at most 16 KB
-  // two heads an item once that fills the SMs, one where latency counts
-  const bool two = rows->M * ceil_div(rows->Hq + 2 * int64_t(rows->Hkv), 2) >= int64_t(grid) * (kQrThreads / a.lanes) * 2;
-  if (t == BL_T_F32) launch_rows_back<float>(a, two, grid, smem, stream);
-  else if (t == BL_T_F16) launch_rows_back<__half>(a, two, grid, smem, stream);
-  else launch_rows_back<__nv_bfloat16>(a, two, grid, smem, stream);
+  if (t == BL_T_F32) launch_norm_rope_back<float>(a, grid, stream);
+  else if (t == BL_T_F16) launch_norm_rope_back<__half>(a, grid, stream);
+  else launch_norm_rope_back<__nv_bfloat16>(a, grid, stream);
   if (a.part) gain_sum_kernel<<<unsigned(ceil_div(2 * a.D, 32)), 256, 0, stream>>>(a.part, grid, a.D, dgq, dgk);
   return launch_status();
 }

@@ -42,7 +42,6 @@ struct QrArgs {
   float *dxq, *dxk, *dxv;
   int64_t lddq, lddk, lddv;
   float* part;              // [grid, 2, D] partial gain gradients
-  int lanes;                // lanes per head: the power of two >= D / 8
 };
 
 __global__ void __launch_bounds__(256)
@@ -58,10 +57,35 @@ rope_table_kernel(float* __restrict__ table, int64_t P, int half, double base) {
   }
 }
 
-// Sum over the `lanes` (power of two) lanes that share a head.
-__device__ __forceinline__ float head_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sum over the kLanes lanes that share a head.
+template <int kLanes> __device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int o = kLanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+__device__ __forceinline__ float4 pick4(bool first, float4 a, float4 b) {
+  return make_float4(first ? a.x : b.x, first ? a.y : b.y, first ? a.z : b.z, first ? a.w : b.w);
+}
+// A head's columns in a lane, and the gains there (ones where there are none).
+struct QrLane {
+  bool on, turned;                  // holds elements; ... of rotated pairs
+  int u, lo, hi;                    // lane in the head; its two groups of four columns
+  float4 gq0, gq1, gk0, gk1;
+};
+__device__ __forceinline__ QrLane qr_lane(const QrArgs& a, int u) {
+  QrLane l;
+  l.u = u;
+  l.on = u < (a.D >> 3);
+  l.turned = l.on && u < (a.R >> 3);
+  const bool split = l.turned && !a.interleaved;
+  l.lo = l.on ? (split ? 4 * u : 8 * u) : 0;
+  l.hi = l.on ? (split ? (a.R >> 1) + 4 * u : 8 * u + 4) : 0;
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+  l.gq0 = a.gq ? *reinterpret_cast<const float4*>(a.gq + l.lo) : one;
+  l.gq1 = a.gq ? *reinterpret_cast<const float4*>(a.gq + l.hi) : one;
+  l.gk0 = a.gk ? *reinterpret_cast<const float4*>(a.gk + l.lo) : one;
+  l.gk1 = a.gk ? *reinterpret_cast<const float4*>(a.gk + l.hi) : one;
+  return l;
 }
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
@@ -95,21 +119,18 @@ __device__ __forceinline__ void rotate(float4& lo, float4& hi, float4 c, float4 
 
 // Item i of the work is a token and up to kHeads consecutive heads of its
 // Hq + 2 Hkv (queries, keys, values).
-template <typename T, bool kAppend, int kHeads>
+template <typename T, bool kAppend, int kHeads, int kLanes>
 __global__ void __launch_bounds__(kQrThreads)
 qk_norm_rope_kernel(const QrArgs a) {
-  const int lanes = a.lanes, u = threadIdx.x & (lanes - 1);
-  const int per_block = kQrThreads / lanes;
-  const int heads = a.Hq + 2 * a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
-  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * per_block;
-  const bool on = u < (a.D >> 3);                    // this lane holds elements
-  const bool turned = on && u < (a.R >> 3);          // ... of rotated pairs
-  const bool split = turned && !a.interleaved;
-  const int lo = on ? (split ? 4 * u : 8 * u) : 0, hi = on ? (split ? (a.R >> 1) + 4 * u : 8 * u + 4) : 0;
+  constexpr int kPerBlock = kQrThreads / kLanes;
+  const QrLane l = qr_lane(a, threadIdx.x & (kLanes - 1));
+  const int u = l.u, nk = a.Hq + a.Hkv, heads = nk + a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
+  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * kPerBlock;
   const float inv_d = 1.f / float(a.D);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false, range = false;
   // whole warps take every turn together: the shuffles need all lanes
-  const int64_t first = int64_t(blockIdx.x) * per_block, mine = threadIdx.x / lanes;
+  const int64_t first = int64_t(blockIdx.x) * kPerBlock, mine = threadIdx.x / kLanes;
   // the token, its position and slot are asked for an item ahead: the table's row follows the position
   int64_t m_next = 0, c_next = 0, p_next = 0, at_next = -1;
   auto ask = [&](int64_t i) {
@@ -124,69 +145,68 @@ qk_norm_rope_kernel(const QrArgs a) {
     const bool live = i < items;
     const int64_t m = m_next, p = p_next, at = at_next;
     const int h0 = int(c_next) * kHeads;
+    // head h's columns at row + h * D in each of the three
+    const float* rq = a.q + m * a.ldq;
+    const float* rk = a.k + m * a.ldk - int64_t(a.Hq) * a.D;
+    const float* rv = a.v + m * a.ldv - int64_t(nk) * a.D;
     float4 x[kHeads], y[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j;
-      x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!live || !on || h >= heads) continue;
-      const float* row = h < a.Hq ? a.q + m * a.ldq + int64_t(h) * a.D
-                         : h < a.Hq + a.Hkv ? a.k + m * a.ldk + int64_t(h - a.Hq) * a.D
-                                            : a.v + m * a.ldv + int64_t(h - a.Hq - a.Hkv) * a.D;
-      const bool value = h >= a.Hq + a.Hkv;
-      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (value ? 8 * u : lo)));
-      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (value ? 8 * u + 4 : hi)));
+      x[j] = y[j] = zero;
+      if (!live || !l.on || h >= heads) continue;
+      const float* row = (h < a.Hq ? rq : h < nk ? rk : rv) + h * a.D;
+      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (h < nk ? l.lo : 8 * u)));
+      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (h < nk ? l.hi : 8 * u + 4)));
     }
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
     if (live && !ok) range = true;
-    float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (turned && ok) {
+    float4 cs = zero, sn = zero;
+    if (l.turned && ok) {
       cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
       sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
     }
     ask(i + step);
-    int64_t page = 0, in = 0;
+    // head h's columns at out + h * D (a cache: h * page * D)
+    T* oq = static_cast<T*>(a.oq) + m * a.Hq * a.D;
+    T *ok_, *ov;
     bool store = true;
+    int stride = a.D;
     if (kAppend) {
       store = live && at >= 0 && at < a.nslots;
       if (live && at >= a.nslots) range = true;
+      int64_t page = 0, in = 0;
       split_index(store ? at : 0, a.page, a.nslots < (int64_t(1) << 31), page, in);
+      stride = a.page * a.D;
+      const int64_t to = page * a.Hkv * stride + in * a.D;
+      ok_ = static_cast<T*>(a.ok) + to - int64_t(a.Hq) * stride;
+      ov = static_cast<T*>(a.ov) + to - int64_t(nk) * stride;
+    } else {
+      ok_ = static_cast<T*>(a.ok) + (m * a.Hkv - a.Hq) * a.D;
+      ov = static_cast<T*>(a.ov) + (m * a.Hkv - nk) * a.D;
     }
+    float ss[kHeads];
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) ss[j] = head_sum<kLanes>(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)));
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j;
-      const float ss = head_sum(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)), lanes);
-      const bool value = h >= a.Hq + a.Hkv;
-      if (!live || h >= heads || !ok || !on) continue;
-      if (value) {
-        if (!(dot4(x[j], make_float4(0, 0, 0, 0), dot4(y[j], make_float4(0, 0, 0, 0), 0.f)) == 0.f)) bad = true;
-      } else {
-        if (!(ss <= 3.4028235e38f)) bad = true;
-        const float r = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
-        const float* g = h < a.Hq ? a.gq : a.gk;
-        x[j] = scale4(x[j], r);
-        y[j] = scale4(y[j], r);
-        if (g) {
-          x[j] = mul4(x[j], *reinterpret_cast<const float4*>(g + lo));
-          y[j] = mul4(y[j], *reinterpret_cast<const float4*>(g + hi));
-        }
-        if (turned) rotate(x[j], y[j], cs, sn, a.interleaved != 0);
+      if (!live || h >= heads || !ok || !l.on) continue;
+      if (!(ss[j] <= 3.4028235e38f)) bad = true;       // a sum of squares: not finite if an element is not
+      int c0 = 8 * u, c1 = 8 * u + 4;
+      if (h < nk) {
+        const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
+        const bool query = h < a.Hq;
+        x[j] = mul4(scale4(x[j], r), pick4(query, l.gq0, l.gk0));
+        y[j] = mul4(scale4(y[j], r), pick4(query, l.gq1, l.gk1));
+        if (l.turned) rotate(x[j], y[j], cs, sn, a.interleaved != 0);
+        c0 = l.lo;
+        c1 = l.hi;
       }
-      T* out;
-      if (h < a.Hq) {
-        out = static_cast<T*>(a.oq) + (m * a.Hq + h) * a.D;
-      } else {
-        const int hk = value ? h - a.Hq - a.Hkv : h - a.Hq;
-        T* o = static_cast<T*>(value ? a.ov : a.ok);
-        if (kAppend) {
-          if (!store) continue;
-          out = o + ((page * a.Hkv + hk) * a.page + in) * a.D;
-        } else {
-          out = o + (m * a.Hkv + hk) * a.D;
-        }
-      }
-      st4(out + (value ? 8 * u : lo), x[j]);
-      st4(out + (value ? 8 * u + 4 : hi), y[j]);
+      T* out = h < a.Hq ? oq + h * a.D : (h < nk ? ok_ : ov) + int64_t(h) * stride;
+      if (kAppend && h >= a.Hq && !store) continue;
+      st4(out + c0, x[j]);
+      st4(out + c1, y[j]);
     }
   }
   if (bad) raise_status(kDevNonFinite);
@@ -196,22 +216,17 @@ qk_norm_rope_kernel(const QrArgs a) {
 // The gradient.  A group of lanes keeps the same columns throughout, so the gains'
 // gradients stay in its registers until the end; then the CTA adds its groups in
 // order and writes one partial row, and gain_sum_kernel adds those in order.
-template <typename T, int kHeads>
+template <typename T, int kHeads, int kLanes>
 __global__ void __launch_bounds__(kQrThreads, 2)
 qk_norm_rope_backward_kernel(const QrArgs a) {
-  extern __shared__ float sums[];                    // [per_block, 2, D]
-  const int lanes = a.lanes, u = threadIdx.x & (lanes - 1), grp = threadIdx.x / lanes;
-  const int per_block = kQrThreads / lanes;
-  const int heads = a.Hq + 2 * a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
-  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * per_block;
-  const bool on = u < (a.D >> 3), turned = on && u < (a.R >> 3), split = turned && !a.interleaved;
-  const int lo = on ? (split ? 4 * u : 8 * u) : 0, hi = on ? (split ? (a.R >> 1) + 4 * u : 8 * u + 4) : 0;
+  extern __shared__ float sums[];                    // [kPerBlock, 2, D]
+  constexpr int kPerBlock = kQrThreads / kLanes;
+  const QrLane l = qr_lane(a, threadIdx.x & (kLanes - 1));
+  const int u = l.u, grp = threadIdx.x / kLanes;
+  const int nk = a.Hq + a.Hkv, heads = nk + a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
+  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * kPerBlock;
   const float inv_d = 1.f / float(a.D);
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f), one = make_float4(1.f, 1.f, 1.f, 1.f);
-  const float4 gq0 = a.gq ? *reinterpret_cast<const float4*>(a.gq + lo) : one;
-  const float4 gq1 = a.gq ? *reinterpret_cast<const float4*>(a.gq + hi) : one;
-  const float4 gk0 = a.gk ? *reinterpret_cast<const float4*>(a.gk + lo) : one;
-  const float4 gk1 = a.gk ? *reinterpret_cast<const float4*>(a.gk + hi) : one;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
   bool bad = false, range = false;
   int64_t m_next = 0, c_next = 0, p_next = 0;        // asked for an item ahead: the table's row follows the position
@@ -220,86 +235,97 @@ qk_norm_rope_backward_kernel(const QrArgs a) {
     split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
     p_next = a.R ? a.pos[m_next] : 0;
   };
-  ask(int64_t(blockIdx.x) * per_block + grp);
-  for (int64_t base = int64_t(blockIdx.x) * per_block; base < items; base += step) {
+  ask(int64_t(blockIdx.x) * kPerBlock + grp);
+  for (int64_t base = int64_t(blockIdx.x) * kPerBlock; base < items; base += step) {
     const int64_t i = base + grp;
     const bool live = i < items;
     const int64_t m = m_next, p = p_next;
     const int h0 = int(c_next) * kHeads;
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
     if (live && !ok) range = true;
-    const bool work = live && on && ok;
+    const bool work = live && l.on && ok;
+    const T* iq = static_cast<const T*>(a.dq) + m * a.Hq * a.D;
+    const T* ik = static_cast<const T*>(a.dk) + (m * a.Hkv - a.Hq) * a.D;
+    const T* iv = static_cast<const T*>(a.dv) + (m * a.Hkv - nk) * a.D;
+    const float* rq = a.q + m * a.ldq;
+    const float* rk = a.k + m * a.ldk - int64_t(a.Hq) * a.D;
     float4 x[kHeads], y[kHeads], e[kHeads], f[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j;
-      const bool value = h >= a.Hq + a.Hkv, query = h < a.Hq;
       x[j] = y[j] = e[j] = f[j] = zero;
       if (!work || h >= heads) continue;
-      const T* d = query ? static_cast<const T*>(a.dq) + (m * a.Hq + h) * a.D
-                         : static_cast<const T*>(value ? a.dv : a.dk) + (m * a.Hkv + (value ? h - a.Hq - a.Hkv : h - a.Hq)) * a.D;
-      e[j] = ld4(d + (value ? 8 * u : lo));
-      f[j] = ld4(d + (value ? 8 * u + 4 : hi));
-      if (value) continue;
-      const float* row = query ? a.q + m * a.ldq + int64_t(h) * a.D : a.k + m * a.ldk + int64_t(h - a.Hq) * a.D;
-      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + lo));
-      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + hi));
+      const T* d = (h < a.Hq ? iq : h < nk ? ik : iv) + h * a.D;
+      e[j] = ld4(d + (h < nk ? l.lo : 8 * u));
+      f[j] = ld4(d + (h < nk ? l.hi : 8 * u + 4));
+      if (h >= nk) continue;
+      const float* row = (h < a.Hq ? rq : rk) + h * a.D;
+      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + l.lo));
+      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + l.hi));
     }
-    float4 cs = one, sn = zero;
-    if (work && turned) {
+    float4 cs = zero, sn = zero;
+    if (work && l.turned) {
       cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
       sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
       sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
     }
     ask(i + step);
+    float* oq = a.dxq + m * a.lddq;
+    float* okk = a.dxk + m * a.lddk - int64_t(a.Hq) * a.D;
+    float* ov = a.dxv + m * a.lddv - int64_t(nk) * a.D;
+    // both sums of a head at once: sum x^2, and sum x g dy, of which mean(x g dy r) is r / D times
+    float ss[kHeads], tt[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j;
-      const bool value = h >= a.Hq + a.Hkv, query = h < a.Hq;
-      if (turned && !value) rotate(e[j], f[j], cs, sn, a.interleaved != 0);
-      const float ss = head_sum(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)), lanes);
-      const float r = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
-      x[j] = scale4(x[j], r);
-      y[j] = scale4(y[j], r);
-      const float4 px = mul4(e[j], x[j]), py = mul4(f[j], y[j]);          // dg terms
-      const float4 ge = mul4(e[j], query ? gq0 : gk0), gf = mul4(f[j], query ? gq1 : gk1);
-      const float t = head_sum(dot4(ge, x[j], dot4(gf, y[j], 0.f)), lanes) * inv_d;
+      if (l.turned && h < nk) rotate(e[j], f[j], cs, sn, a.interleaved != 0);
+      const bool query = h < a.Hq;
+      ss[j] = head_sum<kLanes>(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)));
+      tt[j] = head_sum<kLanes>(dot4(mul4(e[j], pick4(query, l.gq0, l.gk0)), x[j],
+                                    dot4(mul4(f[j], pick4(query, l.gq1, l.gk1)), y[j], 0.f)));
+    }
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+      const int h = h0 + j;
       if (!work || h >= heads) continue;
-      if (value) {
-        float* out = a.dxv + m * a.lddv + int64_t(h - a.Hq - a.Hkv) * a.D;
-        *reinterpret_cast<float4*>(out + 8 * u) = e[j];
-        *reinterpret_cast<float4*>(out + 8 * u + 4) = f[j];
+      if (h >= nk) {
+        float* out = ov + h * a.D + 8 * u;
+        *reinterpret_cast<float4*>(out) = e[j];
+        *reinterpret_cast<float4*>(out + 4) = f[j];
         continue;
       }
-      if (!(ss <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
-      float* out = query ? a.dxq + m * a.lddq + int64_t(h) * a.D : a.dxk + m * a.lddk + int64_t(h - a.Hq) * a.D;
-      *reinterpret_cast<float4*>(out + lo) = make_float4(r * fmaf(-x[j].x, t, ge.x), r * fmaf(-x[j].y, t, ge.y),
-                                                         r * fmaf(-x[j].z, t, ge.z), r * fmaf(-x[j].w, t, ge.w));
-      *reinterpret_cast<float4*>(out + hi) = make_float4(r * fmaf(-y[j].x, t, gf.x), r * fmaf(-y[j].y, t, gf.y),
-                                                         r * fmaf(-y[j].z, t, gf.z), r * fmaf(-y[j].w, t, gf.w));
-      if (query) {
-        sq0 = make_float4(sq0.x + px.x, sq0.y + px.y, sq0.z + px.z, sq0.w + px.w);
-        sq1 = make_float4(sq1.x + py.x, sq1.y + py.y, sq1.z + py.z, sq1.w + py.w);
-      } else {
-        sk0 = make_float4(sk0.x + px.x, sk0.y + px.y, sk0.z + px.z, sk0.w + px.w);
-        sk1 = make_float4(sk1.x + py.x, sk1.y + py.y, sk1.z + py.z, sk1.w + py.w);
-      }
+      const bool query = h < a.Hq;
+      const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
+      const float t = tt[j] * inv_d * r;
+      if (!(ss[j] <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
+      x[j] = scale4(x[j], r);
+      y[j] = scale4(y[j], r);
+      const float4 ge = mul4(e[j], pick4(query, l.gq0, l.gk0)), gf = mul4(f[j], pick4(query, l.gq1, l.gk1));
+      float* out = (query ? oq : okk) + h * a.D;
+      *reinterpret_cast<float4*>(out + l.lo) = make_float4(r * fmaf(-x[j].x, t, ge.x), r * fmaf(-x[j].y, t, ge.y),
+                                                           r * fmaf(-x[j].z, t, ge.z), r * fmaf(-x[j].w, t, ge.w));
+      *reinterpret_cast<float4*>(out + l.hi) = make_float4(r * fmaf(-y[j].x, t, gf.x), r * fmaf(-y[j].y, t, gf.y),
+                                                           r * fmaf(-y[j].z, t, gf.z), r * fmaf(-y[j].w, t, gf.w));
+      float4& s0 = query ? sq0 : sk0;
+      float4& s1 = query ? sq1 : sk1;
+      s0 = make_float4(fmaf(e[j].x, x[j].x, s0.x), fmaf(e[j].y, x[j].y, s0.y), fmaf(e[j].z, x[j].z, s0.z), fmaf(e[j].w, x[j].w, s0.w));
+      s1 = make_float4(fmaf(f[j].x, y[j].x, s1.x), fmaf(f[j].y, y[j].y, s1.y), fmaf(f[j].z, y[j].z, s1.z), fmaf(f[j].w, y[j].w, s1.w));
     }
   }
   if (bad) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
   if (!a.part) return;
-  if (on) {
-    float* s = sums + int64_t(grp) * 2 * a.D;
-    *reinterpret_cast<float4*>(s + lo) = sq0;
-    *reinterpret_cast<float4*>(s + hi) = sq1;
-    *reinterpret_cast<float4*>(s + a.D + lo) = sk0;
-    *reinterpret_cast<float4*>(s + a.D + hi) = sk1;
+  if (l.on) {
+    float* s = sums + grp * 2 * a.D;
+    *reinterpret_cast<float4*>(s + l.lo) = sq0;
+    *reinterpret_cast<float4*>(s + l.hi) = sq1;
+    *reinterpret_cast<float4*>(s + a.D + l.lo) = sk0;
+    *reinterpret_cast<float4*>(s + a.D + l.hi) = sk1;
   }
   __syncthreads();
   for (int d = threadIdx.x; d < 2 * a.D; d += kQrThreads) {
     float s = 0.f;
-    for (int j = 0; j < per_block; ++j) s += sums[j * 2 * a.D + d];
+    for (int j = 0; j < kPerBlock; ++j) s += sums[j * 2 * a.D + d];
     a.part[int64_t(blockIdx.x) * 2 * a.D + d] = s;
   }
 }

@@ -38,4 +38,12 @@ __device__ __forceinline__ bool load_seq(const AttnArgs& a, int b, Seq& s, bool 
   return ok;
 }
 
+// Bits of the columns u of 32 with u < n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Bits of the 32 columns from `first` on that are seen: u <= top and (u >= bot or u < lead).
+// One word and a bit test per column instead of three comparisons.
+__device__ __forceinline__ uint32_t seen_bits(int first, int top, int bot, int lead) {
+  return low_bits(top + 1 - first) & (~low_bits(bot - first) | low_bits(lead - first));
+}
+
 }  // namespace bl

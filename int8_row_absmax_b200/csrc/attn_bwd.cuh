@@ -120,11 +120,19 @@ attn_delta_kernel(const AttnArgs a, float* norms) {
       n = sum(n);
       if (n < INFINITY && n > top_v && seen_key(a, int(r / a.Hkv))) top_v = n;
     }
+    __shared__ float tops[2][8];
     top_o = warp_max(top_o);
     top_v = warp_max(top_v);
-    if ((threadIdx.x & 31) == 0) {                      // squares: not negative, so their bits are ordered
-      atomicMax(reinterpret_cast<unsigned int*>(norms), __float_as_uint(top_o));
-      atomicMax(reinterpret_cast<unsigned int*>(norms + 1), __float_as_uint(top_v));
+    if ((threadIdx.x & 31) == 0) {
+      tops[0][threadIdx.x >> 5] = top_o;
+      tops[1][threadIdx.x >> 5] = top_v;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {                              // squares: not negative, so their bits are ordered
+      float t = 0.f;
+      for (int w = 0; w < 8; ++w) t = fmaxf(t, tops[threadIdx.x][w]);
+      unsigned int* to = reinterpret_cast<unsigned int*>(norms) + threadIdx.x;
+      if (__float_as_uint(t) > *reinterpret_cast<volatile unsigned int*>(to)) atomicMax(to, __float_as_uint(t));
     }
   }
 }
@@ -370,8 +378,12 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
         const int bot = j - off - i0 - half * 64;
         const int top = a.window == 0 || j < a.sinks ? 128 : j + a.window - off - i0 - half * 64;
 #pragma unroll
-        for (int u = 0; u < 64; ++u)
-          if (u < bot || u >= top) p[u] = 0.f;
+        for (int b = 0; b < 64; b += 32) {
+          const uint32_t seen = low_bits(top - b) & ~low_bits(bot - b);
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if (!(seen & (1u << u))) p[b + u] = 0.f;
+        }
       }
 #pragma unroll
       for (int u = 0; u < 32; ++u) w[u] = pack2<T>(p[2 * u], p[2 * u + 1]);
@@ -603,8 +615,12 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       if (masked) {
         const int top = pos - j0 - half * 64, bot = lo - j0 - half * 64, lead = a.window ? a.sinks - j0 - half * 64 : 0;
 #pragma unroll
-        for (int u = 0; u < 64; ++u)
-          if (u > top || (u < bot && u >= lead)) p[u] = 0.f;
+        for (int b = 0; b < 64; b += 32) {
+          const uint32_t seen = seen_bits(b, top, bot, lead);
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if (!(seen & (1u << u))) p[b + u] = 0.f;
+        }
       }
       fine = mbar_wait_near(&dp_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {

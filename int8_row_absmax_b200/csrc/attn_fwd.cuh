@@ -303,8 +303,12 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
       if (j0 + 127 > r + off || (a.window != 0 && j0 <= min(r + 128, s.nq) - 1 + off - a.window && j0 + 128 > a.sinks)) {
         const int top = p - j0, bot = lo - j0, lead = a.window ? a.sinks - j0 : 0;
 #pragma unroll
-        for (int u = 0; u < 128; ++u)
-          if (u > top || (u < bot && u >= lead)) x[u] = -INFINITY;
+        for (int f = 0; f < 128; f += 32) {
+          const uint32_t seen = seen_bits(f, top, bot, lead);
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if (!(seen & (1u << u))) x[f + u] = -INFINITY;
+        }
       }
       float top4[4] = {x[0], x[1], x[2], x[3]};          // four chains: one would be 64 dependent steps
 #pragma unroll

@@ -38,7 +38,9 @@ struct alignas(64) AttnBwdMaps {
 template <int DP>
 struct AbCfg {
   static constexpr int kTile = 128 * DP * 2;
-  static constexpr int kDkvSmem = 6 * kTile + 2048 + 1024;   // K, V, two stages of Q and dO, lse and delta of each
+  // K, V, three stages of Q with the rows' lse, two of dO with delta, barriers: all but a few
+  // hundred bytes of an SM at D = 128, so nothing static and no room to align the base in
+  static constexpr int kDkvRows = 7 * kTile, kDkvBars = kDkvRows + 5 * 512, kDkvSmem = kDkvBars + 256;
   static constexpr int kDqSmem = 7 * kTile + 1024;           // Q, dO, three K, two V
 };
 
@@ -175,14 +177,24 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kAbThreads, 1)
 attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const float* norms) {
   using C = AbCfg<DP>;
-  extern __shared__ unsigned char ab_smem[];
-  __shared__ uint64_t kv_full, q_full[2], q_empty[2], g_full[2], g_empty[2], s_full, dp_full, p_ready, ds_ready, drain;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_err;
+  extern __shared__ __align__(1024) unsigned char dkv_smem[];
+  unsigned char* smem = dkv_smem;
+  const uint32_t base = smem_u32(smem);
+  float* lse_rows = reinterpret_cast<float*>(smem + C::kDkvRows);       // [3][128]
+  float* delta_rows = lse_rows + 3 * 128;                               // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kDkvBars);
+  uint64_t &kv_full = bars[0], &s_full = bars[1], &dp_full = bars[2], &ds_ready = bars[3], &drain = bars[4];
+  uint64_t *q_full = bars + 5, *q_empty = bars + 8, *g_full = bars + 11, *g_empty = bars + 13, *p_ready = bars + 15;
+  uint64_t* d_full = bars + 17;
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(bars + 19);
+  volatile int* err = reinterpret_cast<volatile int*>(bars + 20);
   constexpr int kBoxes = DP / 64;
-  volatile int* err = &s_err;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
+  if (base & 1023u) {                                                   // never, with nothing static before it
+    raise_status(kDevBadWorkspace);
+    return;
+  }
   // the work: key heads fastest, early key blocks (which most queries see) first
   const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
   const int j0 = rest / a.B * 128, group = a.Hq / a.Hkv;
@@ -199,21 +211,24 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   const int per = last < 0 || j0 - off > last ? 0 : last / 128 + 1 - first;   // blocks of one head
   const int n = per * group;
 
-  const uint32_t base = (smem_u32(ab_smem) + 1023u) & ~1023u;
-  unsigned char* smem = ab_smem + (base - smem_u32(ab_smem));
-  float* rows = reinterpret_cast<float*>(smem + 6 * C::kTile);          // [2 stages][lse, delta][128]
+  // tiles: K, V, three of Q, two of dO
+  auto q_tile = [&](int it) { return (2 + it % 3) * C::kTile; };
+  auto g_tile = [&](int it) { return (5 + (it & 1)) * C::kTile; };
   if (tid == 0) {
-    s_err = 0;
+    *err = 0;
     mbar_init(&kv_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&g_full[i], 1);
       mbar_init(&g_empty[i], 1);
+      mbar_init(&p_ready[i], 8);
+      mbar_init(&d_full[i], 1);
     }
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
-    mbar_init(&p_ready, 8);
     mbar_init(&ds_ready, 8);
     mbar_init(&drain, 1);
     fence_mbar_init();
@@ -225,7 +240,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                                         // S, dP, dV, dK: 128 columns each
+  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                 // S, dP, dV, dK: 128 columns each
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
@@ -233,7 +248,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       tma_rows(smem, &maps.k, kBoxes, hk, s.k0 + j0, &kv_full);
       tma_rows(smem + C::kTile, &maps.v, kBoxes, hk, s.k0 + j0, &kv_full);
     }
-    // a block's lse and delta are asked for while the block before waits for its stage
+    // a block's lse and delta are asked for while the block before waits for its places
     float l[4], e[4];
     auto ask = [&](int it) {
       const int h = hk * group + it / per, i0 = (first + it % per) * 128;
@@ -248,34 +263,39 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     if (n > 0) ask(0);
     int it = 0;
     for (; it < n; ++it) {
-      const int st = it & 1, h = hk * group + it / per, i0 = (first + it % per) * 128;
-      unsigned char* q = smem + (2 + 2 * st) * C::kTile;
-      // dO's place is free before Q's: after dV, not after dK of two blocks ago
-      if (it >= 2 && !mbar_wait_near(&g_empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+      const int qs = it % 3, gs = it & 1, h = hk * group + it / per, i0 = (first + it % per) * 128;
+      // places come free in this order: Q's (and lse's) after dK of three blocks ago, dO's after dV of two
+      // blocks ago, delta's, which is read after that, after dK of two blocks ago
+      if (it >= 3 && !mbar_wait_near(&q_empty[qs], uint32_t(it / 3 - 1) & 1u)) *err = 1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        lse_rows[qs * 128 + lane + 32 * u] = l[u] == -INFINITY ? kNoRow : fmaf(l[u], kLog2e, -p_scale_log2<T>());
+      __syncwarp();
       if (__any_sync(0xffffffffu, *err)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&g_full[st], C::kTile);
-        tma_rows(q + C::kTile, &maps.dout, kBoxes, h, s.q0 + i0, &g_full[st]);
+        mbar_arrive_expect_tx(&q_full[qs], C::kTile);
+        tma_rows(smem + q_tile(it), &maps.q, kBoxes, h, s.q0 + i0, &q_full[qs]);
       }
-      if (it >= 2 && !mbar_wait_near(&q_empty[st], uint32_t(it / 2 - 1) & 1u)) *err = 1;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        rows[st * 256 + lane + 32 * u] = l[u] == -INFINITY ? kNoRow : fmaf(l[u], kLog2e, -p_scale_log2<T>());
-        rows[st * 256 + 128 + lane + 32 * u] = e[u];
+      if (it >= 2 && !mbar_wait_near(&g_empty[gs], uint32_t(it / 2 - 1) & 1u)) *err = 1;
+      if (__any_sync(0xffffffffu, *err)) {
+        ++it;
+        break;
       }
-      __syncwarp();
       if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[st], C::kTile);
-        tma_rows(q, &maps.q, kBoxes, h, s.q0 + i0, &q_full[st]);
+        mbar_arrive_expect_tx(&g_full[gs], C::kTile);
+        tma_rows(smem + g_tile(it), &maps.dout, kBoxes, h, s.q0 + i0, &g_full[gs]);
       }
+      if (it >= 2 && !mbar_wait_near(&q_empty[(it - 2) % 3], uint32_t((it - 2) / 3) & 1u)) *err = 1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) delta_rows[gs * 128 + lane + 32 * u] = e[u];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_full[gs]);
       if (it + 1 < n) ask(it + 1);
     }
     if (*err && n > 0) {                                                // leave no copy in flight behind
       mbar_wait_near(&kv_full, 0u);
-      for (int i = max(0, it - 2); i < it; ++i) {
-        mbar_wait_near(&q_full[i & 1], uint32_t(i / 2) & 1u);
-        mbar_wait_near(&g_full[i & 1], uint32_t(i / 2) & 1u);
-      }
+      for (int i = max(0, it - 3); i < it; ++i) mbar_wait_near(&q_full[i % 3], uint32_t(i / 3) & 1u);
+      for (int i = max(0, it - 2); i < it; ++i) mbar_wait_near(&g_full[i & 1], uint32_t(i / 2) & 1u);
     }
   } else if (warp == 8) {
     bool good = true;                                                   // the same in every lane
@@ -287,56 +307,60 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       tc_fence_after();
     };
     const uint32_t S = tmem, dP = tmem + 128, dV = tmem + 256, dK = tmem + 384;
-    auto q_at = [&](int it) { return base + uint32_t((2 + 2 * (it & 1)) * C::kTile); };
     // rows of no query of the sequence must not meet P's and dS's zeros
     auto trim = [&](unsigned char* tile, int it) {
       const int i0 = (first + it % per) * 128;
       if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) zero_rows(tile, kBoxes, s.nq - i0, 128, lane);
     };
     auto wait_q = [&](int it) {
-      wait(&q_full[it & 1], it / 2);
-      trim(smem + (2 + 2 * (it & 1)) * C::kTile, it);
+      wait(&q_full[it % 3], it / 3);
+      trim(smem + q_tile(it), it);
     };
     auto wait_g = [&](int it) {
       wait(&g_full[it & 1], it / 2);
-      trim(smem + (3 + 2 * (it & 1)) * C::kTile, it);
+      trim(smem + g_tile(it), it);
     };
     if (n > 0) {
       wait(&kv_full, 0);
       wait_q(0);
       if (good) {
-        mma_qk<T, DP>(S, base, q_at(0));
+        mma_qk<T, DP>(S, base, base + q_tile(0));
         umma_commit_warp(&s_full);
       }
       wait_g(0);
       if (good) {
-        mma_qk<T, DP>(dP, base + C::kTile, q_at(0) + C::kTile);
+        mma_qk<T, DP>(dP, base + C::kTile, base + g_tile(0));
         umma_commit_warp(&dp_full);
       }
     }
     for (int it = 0; it < n && good; ++it) {
       const bool more = it + 1 < n;
-      wait(&p_ready, it);
-      if (good) {
-        mma_pv_halves<T, DP>(dV, S, q_at(it) + C::kTile, it > 0);
-        umma_commit_warp(&g_empty[it & 1]);
+      // P comes in two parts: columns 0..31 of each half, then 32..63
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        wait(&p_ready[part], it);
+        if (good) {
+          mma_pv_part<T, DP, 32>(dV, S + part * 16, base + g_tile(it) + part * 4096, it > 0 || part > 0);
+          mma_pv_part<T, DP, 32>(dV, S + 64 + part * 16, base + g_tile(it) + 8192 + part * 4096, true);
+        }
       }
+      if (good) umma_commit_warp(&g_empty[it & 1]);
       if (more) {
         wait_q(it + 1);
         if (good) {
-          mma_qk<T, DP>(S, base, q_at(it + 1));                         // in order behind the product that reads P
+          mma_qk<T, DP>(S, base, base + q_tile(it + 1));                  // in order behind the product that reads P
           umma_commit_warp(&s_full);
         }
       }
       wait(&ds_ready, it);
       if (good) {
-        mma_pv_halves<T, DP>(dK, dP, q_at(it), it > 0);
-        umma_commit_warp(&q_empty[it & 1]);
+        mma_pv_halves<T, DP>(dK, dP, base + q_tile(it), it > 0);
+        umma_commit_warp(&q_empty[it % 3]);
       }
       if (more) {
         wait_g(it + 1);
         if (good) {
-          mma_qk<T, DP>(dP, base + C::kTile, q_at(it + 1) + C::kTile);
+          mma_qk<T, DP>(dP, base + C::kTile, base + g_tile(it + 1));
           umma_commit_warp(&dp_full);
         }
       }
@@ -351,9 +375,9 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     bool fine = true;
     for (int it = 0; it < n; ++it) {
       const int i0 = (first + it % per) * 128;
-      const float4* lse = reinterpret_cast<const float4*>(rows + (it & 1) * 256 + half * 64);
-      const float4* del = lse + 32;
-      fine = mbar_wait_near(&q_full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait_near(&s_full, uint32_t(it) & 1u) && !*err;
+      const float4* lse = reinterpret_cast<const float4*>(lse_rows + it % 3 * 128 + half * 64);
+      const float4* del = reinterpret_cast<const float4*>(delta_rows + (it & 1) * 128 + half * 64);
+      fine = mbar_wait_near(&q_full[it % 3], uint32_t(it / 3) & 1u) && mbar_wait_near(&s_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -364,36 +388,37 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
       tmem_ld32(S, reinterpret_cast<uint32_t*>(p));
       tmem_ld32(S + 32, reinterpret_cast<uint32_t*>(p) + 32);
       tmem_ld_wait();
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        const float4 l = lse[u];
-        p[4 * u] = exp2_approx(fmaf(p[4 * u], c, -l.x));
-        p[4 * u + 1] = exp2_approx(fmaf(p[4 * u + 1], c, -l.y));
-        p[4 * u + 2] = exp2_approx(fmaf(p[4 * u + 2], c, -l.z));
-        p[4 * u + 3] = exp2_approx(fmaf(p[4 * u + 3], c, -l.w));
-      }
       // some key of the block is not seen by some query of the block
       const bool masked = i0 + off < j0 + 127 || (a.window != 0 && i0 + 127 + off >= j0 + a.window && j0 + 128 > a.sinks);
-      if (masked) {
-        const int bot = j - off - i0 - half * 64;
-        const int top = a.window == 0 || j < a.sinks ? 128 : j + a.window - off - i0 - half * 64;
+      const int bot = j - off - i0 - half * 64;
+      const int top = a.window == 0 || j < a.sinks ? 128 : j + a.window - off - i0 - half * 64;
 #pragma unroll
-        for (int b = 0; b < 64; b += 32) {
-          const uint32_t seen = low_bits(top - b) & ~low_bits(bot - b);
+      for (int part = 0; part < 2; ++part) {
+        float* pp = p + part * 32;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float4 l = lse[part * 8 + u];
+          pp[4 * u] = exp2_approx(fmaf(pp[4 * u], c, -l.x));
+          pp[4 * u + 1] = exp2_approx(fmaf(pp[4 * u + 1], c, -l.y));
+          pp[4 * u + 2] = exp2_approx(fmaf(pp[4 * u + 2], c, -l.z));
+          pp[4 * u + 3] = exp2_approx(fmaf(pp[4 * u + 3], c, -l.w));
+        }
+        if (masked) {
+          const uint32_t seen = low_bits(top - part * 32) & ~low_bits(bot - part * 32);
 #pragma unroll
           for (int u = 0; u < 32; ++u)
-            if (!(seen & (1u << u))) p[b + u] = 0.f;
+            if (!(seen & (1u << u))) pp[u] = 0.f;
         }
-      }
 #pragma unroll
-      for (int u = 0; u < 32; ++u) w[u] = pack2<T>(p[2 * u], p[2 * u + 1]);
-      tmem_st32(S, w);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready);
+        for (int u = 0; u < 16; ++u) w[part * 16 + u] = pack2<T>(pp[2 * u], pp[2 * u + 1]);
+        tmem_st16(S + part * 16, w + part * 16);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[part]);
+      }
 
-      fine = mbar_wait_near(&dp_full, uint32_t(it) & 1u) && !*err;
+      fine = mbar_wait_near(&d_full[it & 1], uint32_t(it / 2) & 1u) && mbar_wait_near(&dp_full, uint32_t(it) & 1u) && !*err;
       if (__any_sync(0xffffffffu, !fine)) {
         *err = 1;
         break;
@@ -505,7 +530,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                                         // S0, S1, dP, dQ: 128 columns each
+  const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                 // S0, S1, dP, dQ: 128 columns each
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {

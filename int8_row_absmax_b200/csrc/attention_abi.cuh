@@ -83,27 +83,33 @@ QrArgs rows_args(const bl_qkv_rows* r) {
 // Lanes that share a head: the power of two from 4 to 32 that covers D / 8.
 int rows_lanes(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// Four heads an item once that still fills the SMs (eight loads in flight a
-// thread), one head an item below, where latency counts.
+// The ring kernel once its items fill the SMs' warps twice, the one of single heads
+// below, where latency counts.
 template <typename T, bool kAppend, int kLanes>
-void launch_rows(const QrArgs& a, cudaStream_t st) {
+bl_status launch_rows(const QrArgs& a, cudaStream_t st) {
   constexpr int kPerBlock = kQrThreads / kLanes;
   const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t many = a.M * ceil_div(heads, 4);
-  if (many >= int64_t(num_sms()) * 4 * kPerBlock)
-    qk_norm_rope_kernel<T, kAppend, 4, kLanes><<<grid_for(many, kPerBlock, 16), kQrThreads, 0, st>>>(a);
-  else
+  const int64_t items = a.M * ceil_div(heads, kQrRingHeads);
+  if (items >= int64_t(num_sms()) * 4 * kQrRingWarps) {
+    static std::atomic<uint64_t> done{0};
+    const int most = kQrRingWarps * kQrRing * kQrRingHeads * 8 * kLanes * 4, smem = most / (8 * kLanes) * a.D;
+    if (!allow_smem(qk_norm_rope_ring_kernel<T, kAppend, kLanes>, most, done)) return BL_ERR_CUDA;
+    const int64_t per_sm = 220 * 1024 / smem;
+    const int64_t cap = int64_t(num_sms()) * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm), grid = ceil_div(items, kQrRingWarps);
+    qk_norm_rope_ring_kernel<T, kAppend, kLanes><<<unsigned(grid < cap ? grid : cap), 32 * kQrRingWarps, smem, st>>>(a);
+  } else {
     qk_norm_rope_kernel<T, kAppend, 1, kLanes><<<grid_for(a.M * heads, kPerBlock, 16), kQrThreads, 0, st>>>(a);
+  }
+  return launch_status();
 }
 template <typename T, bool kAppend>
 bl_status launch_norm_rope(const QrArgs& a, cudaStream_t st) {
   switch (rows_lanes(a.D)) {
-    case 4: launch_rows<T, kAppend, 4>(a, st); break;
-    case 8: launch_rows<T, kAppend, 8>(a, st); break;
-    case 16: launch_rows<T, kAppend, 16>(a, st); break;
-    default: launch_rows<T, kAppend, 32>(a, st); break;
+    case 4: return launch_rows<T, kAppend, 4>(a, st);
+    case 8: return launch_rows<T, kAppend, 8>(a, st);
+    case 16: return launch_rows<T, kAppend, 16>(a, st);
+    default: return launch_rows<T, kAppend, 32>(a, st);
   }
-  return launch_status();
 }
 
 // CTAs of the backward (and rows of its partial sums): planned for 148 SMs.
@@ -225,8 +231,25 @@ bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
   return a.D <= 64 ? launch_attn_fwd<T, 64>(a, st) : launch_attn_fwd<T, 128>(a, st);
 }
 
-// The backward's workspace: the two norms (float16), then delta [Hq, Tq].
+// The backward's workspace: the two norms (float16), delta [Hq, Tq], the parts of dK and dV.
 constexpr size_t kAbNormBytes = 256;
+
+// CTAs that share the query heads of one key block: one as soon as the key blocks fill
+// B200's 148 SMs, else as many as fill them twice (5 sequences of up to 777 tokens, 6/2
+// heads of 80: dK/dV 50 -> 24 us with the join; 2 x 4096 tokens, 20/5 heads of 128, where
+// the parts would cost more than the evener load gives: not split).
+int dkv_splits(const bl_attn_call* c) {
+  const int group = c->Hq / c->Hkv;
+  const int64_t ctas = int64_t(c->Hkv) * c->B * ceil_div(c->max_k, 128);
+  if (ctas < 1 || ctas >= 148) return 1;
+  const int64_t want = 296 / ctas < group ? 296 / ctas : group;
+  const int64_t heads = ceil_div(group, want);
+  return int(ceil_div(group, heads));
+}
+size_t dkv_part_bytes(const bl_attn_call* c) {
+  const int splits = dkv_splits(c);
+  return splits > 1 ? align_up(size_t(splits) * 2 * size_t(c->Tk) * size_t(c->Hkv) * size_t(c->D) * 4) : 0;
+}
 
 template <typename T, int DP>
 bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
@@ -246,14 +269,17 @@ bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
       !allow_smem(attn_dq_kernel<T, DP>, AbCfg<DP>::kDqSmem, done_q))
     return BL_ERR_CUDA;
   const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
-  if (!int32_max(gq) || !int32_max(gk)) return BL_ERR_UNSUPPORTED;
+  if (!int32_max(gq) || !int32_max(gk * a.splits)) return BL_ERR_UNSUPPORTED;
   if (f16 && cudaMemsetAsync(norms, 0, 8, st) != cudaSuccess) return BL_ERR_CUDA;
   if (queries) {
     const int64_t rows = a.Tq * a.Hq;
     attn_delta_kernel<T, DP><<<grid_for(rows, 256 / (DP / 8), 8), 256, 0, st>>>(a, norms);
   }
   if (queries && gq > 0) attn_dq_kernel<T, DP><<<unsigned(gq), kAbThreads, AbCfg<DP>::kDqSmem, st>>>(maps, a, norms);
-  if (keys && gk > 0) attn_dkv_kernel<T, DP><<<unsigned(gk), kAbThreads, AbCfg<DP>::kDkvSmem, st>>>(maps, a, norms);
+  if (keys && gk > 0) {
+    attn_dkv_kernel<T, DP><<<unsigned(gk * a.splits), kAbThreads, AbCfg<DP>::kDkvSmem, st>>>(maps, a, norms);
+    if (a.splits > 1) attn_dkv_join_kernel<T><<<dim3(unsigned(gk), 8), 256, 0, st>>>(a);
+  }
   return launch_status();
 }
 template <typename T>
@@ -401,7 +427,7 @@ bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStre
 
 size_t bl_attention_backward_workspace_size(const bl_attn_call* call) {
   if (check_attn(call) != BL_OK || call->B == 0) return 0;
-  return kAbNormBytes + align_up(size_t(call->Tq) * size_t(call->Hq) * 4);
+  return kAbNormBytes + align_up(size_t(call->Tq) * size_t(call->Hq) * 4) + dkv_part_bytes(call);
 }
 
 bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
@@ -424,6 +450,9 @@ bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const
   a.dv = dv;
   float* norms = static_cast<float*>(ws);
   a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + kAbNormBytes);
+  a.splits = dkv_splits(call);
+  a.split_heads = int(ceil_div(call->Hq / call->Hkv, a.splits));
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kAbNormBytes + align_up(size_t(call->Tq) * size_t(call->Hq) * 4));
   return call->t == BL_T_F16 ? run_attn_backward<__half>(a, norms, stream)
                              : run_attn_backward<__nv_bfloat16>(a, norms, stream);
 }

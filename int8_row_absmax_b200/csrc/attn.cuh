@@ -20,6 +20,8 @@ struct AttnArgs {
   const void *dout, *o;
   float* delta;
   void *dq, *dk, *dv;
+  int splits, split_heads;    // dK/dV: CTAs that share a key block's query heads, heads of each
+  float* part;                // [splits][dK, dV][Tk, Hkv, D], where splits > 1
 };
 
 struct Seq {

@@ -8,7 +8,9 @@
 //     them, for each head of the group, with the transposed products (keys are the rows):
 //     S^T = K Q^T and dP^T = V dO^T into tensor memory, P^T and dS^T written back over
 //     them in the inputs' type, dV += P^T dO and dK += dS^T Q with the accumulators in
-//     tensor memory throughout: 4 matrix products a block;
+//     tensor memory throughout: 4 matrix products a block.  Where that leaves SMs idle, a
+//     group's heads are shared out over several CTAs, whose float32 parts
+//     attn_dkv_join_kernel adds in order;
 //   attn_dq_kernel    one CTA per 128 queries of a head; S, dP, dQ += dS K: 3 products.
 // Seven products for the formula's five: recomputing S and dP costs 40% more matrix work
 // than one kernel would, whose dQ would have to be summed across CTAs (atomics in float32,
@@ -147,6 +149,54 @@ __device__ __forceinline__ void mma_pv_halves(uint32_t d, uint32_t p, uint32_t b
   mma_pv_part<T, DP, 64>(d, p + 64, b + 8192, true);
 }
 
+// A row of an accumulator, times f, to float32 memory.
+template <int DP>
+__device__ __forceinline__ void store_row_f32(uint32_t taddr, float* out, int D, float f, bool store, bool zero) {
+#pragma unroll 1
+  for (int u = 0; u < DP / 32; ++u) {
+    uint32_t o[32];
+    __syncwarp();
+    tmem_ld32(taddr + u * 32, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      if (!store || u * 32 + e >= D) break;
+      const float4 y = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f, __uint_as_float(o[e + 2]) * f,
+                                   __uint_as_float(o[e + 3]) * f);
+      *reinterpret_cast<float4*>(out + u * 32 + e) = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : y;
+    }
+  }
+}
+
+// dK and dV from the parts of the CTAs that shared a key block's query heads, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+attn_dkv_join_kernel(const AttnArgs a) {
+  const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
+  const int j0 = rest / a.B * 128;
+  Seq s;
+  if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) return;
+  // 16 rows a CTA: 32 lanes a row (one quad each at D = 128), 8 rows at a time
+  const int64_t one = a.Tk * a.Hkv * a.D;
+  const int c = threadIdx.x & 31;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int which = i & 1, r = j0 + int(blockIdx.y) * 16 + (i >> 1) * 8 + (threadIdx.x >> 5);
+    if (r >= s.nk || 4 * c >= a.D) continue;
+    const int64_t at = (int64_t(s.k0 + r) * a.Hkv + hk) * a.D + 4 * c;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) {
+      const float4 x = *reinterpret_cast<const float4*>(a.part + (2 * z + which) * one + at);
+      y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+    }
+    if (!(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY)) bad = true;
+    st4(static_cast<T*>(which ? a.dv : a.dk) + at, y);
+  }
+  if (bad) raise_status(kDevNonFinite);
+}
+
 // A row of an accumulator, times f, to 16-bit memory (D elements); false if not finite.
 template <typename T, int DP>
 __device__ __forceinline__ bool store_row(uint32_t taddr, T* out, int D, float f, bool store, bool zero) {
@@ -195,9 +245,10 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     raise_status(kDevBadWorkspace);
     return;
   }
-  // the work: key heads fastest, early key blocks (which most queries see) first
-  const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
-  const int j0 = rest / a.B * 128, group = a.Hq / a.Hkv;
+  // the work: parts of a group's heads and key heads fastest, early key blocks (which most queries see) first
+  const int unit = int(blockIdx.x % unsigned(a.Hkv * a.splits)), rest = int(blockIdx.x / unsigned(a.Hkv * a.splits));
+  const int hk = unit / a.splits, z = unit - hk * a.splits, group = a.Hq / a.Hkv;
+  const int j0 = rest / a.B * 128, h0 = hk * group + z * a.split_heads, heads = min(a.split_heads, group - z * a.split_heads);
   Seq s;
   if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) return;
   s.q0 = uniform(s.q0);
@@ -209,7 +260,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   const int first = max(0, j0 - off) / 128;
   const int last = a.window == 0 || j0 < a.sinks ? s.nq - 1 : min(s.nq - 1, j0 + 126 + a.window - off);
   const int per = last < 0 || j0 - off > last ? 0 : last / 128 + 1 - first;   // blocks of one head
-  const int n = per * group;
+  const int n = per * heads;
 
   // tiles: K, V, three of Q, two of dO
   auto q_tile = [&](int it) { return (2 + it % 3) * C::kTile; };
@@ -251,7 +302,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     // a block's lse and delta are asked for while the block before waits for its places
     float l[4], e[4];
     auto ask = [&](int it) {
-      const int h = hk * group + it / per, i0 = (first + it % per) * 128;
+      const int h = h0 + it / per, i0 = (first + it % per) * 128;
       const int64_t at = int64_t(h) * a.Tq + s.q0 + i0 + lane;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -263,7 +314,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     if (n > 0) ask(0);
     int it = 0;
     for (; it < n; ++it) {
-      const int qs = it % 3, gs = it & 1, h = hk * group + it / per, i0 = (first + it % per) * 128;
+      const int qs = it % 3, gs = it & 1, h = h0 + it / per, i0 = (first + it % per) * 128;
       // places come free in this order: Q's (and lse's) after dK of three blocks ago, dO's after dV of two
       // blocks ago, delta's, which is read after that, after dK of two blocks ago
       if (it >= 3 && !mbar_wait_near(&q_empty[qs], uint32_t(it / 3 - 1) & 1u)) *err = 1;
@@ -468,8 +519,11 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const bool keys = warp >= 4;
     const uint32_t acc = tmem + (uint32_t((warp & 3) * 32) << 16) + (keys ? 384 : 256);
     const float f = keys ? a.scale / ds_scale<T>(norms) : exp2f(-p_scale_log2<T>());
-    T* out = static_cast<T*>(keys ? a.dk : a.dv) + (int64_t(s.k0 + j) * a.Hkv + hk) * a.D;
-    if (!store_row<T, DP>(acc, out, a.D, f, j < s.nk, n == 0) && j < s.nk) raise_status(kDevNonFinite);
+    const int64_t at = (int64_t(s.k0 + j) * a.Hkv + hk) * a.D;
+    T* out = static_cast<T*>(keys ? a.dk : a.dv) + at;
+    if (a.splits > 1)
+      store_row_f32<DP>(acc, a.part + (2 * z + (keys ? 0 : 1)) * (a.Tk * a.Hkv * a.D) + at, a.D, f, j < s.nk, n == 0);
+    else if (!store_row<T, DP>(acc, out, a.D, f, j < s.nk, n == 0) && j < s.nk) raise_status(kDevNonFinite);
   }
   tc_fence_before();
   __syncthreads();

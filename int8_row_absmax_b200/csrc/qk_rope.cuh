@@ -117,8 +117,8 @@ __device__ __forceinline__ void rotate(float4& lo, float4& hi, float4 c, float4 
   }
 }
 
-// Item i of the work is a token and up to kHeads consecutive heads of its
-// Hq + 2 Hkv (queries, keys, values).
+// Few rows, where latency counts.  Item i of the work is a token and one of its Hq + 2 Hkv
+// heads (queries, keys, values).
 template <typename T, bool kAppend, int kHeads, int kLanes>
 __global__ void __launch_bounds__(kQrThreads)
 qk_norm_rope_kernel(const QrArgs a) {
@@ -207,6 +207,125 @@ qk_norm_rope_kernel(const QrArgs a) {
       if (kAppend && h >= a.Hq && !store) continue;
       st4(out + c0, x[j]);
       st4(out + c1, y[j]);
+    }
+  }
+  if (bad) raise_status(kDevNonFinite);
+  if (range) raise_status(kDevRange);
+}
+
+// The same for many rows, fed by the copy engine: each warp keeps three items of
+// kRingHeads heads of a token in shared memory (bulk copies of whole runs of heads, two
+// ahead of its work), so that 128 KB an SM are on their way whatever the registers allow.
+constexpr int kQrRing = 3, kQrRingHeads = 8, kQrRingWarps = 8;
+
+template <typename T, bool kAppend, int kLanes>
+__global__ void __launch_bounds__(32 * kQrRingWarps, 2)
+qk_norm_rope_ring_kernel(const QrArgs a) {
+  extern __shared__ __align__(128) unsigned char qr_smem[];
+  __shared__ uint64_t full[kQrRingWarps][kQrRing];
+  constexpr int kAtOnce = 32 / kLanes;                 // heads that the warp works on at a time
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const QrLane l = qr_lane(a, lane & (kLanes - 1));
+  const int u = l.u, nk = a.Hq + a.Hkv, heads = nk + a.Hkv, chunks = (heads + kQrRingHeads - 1) / kQrRingHeads;
+  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * kQrRingWarps;
+  const int64_t first = int64_t(blockIdx.x) * kQrRingWarps + warp;
+  const float inv_d = 1.f / float(a.D);
+  float* ring = reinterpret_cast<float*>(qr_smem) + warp * kQrRing * kQrRingHeads * a.D;
+  if (lane == 0) {
+    for (int i = 0; i < kQrRing; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  auto issue = [&](int64_t i, int st) {                // lane 0: the heads of item i, a run from each of q, k, v
+    int64_t m, c;
+    split_index(i, chunks, items < (int64_t(1) << 31), m, c);
+    const int h0 = int(c) * kQrRingHeads, h1 = min(h0 + kQrRingHeads, heads);
+    float* to = ring + st * kQrRingHeads * a.D;
+    mbar_arrive_expect_tx(&full[warp][st], uint32_t((h1 - h0) * a.D * 4));
+    auto run = [&](int lo, int hi, const float* row, int base) {
+      lo = max(lo, h0);
+      hi = min(hi, h1);
+      if (lo < hi) bulk_g2s(to + (lo - h0) * a.D, row + int64_t(lo - base) * a.D, uint32_t((hi - lo) * a.D * 4), &full[warp][st]);
+    };
+    run(0, a.Hq, a.q + m * a.ldq, 0);
+    run(a.Hq, nk, a.k + m * a.ldk, a.Hq);
+    run(nk, heads, a.v + m * a.ldv, nk);
+  };
+  bool bad = false, range = false;
+  int64_t m_next = 0, c_next = 0, p_next = 0, at_next = -1;
+  auto ask = [&](int64_t i) {
+    if (i >= items) return;
+    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
+    p_next = a.R ? a.pos[m_next] : 0;
+    if (kAppend) at_next = a.slots[m_next];
+  };
+  if (lane == 0)
+    for (int k = 0; k < kQrRing - 1; ++k)
+      if (first + k * step < items) issue(first + k * step, k);
+  ask(first);
+  int n = 0;
+  for (int64_t i = first; i < items; i += step, ++n) {
+    const int st = n % kQrRing;
+    const int64_t m = m_next, p = p_next, at = at_next;
+    const int h0 = int(c_next) * kQrRingHeads;
+    __syncwarp();                                      // the item before has been read: its place takes the next copy
+    if (lane == 0 && i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
+    const bool ok = p >= 0 && (a.R == 0 || p < a.P);
+    if (!ok) range = true;
+    float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), sn = cs;
+    if (l.turned && ok) {
+      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
+      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
+    }
+    ask(i + step);
+    T* oq = static_cast<T*>(a.oq) + m * a.Hq * a.D;
+    T *ok_, *ov;
+    bool store = true;
+    int stride = a.D;
+    if (kAppend) {
+      store = at >= 0 && at < a.nslots;
+      if (at >= a.nslots) range = true;
+      int64_t page = 0, in = 0;
+      split_index(store ? at : 0, a.page, a.nslots < (int64_t(1) << 31), page, in);
+      stride = a.page * a.D;
+      const int64_t to = page * a.Hkv * stride + in * a.D;
+      ok_ = static_cast<T*>(a.ok) + to - int64_t(a.Hq) * stride;
+      ov = static_cast<T*>(a.ov) + to - int64_t(nk) * stride;
+    } else {
+      ok_ = static_cast<T*>(a.ok) + (m * a.Hkv - a.Hq) * a.D;
+      ov = static_cast<T*>(a.ov) + (m * a.Hkv - nk) * a.D;
+    }
+    if (__any_sync(0xffffffffu, !mbar_wait_near(&full[warp][st], uint32_t(n / kQrRing) & 1u))) {
+      if (lane == 0) raise_status(kDevTimeout);        // and no copy left in flight
+      for (int k = 1; k < kQrRing; ++k)
+        if (i + k * step < items) mbar_wait(&full[warp][(n + k) % kQrRing], uint32_t((n + k) / kQrRing) & 1u);
+      break;
+    }
+    const float* rows = ring + st * kQrRingHeads * a.D;
+#pragma unroll
+    for (int b = 0; b < kQrRingHeads; b += kAtOnce) {
+      const int slot = b + lane / kLanes, h = h0 + slot;
+      const bool live = h < heads && l.on, value = h >= nk;
+      const int c0 = value ? 8 * u : l.lo, c1 = value ? 8 * u + 4 : l.hi;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (live) {
+        x = *reinterpret_cast<const float4*>(rows + slot * a.D + c0);
+        y = *reinterpret_cast<const float4*>(rows + slot * a.D + c1);
+      }
+      const float ss = head_sum<kLanes>(dot4(x, x, dot4(y, y, 0.f)));
+      if (!live || !ok) continue;
+      if (!(ss <= 3.4028235e38f)) bad = true;          // a sum of squares: not finite if an element is not
+      if (!value) {
+        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const bool query = h < a.Hq;
+        x = mul4(scale4(x, r), pick4(query, l.gq0, l.gk0));
+        y = mul4(scale4(y, r), pick4(query, l.gq1, l.gk1));
+        if (l.turned) rotate(x, y, cs, sn, a.interleaved != 0);
+      }
+      if (kAppend && h >= a.Hq && !store) continue;
+      T* out = h < a.Hq ? oq + h * a.D : (h < nk ? ok_ : ov) + int64_t(h) * stride;
+      st4(out + c0, x);
+      st4(out + c1, y);
     }
   }
   if (bad) raise_status(kDevNonFinite);

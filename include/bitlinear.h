@@ -388,6 +388,7 @@ bl_status bl_linear_backward(const float* dY, const float* X, const float* W, in
  *     without effect).  A row that sees no key gives 0 (its lse -inf, its
  *     gradient 0).
  *   - `scale` multiplies the scores (1/sqrt(D) for the usual attention).
+ *   - Outputs and workspaces overlap no input and not one another.
  *   - Values that no row sees (behind a sequence's end, outside every window,
  *     the unused rest of a page) may hold anything, NaN included.  A NaN or Inf
  *     that a row does see sets BL_ERR_NONFINITE in the status word; in

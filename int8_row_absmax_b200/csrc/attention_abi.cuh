@@ -34,6 +34,23 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
   return true;
 }
 
+// A launch that may begin while the kernel before it on the stream still runs (programmatic
+// dependent launch); the kernel itself waits where it has to.
+template <typename... P, typename... A>
+bool launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+}
+
 // ---- norms and rotation ----------------------------------------------------------
 bl_status check_rows(const bl_qkv_rows* r, bool values) {
   if (!r) return BL_ERR_INVALID_ARG;
@@ -98,7 +115,7 @@ bl_status launch_rows(const QrArgs& a, cudaStream_t st) {
     const int64_t cap = int64_t(num_sms()) * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm), grid = ceil_div(items, kQrRingWarps);
     qk_norm_rope_ring_kernel<T, kAppend, kLanes><<<unsigned(grid < cap ? grid : cap), 32 * kQrRingWarps, smem, st>>>(a);
   } else {
-    qk_norm_rope_kernel<T, kAppend, 1, kLanes><<<grid_for(a.M * heads, kPerBlock, 16), kQrThreads, 0, st>>>(a);
+    qk_norm_rope_kernel<T, kAppend, kLanes><<<grid_for(a.M * heads, kPerBlock, 16), kQrThreads, 0, st>>>(a);
   }
   return launch_status();
 }
@@ -119,23 +136,27 @@ int rows_back_grid(const bl_qkv_rows* r) {
   return int(g < 1 ? 1 : g < kQrBackCtas ? g : kQrBackCtas);
 }
 
-// Two heads an item once that fills the SMs, one where latency counts.
+// As launch_rows.
 template <typename T, int kLanes>
-void launch_rows_back(const QrArgs& a, int grid, cudaStream_t st) {
+bl_status launch_rows_back(const QrArgs& a, int grid, cudaStream_t st) {
   constexpr int kPerBlock = kQrThreads / kLanes;
-  const int smem = kPerBlock * 2 * a.D * 4;            // at most 16 KB
-  if (a.M * ceil_div(a.Hq + 2 * int64_t(a.Hkv), 2) >= int64_t(grid) * kPerBlock * 2)
-    qk_norm_rope_backward_kernel<T, 2, kLanes><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
-  else
-    qk_norm_rope_backward_kernel<T, 1, kLanes><<<unsigned(grid), kQrThreads, size_t(smem), st>>>(a);
+  if (a.M * ceil_div(a.Hq + 2 * int64_t(a.Hkv), kQrBackHeads) >= int64_t(grid) * kQrRingWarps * 2) {
+    static std::atomic<uint64_t> done{0};
+    constexpr int kPerD = kQrRingWarps * kQrRing * kQrBackHeads * (4 + int(sizeof(T)));   // bytes per element of a head
+    if (!allow_smem(qk_norm_rope_backward_ring_kernel<T, kLanes>, kPerD * 8 * kLanes, done)) return BL_ERR_CUDA;
+    qk_norm_rope_backward_ring_kernel<T, kLanes><<<unsigned(grid), 32 * kQrRingWarps, size_t(kPerD) * a.D, st>>>(a);
+  } else {
+    qk_norm_rope_backward_kernel<T, kLanes><<<unsigned(grid), kQrThreads, size_t(kPerBlock) * 2 * a.D * 4, st>>>(a);
+  }
+  return launch_status();
 }
 template <typename T>
-void launch_norm_rope_back(const QrArgs& a, int grid, cudaStream_t st) {
+bl_status launch_norm_rope_back(const QrArgs& a, int grid, cudaStream_t st) {
   switch (rows_lanes(a.D)) {
-    case 4: launch_rows_back<T, 4>(a, grid, st); break;
-    case 8: launch_rows_back<T, 8>(a, grid, st); break;
-    case 16: launch_rows_back<T, 16>(a, grid, st); break;
-    default: launch_rows_back<T, 32>(a, grid, st); break;
+    case 4: return launch_rows_back<T, 4>(a, grid, st);
+    case 8: return launch_rows_back<T, 8>(a, grid, st);
+    case 16: return launch_rows_back<T, 16>(a, grid, st);
+    default: return launch_rows_back<T, 32>(a, grid, st);
   }
 }
 
@@ -277,8 +298,13 @@ bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
   }
   if (queries && gq > 0) attn_dq_kernel<T, DP><<<unsigned(gq), kAbThreads, AbCfg<DP>::kDqSmem, st>>>(maps, a, norms);
   if (keys && gk > 0) {
-    attn_dkv_kernel<T, DP><<<unsigned(gk * a.splits), kAbThreads, AbCfg<DP>::kDkvSmem, st>>>(maps, a, norms);
-    if (a.splits > 1) attn_dkv_join_kernel<T><<<dim3(unsigned(gk), 8), 256, 0, st>>>(a);
+    // dK/dV needs nothing of dQ's: its CTAs take the SMs as those of dQ leave them
+    const bool early = queries && gq > 0;
+    if (early && !launch_early(attn_dkv_kernel<T, DP>, dim3(unsigned(gk * a.splits)), kAbThreads, AbCfg<DP>::kDkvSmem, st,
+                               maps, a, norms))
+      return BL_ERR_CUDA;
+    if (!early) attn_dkv_kernel<T, DP><<<unsigned(gk * a.splits), kAbThreads, AbCfg<DP>::kDkvSmem, st>>>(maps, a, norms);
+    if (a.splits > 1 && !launch_early(attn_dkv_join_kernel<T>, dim3(unsigned(gk), 8), 256, 0, st, a)) return BL_ERR_CUDA;
   }
   return launch_status();
 }
@@ -406,10 +432,13 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
   a.lddq = lddq;
   a.lddk = lddk;
   a.lddv = lddv;
-  if (t == BL_T_F32) launch_norm_rope_back<float>(a, grid, stream);
-  else if (t == BL_T_F16) launch_norm_rope_back<__half>(a, grid, stream);
-  else launch_norm_rope_back<__nv_bfloat16>(a, grid, stream);
-  if (a.part) gain_sum_kernel<<<unsigned(ceil_div(2 * a.D, 32)), 256, 0, stream>>>(a.part, grid, a.D, dgq, dgk);
+  st = t == BL_T_F32   ? launch_norm_rope_back<float>(a, grid, stream)
+       : t == BL_T_F16 ? launch_norm_rope_back<__half>(a, grid, stream)
+                       : launch_norm_rope_back<__nv_bfloat16>(a, grid, stream);
+  if (st != BL_OK) return st;
+  if (a.part && !launch_early(gain_sum_kernel, dim3(unsigned(ceil_div(2 * a.D, 32))), 256, 0, stream, a.part, grid, a.D,
+                              dgq, dgk))
+    return BL_ERR_CUDA;
   return launch_status();
 }
 

@@ -172,6 +172,7 @@ __device__ __forceinline__ void store_row_f32(uint32_t taddr, float* out, int D,
 template <typename T>
 __global__ void __launch_bounds__(256)
 attn_dkv_join_kernel(const AttnArgs a) {
+  griddep_wait();                                      // launched early: the parts are the kernel before's
   const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
   const int j0 = rest / a.B * 128;
   Seq s;
@@ -243,6 +244,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
 
   if (base & 1023u) {                                                   // never, with nothing static before it
     raise_status(kDevBadWorkspace);
+    griddep_wait();
     return;
   }
   // the work: parts of a group's heads and key heads fastest, early key blocks (which most queries see) first
@@ -250,7 +252,12 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   const int hk = unit / a.splits, z = unit - hk * a.splits, group = a.Hq / a.Hkv;
   const int j0 = rest / a.B * 128, h0 = hk * group + z * a.split_heads, heads = min(a.split_heads, group - z * a.split_heads);
   Seq s;
-  if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) return;
+  // Launched while dQ's CTAs still run, and reads nothing of theirs (delta is from the kernel before
+  // them); but it ends after they have ended, so that what follows it on the stream follows both.
+  if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) {
+    griddep_wait();
+    return;
+  }
   s.q0 = uniform(s.q0);
   s.nq = uniform(s.nq);
   s.k0 = uniform(s.k0);
@@ -531,6 +538,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  griddep_wait();
 }
 
 template <typename T, int DP>
@@ -543,6 +551,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
   __shared__ int s_err;
   constexpr int kBoxes = DP / 64;
   volatile int* err = &s_err;
+  griddep_launch_dependents();                                          // dK/dV may take SMs as soon as they are free
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   const int nblk = (a.max_q + 127) / 128;

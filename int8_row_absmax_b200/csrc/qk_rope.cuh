@@ -119,95 +119,63 @@ __device__ __forceinline__ void rotate(float4& lo, float4& hi, float4 c, float4 
 
 // Few rows, where latency counts.  Item i of the work is a token and one of its Hq + 2 Hkv
 // heads (queries, keys, values).
-template <typename T, bool kAppend, int kHeads, int kLanes>
+template <typename T, bool kAppend, int kLanes>
 __global__ void __launch_bounds__(kQrThreads)
 qk_norm_rope_kernel(const QrArgs a) {
   constexpr int kPerBlock = kQrThreads / kLanes;
   const QrLane l = qr_lane(a, threadIdx.x & (kLanes - 1));
-  const int u = l.u, nk = a.Hq + a.Hkv, heads = nk + a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
-  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * kPerBlock;
+  const int u = l.u, nk = a.Hq + a.Hkv, heads = nk + a.Hkv;
+  const int64_t items = a.M * heads, step = int64_t(gridDim.x) * kPerBlock;
   const float inv_d = 1.f / float(a.D);
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false, range = false;
   // whole warps take every turn together: the shuffles need all lanes
-  const int64_t first = int64_t(blockIdx.x) * kPerBlock, mine = threadIdx.x / kLanes;
-  // the token, its position and slot are asked for an item ahead: the table's row follows the position
-  int64_t m_next = 0, c_next = 0, p_next = 0, at_next = -1;
-  auto ask = [&](int64_t i) {
-    if (i >= items) return;
-    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
-    p_next = a.R ? a.pos[m_next] : 0;
-    if (kAppend) at_next = a.slots[m_next];
-  };
-  ask(first + mine);
-  for (int64_t base = first; base < items; base += step) {
-    const int64_t i = base + mine;
+  for (int64_t base = int64_t(blockIdx.x) * kPerBlock; base < items; base += step) {
+    const int64_t i = base + threadIdx.x / kLanes;
     const bool live = i < items;
-    const int64_t m = m_next, p = p_next, at = at_next;
-    const int h0 = int(c_next) * kHeads;
-    // head h's columns at row + h * D in each of the three
-    const float* rq = a.q + m * a.ldq;
-    const float* rk = a.k + m * a.ldk - int64_t(a.Hq) * a.D;
-    const float* rv = a.v + m * a.ldv - int64_t(nk) * a.D;
-    float4 x[kHeads], y[kHeads];
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
-      x[j] = y[j] = zero;
-      if (!live || !l.on || h >= heads) continue;
-      const float* row = (h < a.Hq ? rq : h < nk ? rk : rv) + h * a.D;
-      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (h < nk ? l.lo : 8 * u)));
-      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + (h < nk ? l.hi : 8 * u + 4)));
+    int64_t m = 0, hh = 0;
+    split_index(live ? i : 0, heads, items < (int64_t(1) << 31), m, hh);
+    const int h = int(hh);
+    const bool value = h >= nk, query = h < a.Hq;
+    const int c0 = value ? 8 * u : l.lo, c1 = value ? 8 * u + 4 : l.hi;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (live && l.on) {
+      const float* row = query ? a.q + m * a.ldq + h * a.D
+                               : (value ? a.v + m * a.ldv - int64_t(nk) * a.D : a.k + m * a.ldk - int64_t(a.Hq) * a.D) + h * a.D;
+      x = ld_stream_f4(reinterpret_cast<const float4*>(row + c0));
+      y = ld_stream_f4(reinterpret_cast<const float4*>(row + c1));
     }
+    const int64_t at = kAppend && live ? a.slots[m] : 0;
+    const int64_t p = live && a.R ? a.pos[m] : 0;
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
-    if (live && !ok) range = true;
-    float4 cs = zero, sn = zero;
-    if (l.turned && ok) {
-      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
-      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
+    if (!ok || at >= (kAppend ? a.nslots : 1)) range = true;
+    const float ss = head_sum<kLanes>(dot4(x, x, dot4(y, y, 0.f)));
+    if (!live || !ok || !l.on) continue;
+    if (!(ss <= 3.4028235e38f)) bad = true;            // a sum of squares: not finite if an element is not
+    if (!value) {
+      const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+      x = mul4(scale4(x, r), pick4(query, l.gq0, l.gk0));
+      y = mul4(scale4(y, r), pick4(query, l.gq1, l.gk1));
+      if (l.turned)
+        rotate(x, y, *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u),
+               *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u), a.interleaved != 0);
     }
-    ask(i + step);
-    // head h's columns at out + h * D (a cache: h * page * D)
-    T* oq = static_cast<T*>(a.oq) + m * a.Hq * a.D;
-    T *ok_, *ov;
-    bool store = true;
-    int stride = a.D;
-    if (kAppend) {
-      store = live && at >= 0 && at < a.nslots;
-      if (live && at >= a.nslots) range = true;
-      int64_t page = 0, in = 0;
-      split_index(store ? at : 0, a.page, a.nslots < (int64_t(1) << 31), page, in);
-      stride = a.page * a.D;
-      const int64_t to = page * a.Hkv * stride + in * a.D;
-      ok_ = static_cast<T*>(a.ok) + to - int64_t(a.Hq) * stride;
-      ov = static_cast<T*>(a.ov) + to - int64_t(nk) * stride;
+    T* out;
+    if (query) {
+      out = static_cast<T*>(a.oq) + (m * a.Hq + h) * a.D;
     } else {
-      ok_ = static_cast<T*>(a.ok) + (m * a.Hkv - a.Hq) * a.D;
-      ov = static_cast<T*>(a.ov) + (m * a.Hkv - nk) * a.D;
-    }
-    float ss[kHeads];
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) ss[j] = head_sum<kLanes>(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)));
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
-      if (!live || h >= heads || !ok || !l.on) continue;
-      if (!(ss[j] <= 3.4028235e38f)) bad = true;       // a sum of squares: not finite if an element is not
-      int c0 = 8 * u, c1 = 8 * u + 4;
-      if (h < nk) {
-        const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
-        const bool query = h < a.Hq;
-        x[j] = mul4(scale4(x[j], r), pick4(query, l.gq0, l.gk0));
-        y[j] = mul4(scale4(y[j], r), pick4(query, l.gq1, l.gk1));
-        if (l.turned) rotate(x[j], y[j], cs, sn, a.interleaved != 0);
-        c0 = l.lo;
-        c1 = l.hi;
+      const int hk = value ? h - nk : h - a.Hq;
+      out = static_cast<T*>(value ? a.ov : a.ok);
+      if (kAppend) {
+        if (at < 0 || at >= a.nslots) continue;
+        int64_t page, in;
+        split_index(at, a.page, a.nslots < (int64_t(1) << 31), page, in);
+        out += ((page * a.Hkv + hk) * a.page + in) * a.D;
+      } else {
+        out += (m * a.Hkv + hk) * a.D;
       }
-      T* out = h < a.Hq ? oq + h * a.D : (h < nk ? ok_ : ov) + int64_t(h) * stride;
-      if (kAppend && h >= a.Hq && !store) continue;
-      st4(out + c0, x[j]);
-      st4(out + c1, y[j]);
     }
+    st4(out + c0, x);
+    st4(out + c1, y);
   }
   if (bad) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
@@ -332,108 +300,41 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
   if (range) raise_status(kDevRange);
 }
 
-// The gradient.  A group of lanes keeps the same columns throughout, so the gains'
-// gradients stay in its registers until the end; then the CTA adds its groups in
-// order and writes one partial row, and gain_sum_kernel adds those in order.
-template <typename T, int kHeads, int kLanes>
-__global__ void __launch_bounds__(kQrThreads, 2)
-qk_norm_rope_backward_kernel(const QrArgs a) {
-  extern __shared__ float sums[];                    // [kPerBlock, 2, D]
-  constexpr int kPerBlock = kQrThreads / kLanes;
-  const QrLane l = qr_lane(a, threadIdx.x & (kLanes - 1));
-  const int u = l.u, grp = threadIdx.x / kLanes;
-  const int nk = a.Hq + a.Hkv, heads = nk + a.Hkv, chunks = (heads + kHeads - 1) / kHeads;
-  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * kPerBlock;
-  const float inv_d = 1.f / float(a.D);
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
-  bool bad = false, range = false;
-  int64_t m_next = 0, c_next = 0, p_next = 0;        // asked for an item ahead: the table's row follows the position
-  auto ask = [&](int64_t i) {
-    if (i >= items) return;
-    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
-    p_next = a.R ? a.pos[m_next] : 0;
-  };
-  ask(int64_t(blockIdx.x) * kPerBlock + grp);
-  for (int64_t base = int64_t(blockIdx.x) * kPerBlock; base < items; base += step) {
-    const int64_t i = base + grp;
-    const bool live = i < items;
-    const int64_t m = m_next, p = p_next;
-    const int h0 = int(c_next) * kHeads;
-    const bool ok = p >= 0 && (a.R == 0 || p < a.P);
-    if (live && !ok) range = true;
-    const bool work = live && l.on && ok;
-    const T* iq = static_cast<const T*>(a.dq) + m * a.Hq * a.D;
-    const T* ik = static_cast<const T*>(a.dk) + (m * a.Hkv - a.Hq) * a.D;
-    const T* iv = static_cast<const T*>(a.dv) + (m * a.Hkv - nk) * a.D;
-    const float* rq = a.q + m * a.ldq;
-    const float* rk = a.k + m * a.ldk - int64_t(a.Hq) * a.D;
-    float4 x[kHeads], y[kHeads], e[kHeads], f[kHeads];
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
-      x[j] = y[j] = e[j] = f[j] = zero;
-      if (!work || h >= heads) continue;
-      const T* d = (h < a.Hq ? iq : h < nk ? ik : iv) + h * a.D;
-      e[j] = ld4(d + (h < nk ? l.lo : 8 * u));
-      f[j] = ld4(d + (h < nk ? l.hi : 8 * u + 4));
-      if (h >= nk) continue;
-      const float* row = (h < a.Hq ? rq : rk) + h * a.D;
-      x[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + l.lo));
-      y[j] = ld_stream_f4(reinterpret_cast<const float4*>(row + l.hi));
-    }
-    float4 cs = zero, sn = zero;
-    if (work && l.turned) {
-      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
-      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
-      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
-    }
-    ask(i + step);
-    float* oq = a.dxq + m * a.lddq;
-    float* okk = a.dxk + m * a.lddk - int64_t(a.Hq) * a.D;
-    float* ov = a.dxv + m * a.lddv - int64_t(nk) * a.D;
-    // both sums of a head at once: sum x^2, and sum x g dy, of which mean(x g dy r) is r / D times
-    float ss[kHeads], tt[kHeads];
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
-      if (l.turned && h < nk) rotate(e[j], f[j], cs, sn, a.interleaved != 0);
-      const bool query = h < a.Hq;
-      ss[j] = head_sum<kLanes>(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)));
-      tt[j] = head_sum<kLanes>(dot4(mul4(e[j], pick4(query, l.gq0, l.gk0)), x[j],
-                                    dot4(mul4(f[j], pick4(query, l.gq1, l.gk1)), y[j], 0.f)));
-    }
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
-      if (!work || h >= heads) continue;
-      if (h >= nk) {
-        float* out = ov + h * a.D + 8 * u;
-        *reinterpret_cast<float4*>(out) = e[j];
-        *reinterpret_cast<float4*>(out + 4) = f[j];
-        continue;
-      }
-      const bool query = h < a.Hq;
-      const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
-      const float t = tt[j] * inv_d * r;
-      if (!(ss[j] <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
-      x[j] = scale4(x[j], r);
-      y[j] = scale4(y[j], r);
-      const float4 ge = mul4(e[j], pick4(query, l.gq0, l.gk0)), gf = mul4(f[j], pick4(query, l.gq1, l.gk1));
-      float* out = (query ? oq : okk) + h * a.D;
-      *reinterpret_cast<float4*>(out + l.lo) = make_float4(r * fmaf(-x[j].x, t, ge.x), r * fmaf(-x[j].y, t, ge.y),
-                                                           r * fmaf(-x[j].z, t, ge.z), r * fmaf(-x[j].w, t, ge.w));
-      *reinterpret_cast<float4*>(out + l.hi) = make_float4(r * fmaf(-y[j].x, t, gf.x), r * fmaf(-y[j].y, t, gf.y),
-                                                           r * fmaf(-y[j].z, t, gf.z), r * fmaf(-y[j].w, t, gf.w));
-      float4& s0 = query ? sq0 : sk0;
-      float4& s1 = query ? sq1 : sk1;
-      s0 = make_float4(fmaf(e[j].x, x[j].x, s0.x), fmaf(e[j].y, x[j].y, s0.y), fmaf(e[j].z, x[j].z, s0.z), fmaf(e[j].w, x[j].w, s0.w));
-      s1 = make_float4(fmaf(f[j].x, y[j].x, s1.x), fmaf(f[j].y, y[j].y, s1.y), fmaf(f[j].z, y[j].z, s1.z), fmaf(f[j].w, y[j].w, s1.w));
-    }
+// A head's gradient from its row, its rotated-back gradient (e, f) and both sums.
+__device__ __forceinline__ void head_back(const QrArgs& a, const QrLane& l, int h, int nk, float4 x, float4 y, float4 e,
+                                          float4 f, float ss, float tt, float inv_d, float* oq, float* ok, float* ov,
+                                          float4& sq0, float4& sq1, float4& sk0, float4& sk1, bool& bad) {
+  if (h >= nk) {
+    float* out = ov + h * a.D + 8 * l.u;
+    *reinterpret_cast<float4*>(out) = e;
+    *reinterpret_cast<float4*>(out + 4) = f;
+    return;
   }
-  if (bad) raise_status(kDevNonFinite);
-  if (range) raise_status(kDevRange);
-  if (!a.part) return;
+  const bool query = h < a.Hq;
+  const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+  const float t = tt * inv_d * r;
+  if (!(ss <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
+  x = scale4(x, r);
+  y = scale4(y, r);
+  const float4 ge = mul4(e, pick4(query, l.gq0, l.gk0)), gf = mul4(f, pick4(query, l.gq1, l.gk1));
+  float* out = (query ? oq : ok) + h * a.D;
+  *reinterpret_cast<float4*>(out + l.lo) = make_float4(r * fmaf(-x.x, t, ge.x), r * fmaf(-x.y, t, ge.y),
+                                                       r * fmaf(-x.z, t, ge.z), r * fmaf(-x.w, t, ge.w));
+  *reinterpret_cast<float4*>(out + l.hi) = make_float4(r * fmaf(-y.x, t, gf.x), r * fmaf(-y.y, t, gf.y),
+                                                       r * fmaf(-y.z, t, gf.z), r * fmaf(-y.w, t, gf.w));
+  if (query) {
+    sq0 = make_float4(fmaf(e.x, x.x, sq0.x), fmaf(e.y, x.y, sq0.y), fmaf(e.z, x.z, sq0.z), fmaf(e.w, x.w, sq0.w));
+    sq1 = make_float4(fmaf(f.x, y.x, sq1.x), fmaf(f.y, y.y, sq1.y), fmaf(f.z, y.z, sq1.z), fmaf(f.w, y.w, sq1.w));
+  } else {
+    sk0 = make_float4(fmaf(e.x, x.x, sk0.x), fmaf(e.y, x.y, sk0.y), fmaf(e.z, x.z, sk0.z), fmaf(e.w, x.w, sk0.w));
+    sk1 = make_float4(fmaf(f.x, y.x, sk1.x), fmaf(f.y, y.y, sk1.y), fmaf(f.z, y.z, sk1.z), fmaf(f.w, y.w, sk1.w));
+  }
+}
+
+// The CTA's part of the gains' gradients: its groups' sums, added in order.
+template <int kGroups>
+__device__ __forceinline__ void gain_part(const QrArgs& a, const QrLane& l, int grp, float* sums, float4 sq0, float4 sq1,
+                                          float4 sk0, float4 sk1) {
   if (l.on) {
     float* s = sums + grp * 2 * a.D;
     *reinterpret_cast<float4*>(s + l.lo) = sq0;
@@ -442,17 +343,201 @@ qk_norm_rope_backward_kernel(const QrArgs a) {
     *reinterpret_cast<float4*>(s + a.D + l.hi) = sk1;
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < 2 * a.D; d += kQrThreads) {
+  for (int d = threadIdx.x; d < 2 * a.D; d += blockDim.x) {
     float s = 0.f;
-    for (int j = 0; j < kPerBlock; ++j) s += sums[j * 2 * a.D + d];
+    for (int j = 0; j < kGroups; ++j) s += sums[j * 2 * a.D + d];
     a.part[int64_t(blockIdx.x) * 2 * a.D + d] = s;
   }
+}
+
+// The gradient.  A group of lanes keeps the same columns throughout, so the gains'
+// gradients stay in its registers until the end; then the CTA adds its groups in
+// order and writes one partial row, and gain_sum_kernel adds those in order.
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(kQrThreads, 2)
+qk_norm_rope_backward_kernel(const QrArgs a) {
+  extern __shared__ __align__(16) float sums[];      // [kPerBlock, 2, D]
+  constexpr int kPerBlock = kQrThreads / kLanes;
+  const QrLane l = qr_lane(a, threadIdx.x & (kLanes - 1));
+  const int u = l.u, grp = threadIdx.x / kLanes;
+  const int nk = a.Hq + a.Hkv, heads = nk + a.Hkv;
+  const int64_t items = a.M * heads, step = int64_t(gridDim.x) * kPerBlock;
+  const float inv_d = 1.f / float(a.D);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
+  bool bad = false, range = false;
+  int64_t m_next = 0, h_next = 0, p_next = 0;        // asked for an item ahead: the table's row follows the position
+  auto ask = [&](int64_t i) {
+    if (i >= items) return;
+    split_index(i, heads, items < (int64_t(1) << 31), m_next, h_next);
+    p_next = a.R ? a.pos[m_next] : 0;
+  };
+  ask(int64_t(blockIdx.x) * kPerBlock + grp);
+  for (int64_t base = int64_t(blockIdx.x) * kPerBlock; base < items; base += step) {
+    const int64_t i = base + grp;
+    const bool live = i < items;
+    const int64_t m = m_next, p = p_next;
+    const int h = int(h_next);
+    const bool ok = p >= 0 && (a.R == 0 || p < a.P);
+    if (live && !ok) range = true;
+    const bool work = live && l.on && ok;
+    float4 x = zero, y = zero, e = zero, f = zero;
+    if (work) {
+      const T* d = (h < a.Hq ? static_cast<const T*>(a.dq) + m * a.Hq * a.D
+                             : static_cast<const T*>(h < nk ? a.dk : a.dv) + (m * a.Hkv - (h < nk ? a.Hq : nk)) * a.D) + h * a.D;
+      e = ld4(d + (h < nk ? l.lo : 8 * u));
+      f = ld4(d + (h < nk ? l.hi : 8 * u + 4));
+      if (h < nk) {
+        const float* row = (h < a.Hq ? a.q + m * a.ldq : a.k + m * a.ldk - int64_t(a.Hq) * a.D) + h * a.D;
+        x = ld_stream_f4(reinterpret_cast<const float4*>(row + l.lo));
+        y = ld_stream_f4(reinterpret_cast<const float4*>(row + l.hi));
+      }
+    }
+    ask(i + step);
+    if (work && l.turned && h < nk) {
+      const float4 cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
+      const float4 sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
+      rotate(e, f, cs, make_float4(-sn.x, -sn.y, -sn.z, -sn.w), a.interleaved != 0);
+    }
+    // both sums at once: sum x^2, and sum x g dy, of which mean(x g dy r) is r / D times
+    const bool query = h < a.Hq;
+    const float ss = head_sum<kLanes>(dot4(x, x, dot4(y, y, 0.f)));
+    const float tt = head_sum<kLanes>(dot4(mul4(e, pick4(query, l.gq0, l.gk0)), x,
+                                           dot4(mul4(f, pick4(query, l.gq1, l.gk1)), y, 0.f)));
+    if (work)
+      head_back(a, l, h, nk, x, y, e, f, ss, tt, inv_d, a.dxq + m * a.lddq, a.dxk + m * a.lddk - int64_t(a.Hq) * a.D,
+                a.dxv + m * a.lddv - int64_t(nk) * a.D, sq0, sq1, sk0, sk1, bad);
+  }
+  if (bad) raise_status(kDevNonFinite);
+  if (range) raise_status(kDevRange);
+  if (a.part) gain_part<kPerBlock>(a, l, grp, sums, sq0, sq1, sk0, sk1);
+}
+
+// The gradient of many rows, fed like qk_norm_rope_ring_kernel: an item is
+// kQrBackHeads heads of a token, their float32 rows and their gradients.
+constexpr int kQrBackHeads = 4;
+
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(32 * kQrRingWarps, 2)
+qk_norm_rope_backward_ring_kernel(const QrArgs a) {
+  extern __shared__ __align__(128) unsigned char qr_smem[];
+  __shared__ uint64_t full[kQrRingWarps][kQrRing];
+  constexpr int kAtOnce = 32 / kLanes, kGroups = kQrRingWarps * kAtOnce;
+  constexpr int kPasses = (kQrBackHeads + kAtOnce - 1) / kAtOnce;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const QrLane l = qr_lane(a, lane & (kLanes - 1));
+  const int u = l.u, nk = a.Hq + a.Hkv, heads = nk + a.Hkv, chunks = (heads + kQrBackHeads - 1) / kQrBackHeads;
+  const int64_t items = a.M * chunks, step = int64_t(gridDim.x) * kQrRingWarps;
+  const int64_t first = int64_t(blockIdx.x) * kQrRingWarps + warp;
+  const float inv_d = 1.f / float(a.D);
+  const int x_bytes = kQrBackHeads * a.D * 4, stage = x_bytes + kQrBackHeads * a.D * int(sizeof(T));
+  unsigned char* ring = qr_smem + warp * kQrRing * stage;
+  if (lane == 0) {
+    for (int i = 0; i < kQrRing; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  auto issue = [&](int64_t i, int st) {                // lane 0: rows of q and k, gradients of all three
+    int64_t m, c;
+    split_index(i, chunks, items < (int64_t(1) << 31), m, c);
+    const int h0 = int(c) * kQrBackHeads, h1 = min(h0 + kQrBackHeads, heads);
+    unsigned char* to = ring + st * stage;
+    uint64_t* bar = &full[warp][st];
+    const int rows = max(0, min(h1, nk) - h0);
+    mbar_arrive_expect_tx(bar, uint32_t(rows * a.D * 4 + (h1 - h0) * a.D * int(sizeof(T))));
+    auto run = [&](int lo, int hi, const void* src, int base, int size, unsigned char* dst) {
+      lo = max(lo, h0);
+      hi = min(hi, h1);
+      if (lo < hi)
+        bulk_g2s(dst + (lo - h0) * a.D * size, static_cast<const unsigned char*>(src) + int64_t(lo - base) * a.D * size,
+                 uint32_t((hi - lo) * a.D * size), bar);
+    };
+    run(0, a.Hq, a.q + m * a.ldq, 0, 4, to);
+    run(a.Hq, nk, a.k + m * a.ldk, a.Hq, 4, to);
+    run(0, a.Hq, static_cast<const T*>(a.dq) + m * a.Hq * a.D, 0, sizeof(T), to + x_bytes);
+    run(a.Hq, nk, static_cast<const T*>(a.dk) + m * a.Hkv * a.D, a.Hq, sizeof(T), to + x_bytes);
+    run(nk, heads, static_cast<const T*>(a.dv) + m * a.Hkv * a.D, nk, sizeof(T), to + x_bytes);
+  };
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
+  bool bad = false, range = false;
+  int64_t m_next = 0, c_next = 0, p_next = 0;
+  auto ask = [&](int64_t i) {
+    if (i >= items) return;
+    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
+    p_next = a.R ? a.pos[m_next] : 0;
+  };
+  if (lane == 0)
+    for (int k = 0; k < kQrRing - 1; ++k)
+      if (first + k * step < items) issue(first + k * step, k);
+  ask(first);
+  int n = 0;
+  for (int64_t i = first; i < items; i += step, ++n) {
+    const int st = n % kQrRing;
+    const int64_t m = m_next, p = p_next;
+    const int h0 = int(c_next) * kQrBackHeads;
+    __syncwarp();                                      // the item before has been read: its place takes the next copy
+    if (lane == 0 && i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
+    const bool ok = p >= 0 && (a.R == 0 || p < a.P);
+    if (!ok) range = true;
+    float4 cs = zero, sn = zero;
+    if (l.turned && ok) {
+      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
+      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
+      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
+    }
+    ask(i + step);
+    float* oq = a.dxq + m * a.lddq;
+    float* okk = a.dxk + m * a.lddk - int64_t(a.Hq) * a.D;
+    float* ov = a.dxv + m * a.lddv - int64_t(nk) * a.D;
+    if (__any_sync(0xffffffffu, !mbar_wait_near(&full[warp][st], uint32_t(n / kQrRing) & 1u))) {
+      if (lane == 0) raise_status(kDevTimeout);        // and no copy left in flight
+      for (int k = 1; k < kQrRing; ++k)
+        if (i + k * step < items) mbar_wait(&full[warp][(n + k) % kQrRing], uint32_t((n + k) / kQrRing) & 1u);
+      break;
+    }
+    const float* rows = reinterpret_cast<const float*>(ring + st * stage);
+    const T* grads = reinterpret_cast<const T*>(ring + st * stage + x_bytes);
+    float4 x[kPasses], y[kPasses], e[kPasses], f[kPasses];
+    float ss[kPasses], tt[kPasses];
+#pragma unroll
+    for (int j = 0; j < kPasses; ++j) {
+      const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
+      const bool live = slot < kQrBackHeads && h < heads && l.on, value = h >= nk;
+      x[j] = y[j] = e[j] = f[j] = zero;
+      if (live) {
+        e[j] = ld4(grads + slot * a.D + (value ? 8 * u : l.lo));
+        f[j] = ld4(grads + slot * a.D + (value ? 8 * u + 4 : l.hi));
+        if (!value) {
+          x[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + l.lo);
+          y[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + l.hi);
+          if (l.turned) rotate(e[j], f[j], cs, sn, a.interleaved != 0);
+        }
+      }
+      const bool query = h < a.Hq;
+      ss[j] = head_sum<kLanes>(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)));
+      tt[j] = head_sum<kLanes>(dot4(mul4(e[j], pick4(query, l.gq0, l.gk0)), x[j],
+                                    dot4(mul4(f[j], pick4(query, l.gq1, l.gk1)), y[j], 0.f)));
+    }
+#pragma unroll
+    for (int j = 0; j < kPasses; ++j) {
+      const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
+      if (slot < kQrBackHeads && h < heads && l.on && ok)
+        head_back(a, l, h, nk, x[j], y[j], e[j], f[j], ss[j], tt[j], inv_d, oq, okk, ov, sq0, sq1, sk0, sk1, bad);
+    }
+  }
+  if (bad) raise_status(kDevNonFinite);
+  if (range) raise_status(kDevRange);
+  if (!a.part) return;
+  __syncthreads();                                     // the rings are read: their place takes the sums
+  gain_part<kGroups>(a, l, threadIdx.x / kLanes, reinterpret_cast<float*>(qr_smem), sq0, sq1, sk0, sk1);
 }
 
 // dg[d] = sum over the CTAs' partial rows, 32 columns a CTA, 8 slices of rows.
 __global__ void __launch_bounds__(256)
 gain_sum_kernel(const float* __restrict__ part, int rows, int D, float* __restrict__ dgq, float* __restrict__ dgk) {
   __shared__ float s[8][32];
+  griddep_wait();                                      // launched early: the parts are the kernel before's
   const int c = threadIdx.x & 31, sl = threadIdx.x >> 5, d = blockIdx.x * 32 + c;
   float v = 0.f;
   if (d < 2 * D) {

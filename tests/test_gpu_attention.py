@@ -61,7 +61,11 @@ def split(x, hq, hk, d):
 
 SHAPES = [(1, 20, 5, 128, 128, False, "bfloat16"), (7, 4, 4, 32, 16, True, "float32"), (33, 6, 2, 80, 80, False, "float16"),
           (3, 3, 1, 8, 8, True, "bfloat16"), (5, 2, 2, 256, 64, False, "float32"), (300, 32, 8, 128, 128, True, "float16"),
-          (4, 5, 1, 96, 0, False, "float32"), (2, 1, 1, 24, 8, False, "float16"), (900, 8, 8, 64, 64, False, "bfloat16")]
+          (4, 5, 1, 96, 0, False, "float32"), (2, 1, 1, 24, 8, False, "float16"), (900, 8, 8, 64, 64, False, "bfloat16"),
+          # enough rows for the kernels that are fed by bulk copies, each number of lanes a head
+          (5001, 4, 2, 32, 32, False, "float16"), (4801, 3, 1, 56, 24, True, "float32"),
+          (1705, 20, 4, 128, 128, False, "bfloat16"), (1301, 18, 9, 256, 64, True, "float32"),
+          (4803, 2, 1, 80, 40, False, "bfloat16"), (4802, 1, 1, 8, 8, False, "float32")]
 
 
 @pytest.mark.parametrize("m,hq,hk,d,rot,inter,dtype", SHAPES)
@@ -125,6 +129,30 @@ def test_append_fills_only_its_slots(bl, page):
         if s >= 0:
             k0[s // page, :, s % page], v0[s // page, :, s % page] = rk[i], rv[i]
     assert torch.equal(kc, k0) and torch.equal(vc, v0)
+
+
+def test_append_of_many_rows(bl):
+    """As many rows as the kernel fed by bulk copies takes, some without a slot, some out of range."""
+    import torch
+    m, hq, hk, d, page = 2400, 12, 2, 64, 16
+    qkv, pos, gq, gk = rows(3, m, hq, hk, d, d)
+    table = bl.rope_table(5000, d)
+    n = m // page + 7
+    kc, vc = torch.zeros(n, hk, page, d, dtype=torch.float16, device="cuda"), torch.zeros(n, hk, page, d, dtype=torch.float16, device="cuda")
+    k0, v0 = kc.clone(), vc.clone()
+    slots = torch.from_numpy(np.random.default_rng(1).permutation(n * page)[:m]).cuda()
+    slots[7::100] = -1
+    q = bl.qk_norm_rope_append(qkv, hq, hk, d, pos, table, gq, gk, kc, vc, slots)
+    rq, rk, rv = bl.qk_norm_rope(qkv, hq, hk, d, pos, table, gq, gk, dtype=torch.float16)
+    ok(bl)
+    keep = slots >= 0
+    k0[slots[keep] // page, :, slots[keep] % page], v0[slots[keep] // page, :, slots[keep] % page] = rk[keep], rv[keep]
+    assert torch.equal(q, rq) and torch.equal(kc, k0) and torch.equal(vc, v0)
+    pos[11], slots[13] = 5000, n * page
+    before = kc.clone()
+    bl.qk_norm_rope_append(qkv, hq, hk, d, pos, table, gq, gk, kc, vc, slots)
+    assert bl.sync_status() == "BL_ERR_RANGE"
+    assert torch.equal(kc, before)
 
 
 def test_bad_positions_and_slots_are_reported_and_not_written(bl):

@@ -1,8 +1,9 @@
-"""Build the BitLinear CUDA library in-tree for sm_100a.
+"""Build the BitLinear CUDA library in-tree for sm_100a, and the tensor binding of
+its attention operators over it.
 
-    python -m int8_row_absmax_b200.build        # -> int8_row_absmax_b200/libbitlinear.so
+    python -m int8_row_absmax_b200.build        # -> int8_row_absmax_b200/libbitlinear.so, _binding.so
 
-One nvcc invocation over one translation unit.  No fast-math: the quantizers
+One nvcc invocation over one translation unit, and one of the host compiler.  No fast-math: the quantizers
 need IEEE division and round-half-even, and -fmad=false keeps the dequant
 epilogue from being contracted into an FMA.
 """
@@ -12,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "bitlinear_lib.cu")
 OUT = os.path.join(PKG, "libbitlinear.so")
+BINDING_SRC = os.path.join(PKG, "csrc", "torch_binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "-gencode=arch=compute_100a,code=sm_100a"
 
 
@@ -33,28 +37,53 @@ def sources():
         [os.path.join(ROOT, "include", "bitlinear.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(OUT):
+def binding_sources():
+    return [BINDING_SRC, os.path.join(ROOT, "include", "bitlinear.h")]
+
+
+def up_to_date(out: str = OUT, srcs=None) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(OUT)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(s) <= t for s in (sources() if srcs is None else srcs))
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and up_to_date():
-        return OUT
-    cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-fmad=false",
-           "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-warn-spills",
-           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
-           *extra, "-o", OUT + ".tmp", SRC]
+def run(cmd, verbose: bool = False) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + res.stdout + res.stderr)
     if verbose and (res.stdout or res.stderr):
         print(res.stdout + res.stderr)
-    os.replace(OUT + ".tmp", OUT)
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The tensor binding, against the PyTorch that is installed."""
+    if not force and up_to_date(BINDING, binding_sources()):
+        return BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
+    run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_binding",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-I", os.path.join(ROOT, "include"), "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"],
+         *(x for d in inc for x in ("-isystem", d)), BINDING_SRC, "-o", BINDING + ".tmp", "-L", PKG,
+         "-l:libbitlinear.so", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+         "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    if force or not up_to_date():
+        run([nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-fmad=false",
+             "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-warn-spills",
+             "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
+             *extra, "-o", OUT + ".tmp", SRC], verbose)
+        os.replace(OUT + ".tmp", OUT)
+    build_binding(force, verbose)
     return OUT
 
 

@@ -160,13 +160,3 @@ def test_paged_attention_refusals(lib):
         assert run(**kw) == e, kw
     assert lib.bl_paged_attention_workspace_size(2, 4, pages()) % 256 == 0
     assert lib.bl_paged_attention_workspace_size(2, 3, pages()) == 0
-
-
-def test_packed_structs_equal_the_classes():
-    """The binding packs the structs in one step: the same bytes as the ctypes classes."""
-    r = attn.QkvRows(7, 4, 2, 32, 16, 32, 48, 128, 64, 65, 80, 96, 10, 8, 1, 112, 128, 0.5)
-    assert bytes(r) == attn._pack_rows(7, 4, 2, 32, 16, 32, 48, 128, 64, 65, 80, 96, 10, 8, 1, 112, 128, 0.5)
-    p = attn.KvPages(2, 16, 32, 1 << 40, 24, 3, 64)
-    assert bytes(p) == attn._pack_pages(2, 16, 32, 1 << 40, 24, 3, 64)
-    c = attn.AttnCall(1, 4, 2, 64, 16, 32, 48, 256, 128, 129, 10, 11, 64, 80, 3, 9, 8, 5, 2, 0.25)
-    assert bytes(c) == attn._pack_call(1, 4, 2, 64, 16, 32, 48, 256, 128, 129, 10, 11, 64, 80, 3, 9, 8, 5, 2, 0.25)

@@ -94,6 +94,12 @@ template <int DP> __device__ __forceinline__ uint32_t pa_off(int r, int c) {
   return uint32_t(r * DP * 2 + ((c ^ x) << 4));
 }
 
+// a / b of values that are not negative; 32 bits where they do (64-bit division is a long
+// software routine).
+__device__ __forceinline__ int64_t div_near(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // The visible tiles of a sequence of `len` tokens: `lead` of them from tile 0, the
 // others from tile `from` on.
 struct PaTiles {
@@ -127,7 +133,8 @@ struct PaCfg {
   static constexpr int kPerSm = DP == 128 ? 3 : 4;     // CTAs an SM
   static constexpr int kStages = DP == 128 ? 2 : 3;
   static constexpr int kCtas = 148 * kPerSm;
-  static constexpr int kJoin = kHeads * DP * 4 > kPaThreads * 16 ? kHeads * DP * 4 : kPaThreads * 16;   // O, or a float4 a thread
+  static constexpr int kJoinRow = DP + 4;              // a row of O in shared memory: the lanes' heads in banks of their own
+  static constexpr int kJoin = kHeads * kJoinRow * 4 > kPaThreads * 16 ? kHeads * kJoinRow * 4 : kPaThreads * 16;   // O, or a float4 a thread
   static constexpr int kSmem = kStages * kStage + kJoin;
 };
 
@@ -184,8 +191,8 @@ paged_attn_kernel(const PaArgs a) {
     for (int64_t r = 0; r < rounds; ++r) total += scan(r * kPaThreads + tid);
     ctas = min(int64_t(gridDim.x), total);
     if (int64_t(blockIdx.x) < ctas) {
-      lo = int64_t(blockIdx.x) * total / ctas;
-      hi = (int64_t(blockIdx.x) + 1) * total / ctas;
+      lo = div_near(int64_t(blockIdx.x) * total, ctas);
+      hi = div_near((int64_t(blockIdx.x) + 1) * total, ctas);
       for (int64_t r = 0; r < rounds; ++r) {
         const int64_t sum = rounds == 1 ? total : scan(r * kPaThreads + tid);
         const int64_t first = before + x - n;
@@ -217,7 +224,7 @@ paged_attn_kernel(const PaArgs a) {
     p.b = b;
     p.len = len;
     p.tiles = pa_tiles(p.len, a.window, a.sinks);
-    p.item = int((x - first) / p.tiles.n);
+    p.item = int(div_near(x - first, p.tiles.n));
     p.flat = first + int64_t(p.item) * p.tiles.n;
     p.t = int(x - p.flat);
   };
@@ -449,7 +456,7 @@ paged_attn_kernel(const PaArgs a) {
             for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float* d = join + (u * 8 + hpair + (e & 1)) * DP + i * 16 + (lane >> 2) + 8 * (e >> 1);
+                float* d = join + (u * 8 + hpair + (e & 1)) * C::kJoinRow + i * 16 + (lane >> 2) + 8 * (e >> 1);
                 const float x = o[i][u][e] * f[u][e & 1];
                 *d = w == 0 ? x : *d + x;
               }
@@ -465,7 +472,7 @@ paged_attn_kernel(const PaArgs a) {
           const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
           float sum = 0.f;
           for (int w = 0; w < 4; ++w) sum = fmaf(s_l[w][h], exp2_approx(s_m[w][h] - top), sum);
-          const float r = join[h * DP + d] / sum;
+          const float r = join[h * C::kJoinRow + d] / sum;
           if (!(fabsf(r) < INFINITY)) bad = true;
           out[i] = from_f32<OutT>(r);
         }
@@ -473,24 +480,25 @@ paged_attn_kernel(const PaArgs a) {
         // its part to the workspace: slot 0 of the CTA if the item began before it, slot 1 if it goes on
         float* part = a.part + (2 * int64_t(blockIdx.x) + (seg_first == 0 ? 1 : 0)) * C::kHeads * (DP + 2);
         for (int i = tid; i < nh * DP / 4; i += kPaThreads)
-          __stcg(reinterpret_cast<float4*>(part) + i, reinterpret_cast<const float4*>(join)[i]);
+          __stcg(reinterpret_cast<float4*>(part) + i,
+                 *reinterpret_cast<const float4*>(join + i / (DP / 4) * C::kJoinRow + i % (DP / 4) * 4));
         for (int h = tid; h < nh; h += kPaThreads) {
           const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
           float sum = 0.f;
           for (int w = 0; w < 4; ++w) sum = fmaf(s_l[w][h], exp2_approx(s_m[w][h] - top), sum);
           __stcg(reinterpret_cast<float2*>(part + C::kHeads * DP) + h, make_float2(top, sum));
         }
-        __threadfence();
-        __syncthreads();
         // CTAs of the item: those that hold its first and its last tile, and all between
-        const int64_t c0 = ((cur.flat + 1) * ctas + total - 1) / total - 1;
-        const int64_t c1 = ((cur.flat + cur.tiles.n) * ctas + total - 1) / total - 1;
+        const int64_t c0 = div_near((cur.flat + 1) * ctas + total - 1, total) - 1;
+        const int64_t c1 = div_near((cur.flat + cur.tiles.n) * ctas + total - 1, total) - 1;
+        __syncthreads();
         if (tid == 0) {
-          const unsigned int before = atomicAdd(a.count + c0, 1u);
+          // releases what the CTA has written before the barrier, and acquires what the other CTAs have
+          unsigned int before;
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + c0) : "memory");
           s_last = before == unsigned(c1 - c0);
           if (s_last) a.count[c0] = 0u;
           if (before > unsigned(c1 - c0)) raise_status(kDevBadWorkspace);
-          __threadfence();
         }
         __syncthreads();
         if (s_last) {
@@ -543,7 +551,7 @@ paged_attn_kernel(const PaArgs a) {
               }
               const int d = col * 4 - h * DP;
               if (d < a.D) {
-                const float r[4] = {x.x / sum, x.y / sum, x.z / sum, x.w / sum};
+                const float inv = 1.f / sum, r[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   if (!(fabsf(r[e]) < INFINITY)) bad = true;

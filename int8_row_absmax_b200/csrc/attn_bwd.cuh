@@ -263,10 +263,10 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   s.k0 = uniform(s.k0);
   s.nk = uniform(s.nk);
   const int off = s.nk - s.nq;
-  // query blocks that see these keys: rows from `first` to `last`
-  const int first = max(0, j0 - off) / 128;
+  // query blocks that see these keys: rows from `first` (any row, not a multiple of 128) to `last`
+  const int first = max(0, j0 - off);
   const int last = a.window == 0 || j0 < a.sinks ? s.nq - 1 : min(s.nq - 1, j0 + 126 + a.window - off);
-  const int per = last < 0 || j0 - off > last ? 0 : last / 128 + 1 - first;   // blocks of one head
+  const int per = last < first ? 0 : (last - first) / 128 + 1;          // blocks of one head
   const int n = per * heads;
 
   // tiles: K, V, three of Q, two of dO
@@ -309,7 +309,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     // a block's lse and delta are asked for while the block before waits for its places
     float l[4], e[4];
     auto ask = [&](int it) {
-      const int h = h0 + it / per, i0 = (first + it % per) * 128;
+      const int h = h0 + it / per, i0 = first + it % per * 128;
       const int64_t at = int64_t(h) * a.Tq + s.q0 + i0 + lane;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -321,7 +321,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     if (n > 0) ask(0);
     int it = 0;
     for (; it < n; ++it) {
-      const int qs = it % 3, gs = it & 1, h = h0 + it / per, i0 = (first + it % per) * 128;
+      const int qs = it % 3, gs = it & 1, h = h0 + it / per, i0 = first + it % per * 128;
       // places come free in this order: Q's (and lse's) after dK of three blocks ago, dO's after dV of two
       // blocks ago, delta's, which is read after that, after dK of two blocks ago
       if (it >= 3 && !mbar_wait_near(&q_empty[qs], uint32_t(it / 3 - 1) & 1u)) *err = 1;
@@ -367,7 +367,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const uint32_t S = tmem, dP = tmem + 128, dV = tmem + 256, dK = tmem + 384;
     // rows of no query of the sequence must not meet P's and dS's zeros
     auto trim = [&](unsigned char* tile, int it) {
-      const int i0 = (first + it % per) * 128;
+      const int i0 = first + it % per * 128;
       if (i0 + 128 > s.nq && s.q0 + s.nq < a.Tq) zero_rows(tile, kBoxes, s.nq - i0, 128, lane);
     };
     auto wait_q = [&](int it) {
@@ -432,7 +432,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const float mult = ds_scale<T>(norms), f = mult * exp2f(-p_scale_log2<T>());
     bool fine = true;
     for (int it = 0; it < n; ++it) {
-      const int i0 = (first + it % per) * 128;
+      const int i0 = first + it % per * 128;
       const float4* lse = reinterpret_cast<const float4*>(lse_rows + it % 3 * 128 + half * 64);
       const float4* del = reinterpret_cast<const float4*>(delta_rows + (it & 1) * 128 + half * 64);
       fine = mbar_wait_near(&q_full[it % 3], uint32_t(it / 3) & 1u) && mbar_wait_near(&s_full, uint32_t(it) & 1u) && !*err;

@@ -126,11 +126,12 @@ __device__ __forceinline__ void zero_dead_keys(unsigned char* tile, int boxes, i
   if (window != 0 && first > sinks && j0 < first && j0 + 128 > sinks) zero_rows(tile, boxes, sinks - j0, first - j0, lane);
 }
 
-// The 128-key blocks that the rows at positions lo .. hi see: `lead` from block 0, the
-// others from block `from`.
+// The 128-key blocks that the rows at positions lo .. hi see: `lead` from key 0, the others
+// from key `from` on, which is the first window's first key itself and not the multiple of
+// 128 below it (a copy may start at any row): a block less for most windows.
 struct Blocks {
   int lead, from, n;
-  __device__ __forceinline__ int at(int i) const { return (i < lead ? i : i - lead + from) * 128; }
+  __device__ __forceinline__ int at(int i) const { return i < lead ? i * 128 : from + (i - lead) * 128; }
 };
 __device__ __forceinline__ Blocks key_blocks(int lo, int hi, int window, int sinks) {
   Blocks b;
@@ -138,9 +139,9 @@ __device__ __forceinline__ Blocks key_blocks(int lo, int hi, int window, int sin
   if (window != 0 && lo >= window) {
     const int ws = lo - window + 1;
     b.lead = (min(sinks, ws) + 127) / 128;
-    b.from = max(b.lead, ws / 128);
+    b.from = max(b.lead * 128, ws);
   }
-  b.n = hi < 0 ? 0 : b.lead + max(0, hi / 128 + 1 - b.from);
+  b.n = hi < 0 ? 0 : b.lead + (max(0, hi + 1 - b.from) + 127) / 128;
   return b;
 }
 

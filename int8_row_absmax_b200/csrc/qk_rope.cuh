@@ -186,6 +186,18 @@ qk_norm_rope_kernel(const QrArgs a) {
 // ahead of its work), so that 128 KB an SM are on their way whatever the registers allow.
 constexpr int kQrRing = 3, kQrRingHeads = 8, kQrRingWarps = 8;
 
+// What one lane copies of each item: the heads lo .. hi - 1, `size` bytes each, of the token's
+// row at src + m * row, to the item's place `to` on.
+struct QrRun {
+  const unsigned char* src;
+  int64_t row;
+  int lo, hi, size, to;
+  __device__ __forceinline__ void copy(unsigned char* stage, int64_t m, int h0, int h1, uint64_t* bar) const {
+    const int a = max(lo, h0), b = min(hi, h1);
+    if (a < b) bulk_g2s(stage + to + (a - h0) * size, src + m * row + int64_t(a - lo) * size, uint32_t((b - a) * size), bar);
+  }
+};
+
 template <typename T, bool kAppend, int kLanes>
 __global__ void __launch_bounds__(32 * kQrRingWarps, 2)
 qk_norm_rope_ring_kernel(const QrArgs a) {
@@ -204,20 +216,21 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     fence_mbar_init();
   }
   __syncwarp();
-  auto issue = [&](int64_t i, int st) {                // lane 0: the heads of item i, a run from each of q, k, v
+  // lanes 0..2 each copy the run of an item's heads that lies in q, k or v
+  QrRun run;
+  run.src = reinterpret_cast<const unsigned char*>(lane == 0 ? a.q : lane == 1 ? a.k : a.v);
+  run.row = (lane == 0 ? a.ldq : lane == 1 ? a.ldk : a.ldv) * 4;
+  run.lo = lane == 0 ? 0 : lane == 1 ? a.Hq : nk;
+  run.hi = lane == 0 ? a.Hq : lane == 1 ? nk : lane == 2 ? heads : 0;
+  run.size = a.D * 4;
+  run.to = 0;
+  auto issue = [&](int64_t i, int st) {
     int64_t m, c;
     split_index(i, chunks, items < (int64_t(1) << 31), m, c);
     const int h0 = int(c) * kQrRingHeads, h1 = min(h0 + kQrRingHeads, heads);
-    float* to = ring + st * kQrRingHeads * a.D;
-    mbar_arrive_expect_tx(&full[warp][st], uint32_t((h1 - h0) * a.D * 4));
-    auto run = [&](int lo, int hi, const float* row, int base) {
-      lo = max(lo, h0);
-      hi = min(hi, h1);
-      if (lo < hi) bulk_g2s(to + (lo - h0) * a.D, row + int64_t(lo - base) * a.D, uint32_t((hi - lo) * a.D * 4), &full[warp][st]);
-    };
-    run(0, a.Hq, a.q + m * a.ldq, 0);
-    run(a.Hq, nk, a.k + m * a.ldk, a.Hq);
-    run(nk, heads, a.v + m * a.ldv, nk);
+    if (lane == 0) mbar_arrive_expect_tx(&full[warp][st], uint32_t((h1 - h0) * a.D * 4));
+    __syncwarp();
+    run.copy(reinterpret_cast<unsigned char*>(ring + st * kQrRingHeads * a.D), m, h0, h1, &full[warp][st]);
   };
   bool bad = false, range = false;
   int64_t m_next = 0, c_next = 0, p_next = 0, at_next = -1;
@@ -227,9 +240,8 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     p_next = a.R ? a.pos[m_next] : 0;
     if (kAppend) at_next = a.slots[m_next];
   };
-  if (lane == 0)
-    for (int k = 0; k < kQrRing - 1; ++k)
-      if (first + k * step < items) issue(first + k * step, k);
+  for (int k = 0; k < kQrRing - 1; ++k)
+    if (first + k * step < items) issue(first + k * step, k);
   ask(first);
   int n = 0;
   for (int64_t i = first; i < items; i += step, ++n) {
@@ -237,7 +249,7 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     const int64_t m = m_next, p = p_next, at = at_next;
     const int h0 = int(c_next) * kQrRingHeads;
     __syncwarp();                                      // the item before has been read: its place takes the next copy
-    if (lane == 0 && i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
+    if (i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
     if (!ok) range = true;
     float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), sn = cs;
@@ -437,26 +449,24 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
     fence_mbar_init();
   }
   __syncwarp();
-  auto issue = [&](int64_t i, int st) {                // lane 0: rows of q and k, gradients of all three
+  // lanes 0..4 each copy a run of an item's heads: the rows of q and k, the gradients of all three
+  const int size = int(sizeof(T));
+  QrRun run;
+  run.src = static_cast<const unsigned char*>(lane == 0 ? static_cast<const void*>(a.q) : lane == 1 ? a.k : lane == 2 ? a.dq
+                                              : lane == 3 ? a.dk : a.dv);
+  run.row = lane == 0 ? a.ldq * 4 : lane == 1 ? a.ldk * 4 : int64_t(lane == 2 ? a.Hq : a.Hkv) * a.D * size;
+  run.lo = lane == 0 || lane == 2 ? 0 : lane == 4 ? nk : a.Hq;
+  run.hi = lane == 0 || lane == 2 ? a.Hq : lane == 4 ? heads : lane < 4 ? nk : 0;
+  run.size = a.D * (lane < 2 ? 4 : size);
+  run.to = lane < 2 ? 0 : x_bytes;
+  auto issue = [&](int64_t i, int st) {
     int64_t m, c;
     split_index(i, chunks, items < (int64_t(1) << 31), m, c);
     const int h0 = int(c) * kQrBackHeads, h1 = min(h0 + kQrBackHeads, heads);
-    unsigned char* to = ring + st * stage;
-    uint64_t* bar = &full[warp][st];
-    const int rows = max(0, min(h1, nk) - h0);
-    mbar_arrive_expect_tx(bar, uint32_t(rows * a.D * 4 + (h1 - h0) * a.D * int(sizeof(T))));
-    auto run = [&](int lo, int hi, const void* src, int base, int size, unsigned char* dst) {
-      lo = max(lo, h0);
-      hi = min(hi, h1);
-      if (lo < hi)
-        bulk_g2s(dst + (lo - h0) * a.D * size, static_cast<const unsigned char*>(src) + int64_t(lo - base) * a.D * size,
-                 uint32_t((hi - lo) * a.D * size), bar);
-    };
-    run(0, a.Hq, a.q + m * a.ldq, 0, 4, to);
-    run(a.Hq, nk, a.k + m * a.ldk, a.Hq, 4, to);
-    run(0, a.Hq, static_cast<const T*>(a.dq) + m * a.Hq * a.D, 0, sizeof(T), to + x_bytes);
-    run(a.Hq, nk, static_cast<const T*>(a.dk) + m * a.Hkv * a.D, a.Hq, sizeof(T), to + x_bytes);
-    run(nk, heads, static_cast<const T*>(a.dv) + m * a.Hkv * a.D, nk, sizeof(T), to + x_bytes);
+    if (lane == 0)
+      mbar_arrive_expect_tx(&full[warp][st], uint32_t(max(0, min(h1, nk) - h0) * a.D * 4 + (h1 - h0) * a.D * size));
+    __syncwarp();
+    run.copy(ring + st * stage, m, h0, h1, &full[warp][st]);
   };
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
@@ -467,9 +477,8 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
     split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
     p_next = a.R ? a.pos[m_next] : 0;
   };
-  if (lane == 0)
-    for (int k = 0; k < kQrRing - 1; ++k)
-      if (first + k * step < items) issue(first + k * step, k);
+  for (int k = 0; k < kQrRing - 1; ++k)
+    if (first + k * step < items) issue(first + k * step, k);
   ask(first);
   int n = 0;
   for (int64_t i = first; i < items; i += step, ++n) {
@@ -477,7 +486,7 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
     const int64_t m = m_next, p = p_next;
     const int h0 = int(c_next) * kQrBackHeads;
     __syncwarp();                                      // the item before has been read: its place takes the next copy
-    if (lane == 0 && i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
+    if (i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
     if (!ok) range = true;
     float4 cs = zero, sn = zero;

@@ -63,14 +63,10 @@ template <int kLanes> __device__ __forceinline__ float head_sum(float v) {
   for (int o = kLanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float4 pick4(bool first, float4 a, float4 b) {
-  return make_float4(first ? a.x : b.x, first ? a.y : b.y, first ? a.z : b.z, first ? a.w : b.w);
-}
-// A head's columns in a lane, and the gains there (ones where there are none).
+// A head's columns in a lane.
 struct QrLane {
   bool on, turned;                  // holds elements; ... of rotated pairs
   int u, lo, hi;                    // lane in the head; its two groups of four columns
-  float4 gq0, gq1, gk0, gk1;
 };
 __device__ __forceinline__ QrLane qr_lane(const QrArgs& a, int u) {
   QrLane l;
@@ -80,18 +76,36 @@ __device__ __forceinline__ QrLane qr_lane(const QrArgs& a, int u) {
   const bool split = l.turned && !a.interleaved;
   l.lo = l.on ? (split ? 4 * u : 8 * u) : 0;
   l.hi = l.on ? (split ? (a.R >> 1) + 4 * u : 8 * u + 4) : 0;
-  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-  l.gq0 = a.gq ? *reinterpret_cast<const float4*>(a.gq + l.lo) : one;
-  l.gq1 = a.gq ? *reinterpret_cast<const float4*>(a.gq + l.hi) : one;
-  l.gk0 = a.gk ? *reinterpret_cast<const float4*>(a.gk + l.lo) : one;
-  l.gk1 = a.gk ? *reinterpret_cast<const float4*>(a.gk + l.hi) : one;
   return l;
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+// The gains at four columns; ones where there are none.
+__device__ __forceinline__ float4 gain4(const float* g, int col) {
+  return g ? *reinterpret_cast<const float4*>(g + col) : make_float4(1.f, 1.f, 1.f, 1.f);
 }
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
-__device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
+// Both gains in shared memory (a CTA's threads; a barrier follows).
+__device__ __forceinline__ void share_gains(const QrArgs& a, float* to) {
+  for (int d = threadIdx.x; d < 2 * a.D; d += blockDim.x) {
+    const float* g = d < a.D ? a.gq : a.gk;
+    to[d] = g ? g[d < a.D ? d : d - a.D] : 1.f;
+  }
+}
+__device__ __forceinline__ float2 lo2(float4 a) { return make_float2(a.x, a.y); }
+__device__ __forceinline__ float2 hi2(float4 a) { return make_float2(a.z, a.w); }
+__device__ __forceinline__ float4 join4(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
+// The eight products' sum, packed: a0 b0 + a1 b1.
+__device__ __forceinline__ float dot8(float4 a0, float4 b0, float4 a1, float4 b1) {
+  float2 t = mul2(lo2(a0), lo2(b0));
+  t = fma2(hi2(a0), hi2(b0), t);
+  t = fma2(lo2(a1), lo2(b1), t);
+  t = fma2(hi2(a1), hi2(b1), t);
+  return t.x + t.y;
+}
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return join4(mul2(lo2(a), lo2(b)), mul2(hi2(a), hi2(b))); }
+__device__ __forceinline__ float4 scale4(float4 a, float s) { return mul4(a, make_float4(s, s, s, s)); }
+__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
+  return join4(fma2(lo2(a), lo2(b), lo2(c)), fma2(hi2(a), hi2(b), hi2(c)));
+}
+__device__ __forceinline__ float4 neg4(float4 a) { return make_float4(-a.x, -a.y, -a.z, -a.w); }
 
 // Rotates the pairs of (lo, hi) by (c, s): split pairs are (lo.x, hi.x) ...,
 // interleaved ones (lo.x, lo.y) ... with c, s of four consecutive pairs.
@@ -104,10 +118,7 @@ __device__ __forceinline__ void rotate(float4& lo, float4& hi, float4 c, float4 
     a = lo;
     b = hi;
   }
-  const float4 x = make_float4(fmaf(a.x, c.x, -(b.x * s.x)), fmaf(a.y, c.y, -(b.y * s.y)), fmaf(a.z, c.z, -(b.z * s.z)),
-                               fmaf(a.w, c.w, -(b.w * s.w)));
-  const float4 y = make_float4(fmaf(a.x, s.x, b.x * c.x), fmaf(a.y, s.y, b.y * c.y), fmaf(a.z, s.z, b.z * c.z),
-                               fmaf(a.w, s.w, b.w * c.w));
+  const float4 x = fma4(a, c, neg4(mul4(b, s))), y = fma4(a, s, mul4(b, c));
   if (interleaved) {
     lo = make_float4(x.x, y.x, x.y, y.y);
     hi = make_float4(x.z, y.z, x.w, y.w);
@@ -148,13 +159,14 @@ qk_norm_rope_kernel(const QrArgs a) {
     const int64_t p = live && a.R ? a.pos[m] : 0;
     const bool ok = p >= 0 && (a.R == 0 || p < a.P);
     if (!ok || at >= (kAppend ? a.nslots : 1)) range = true;
-    const float ss = head_sum<kLanes>(dot4(x, x, dot4(y, y, 0.f)));
+    const float ss = head_sum<kLanes>(dot8(x, x, y, y));
     if (!live || !ok || !l.on) continue;
     if (!(ss <= 3.4028235e38f)) bad = true;            // a sum of squares: not finite if an element is not
     if (!value) {
       const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-      x = mul4(scale4(x, r), pick4(query, l.gq0, l.gk0));
-      y = mul4(scale4(y, r), pick4(query, l.gq1, l.gk1));
+      const float* g = query ? a.gq : a.gk;
+      x = mul4(scale4(x, r), gain4(g, l.lo));
+      y = mul4(scale4(y, r), gain4(g, l.hi));
       if (l.turned)
         rotate(x, y, *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u),
                *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u), a.interleaved != 0);
@@ -186,6 +198,27 @@ qk_norm_rope_kernel(const QrArgs a) {
 // ahead of its work), so that 128 KB an SM are on their way whatever the registers allow.
 constexpr int kQrRing = 3, kQrRingHeads = 8, kQrRingWarps = 8;
 
+// What an item needs besides its rows.
+template <bool kAppend>
+struct QrAhead {
+  int64_t m, c, p, at;
+  float4 cs, sn;
+  __device__ __forceinline__ void ask(const QrArgs& a, int64_t i, int64_t items, int chunks) {
+    m = c = p = 0;
+    at = -1;
+    if (i >= items) return;
+    split_index(i, chunks, items < (int64_t(1) << 31), m, c);
+    if (a.R) p = a.pos[m];
+    if (kAppend) at = a.slots[m];
+  }
+  __device__ __forceinline__ bool fits(const QrArgs& a) const { return p >= 0 && (a.R == 0 || p < a.P); }
+  __device__ __forceinline__ void turn(const QrArgs& a, const QrLane& l) {
+    if (!l.turned || !fits(a)) return;
+    cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * l.u);
+    sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * l.u);
+  }
+};
+
 // What one lane copies of each item: the heads lo .. hi - 1, `size` bytes each, of the token's
 // row at src + m * row, to the item's place `to` on.
 struct QrRun {
@@ -203,6 +236,7 @@ __global__ void __launch_bounds__(32 * kQrRingWarps, 2)
 qk_norm_rope_ring_kernel(const QrArgs a) {
   extern __shared__ __align__(128) unsigned char qr_smem[];
   __shared__ uint64_t full[kQrRingWarps][kQrRing];
+  __shared__ __align__(16) float gains[2 * 256];
   constexpr int kAtOnce = 32 / kLanes;                 // heads that the warp works on at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const QrLane l = qr_lane(a, lane & (kLanes - 1));
@@ -215,7 +249,8 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     for (int i = 0; i < kQrRing; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
-  __syncwarp();
+  share_gains(a, gains);
+  __syncthreads();
   // lanes 0..2 each copy the run of an item's heads that lies in q, k or v
   QrRun run;
   run.src = reinterpret_cast<const unsigned char*>(lane == 0 ? a.q : lane == 1 ? a.k : a.v);
@@ -233,31 +268,28 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     run.copy(reinterpret_cast<unsigned char*>(ring + st * kQrRingHeads * a.D), m, h0, h1, &full[warp][st]);
   };
   bool bad = false, range = false;
-  int64_t m_next = 0, c_next = 0, p_next = 0, at_next = -1;
-  auto ask = [&](int64_t i) {
-    if (i >= items) return;
-    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
-    p_next = a.R ? a.pos[m_next] : 0;
-    if (kAppend) at_next = a.slots[m_next];
-  };
+  // Ahead of the work: an item's token, position and slot two items, its table row (which
+  // follows the position) one.
+  QrAhead<kAppend> one, two;
+  two.ask(a, first, items, chunks);
+  one = two;
+  one.turn(a, l);
+  two.ask(a, first + step, items, chunks);
   for (int k = 0; k < kQrRing - 1; ++k)
     if (first + k * step < items) issue(first + k * step, k);
-  ask(first);
   int n = 0;
   for (int64_t i = first; i < items; i += step, ++n) {
     const int st = n % kQrRing;
-    const int64_t m = m_next, p = p_next, at = at_next;
-    const int h0 = int(c_next) * kQrRingHeads;
+    const QrAhead<kAppend> now = one;
+    one = two;
+    one.turn(a, l);
+    two.ask(a, i + 2 * step, items, chunks);
+    const int64_t m = now.m, at = now.at;
+    const int h0 = int(now.c) * kQrRingHeads;
     __syncwarp();                                      // the item before has been read: its place takes the next copy
     if (i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
-    const bool ok = p >= 0 && (a.R == 0 || p < a.P);
+    const bool ok = now.fits(a);
     if (!ok) range = true;
-    float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), sn = cs;
-    if (l.turned && ok) {
-      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
-      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
-    }
-    ask(i + step);
     T* oq = static_cast<T*>(a.oq) + m * a.Hq * a.D;
     T *ok_, *ov;
     bool store = true;
@@ -282,30 +314,39 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
       break;
     }
     const float* rows = ring + st * kQrRingHeads * a.D;
+    // all passes' sums first, so that their exchanges overlap
+    constexpr int kPasses = kQrRingHeads / kAtOnce;
+    float4 x[kPasses], y[kPasses];
+    float ss[kPasses];
 #pragma unroll
-    for (int b = 0; b < kQrRingHeads; b += kAtOnce) {
-      const int slot = b + lane / kLanes, h = h0 + slot;
-      const bool live = h < heads && l.on, value = h >= nk;
-      const int c0 = value ? 8 * u : l.lo, c1 = value ? 8 * u + 4 : l.hi;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (live) {
-        x = *reinterpret_cast<const float4*>(rows + slot * a.D + c0);
-        y = *reinterpret_cast<const float4*>(rows + slot * a.D + c1);
+    for (int j = 0; j < kPasses; ++j) {
+      const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
+      x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (h < heads && l.on) {
+        x[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + (h < nk ? l.lo : 8 * u));
+        y[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + (h < nk ? l.hi : 8 * u + 4));
       }
-      const float ss = head_sum<kLanes>(dot4(x, x, dot4(y, y, 0.f)));
-      if (!live || !ok) continue;
-      if (!(ss <= 3.4028235e38f)) bad = true;          // a sum of squares: not finite if an element is not
-      if (!value) {
-        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-        const bool query = h < a.Hq;
-        x = mul4(scale4(x, r), pick4(query, l.gq0, l.gk0));
-        y = mul4(scale4(y, r), pick4(query, l.gq1, l.gk1));
-        if (l.turned) rotate(x, y, cs, sn, a.interleaved != 0);
+      ss[j] = head_sum<kLanes>(dot8(x[j], x[j], y[j], y[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < kPasses; ++j) {
+      const int h = h0 + j * kAtOnce + lane / kLanes;
+      if (h >= heads || !l.on || !ok) continue;
+      if (!(ss[j] <= 3.4028235e38f)) bad = true;       // a sum of squares: not finite if an element is not
+      int c0 = 8 * u, c1 = 8 * u + 4;
+      if (h < nk) {
+        const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
+        const float* g = gains + (h < a.Hq ? 0 : a.D);
+        x[j] = mul4(scale4(x[j], r), *reinterpret_cast<const float4*>(g + l.lo));
+        y[j] = mul4(scale4(y[j], r), *reinterpret_cast<const float4*>(g + l.hi));
+        if (l.turned) rotate(x[j], y[j], now.cs, now.sn, a.interleaved != 0);
+        c0 = l.lo;
+        c1 = l.hi;
       }
       if (kAppend && h >= a.Hq && !store) continue;
       T* out = h < a.Hq ? oq + h * a.D : (h < nk ? ok_ : ov) + int64_t(h) * stride;
-      st4(out + c0, x);
-      st4(out + c1, y);
+      st4(out + c0, x[j]);
+      st4(out + c1, y[j]);
     }
   }
   if (bad) raise_status(kDevNonFinite);
@@ -314,8 +355,8 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
 
 // A head's gradient from its row, its rotated-back gradient (e, f) and both sums.
 __device__ __forceinline__ void head_back(const QrArgs& a, const QrLane& l, int h, int nk, float4 x, float4 y, float4 e,
-                                          float4 f, float ss, float tt, float inv_d, float* oq, float* ok, float* ov,
-                                          float4& sq0, float4& sq1, float4& sk0, float4& sk1, bool& bad) {
+                                          float4 f, float4 g0, float4 g1, float ss, float tt, float inv_d, float* oq,
+                                          float* ok, float* ov, float4& sq0, float4& sq1, float4& sk0, float4& sk1, bool& bad) {
   if (h >= nk) {
     float* out = ov + h * a.D + 8 * l.u;
     *reinterpret_cast<float4*>(out) = e;
@@ -328,18 +369,16 @@ __device__ __forceinline__ void head_back(const QrArgs& a, const QrLane& l, int 
   if (!(ss <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
   x = scale4(x, r);
   y = scale4(y, r);
-  const float4 ge = mul4(e, pick4(query, l.gq0, l.gk0)), gf = mul4(f, pick4(query, l.gq1, l.gk1));
+  const float4 nt = make_float4(-t, -t, -t, -t);
   float* out = (query ? oq : ok) + h * a.D;
-  *reinterpret_cast<float4*>(out + l.lo) = make_float4(r * fmaf(-x.x, t, ge.x), r * fmaf(-x.y, t, ge.y),
-                                                       r * fmaf(-x.z, t, ge.z), r * fmaf(-x.w, t, ge.w));
-  *reinterpret_cast<float4*>(out + l.hi) = make_float4(r * fmaf(-y.x, t, gf.x), r * fmaf(-y.y, t, gf.y),
-                                                       r * fmaf(-y.z, t, gf.z), r * fmaf(-y.w, t, gf.w));
+  *reinterpret_cast<float4*>(out + l.lo) = scale4(fma4(x, nt, mul4(e, g0)), r);
+  *reinterpret_cast<float4*>(out + l.hi) = scale4(fma4(y, nt, mul4(f, g1)), r);
   if (query) {
-    sq0 = make_float4(fmaf(e.x, x.x, sq0.x), fmaf(e.y, x.y, sq0.y), fmaf(e.z, x.z, sq0.z), fmaf(e.w, x.w, sq0.w));
-    sq1 = make_float4(fmaf(f.x, y.x, sq1.x), fmaf(f.y, y.y, sq1.y), fmaf(f.z, y.z, sq1.z), fmaf(f.w, y.w, sq1.w));
+    sq0 = fma4(e, x, sq0);
+    sq1 = fma4(f, y, sq1);
   } else {
-    sk0 = make_float4(fmaf(e.x, x.x, sk0.x), fmaf(e.y, x.y, sk0.y), fmaf(e.z, x.z, sk0.z), fmaf(e.w, x.w, sk0.w));
-    sk1 = make_float4(fmaf(f.x, y.x, sk1.x), fmaf(f.y, y.y, sk1.y), fmaf(f.z, y.z, sk1.z), fmaf(f.w, y.w, sk1.w));
+    sk0 = fma4(e, x, sk0);
+    sk1 = fma4(f, y, sk1);
   }
 }
 
@@ -412,12 +451,12 @@ qk_norm_rope_backward_kernel(const QrArgs a) {
       rotate(e, f, cs, make_float4(-sn.x, -sn.y, -sn.z, -sn.w), a.interleaved != 0);
     }
     // both sums at once: sum x^2, and sum x g dy, of which mean(x g dy r) is r / D times
-    const bool query = h < a.Hq;
-    const float ss = head_sum<kLanes>(dot4(x, x, dot4(y, y, 0.f)));
-    const float tt = head_sum<kLanes>(dot4(mul4(e, pick4(query, l.gq0, l.gk0)), x,
-                                           dot4(mul4(f, pick4(query, l.gq1, l.gk1)), y, 0.f)));
+    const float* g = h < a.Hq ? a.gq : a.gk;
+    const float4 g0 = gain4(g, l.lo), g1 = gain4(g, l.hi);
+    const float ss = head_sum<kLanes>(dot8(x, x, y, y));
+    const float tt = head_sum<kLanes>(dot8(mul4(e, g0), x, mul4(f, g1), y));
     if (work)
-      head_back(a, l, h, nk, x, y, e, f, ss, tt, inv_d, a.dxq + m * a.lddq, a.dxk + m * a.lddk - int64_t(a.Hq) * a.D,
+      head_back(a, l, h, nk, x, y, e, f, g0, g1, ss, tt, inv_d, a.dxq + m * a.lddq, a.dxk + m * a.lddk - int64_t(a.Hq) * a.D,
                 a.dxv + m * a.lddv - int64_t(nk) * a.D, sq0, sq1, sk0, sk1, bad);
   }
   if (bad) raise_status(kDevNonFinite);
@@ -434,6 +473,7 @@ __global__ void __launch_bounds__(32 * kQrRingWarps, 2)
 qk_norm_rope_backward_ring_kernel(const QrArgs a) {
   extern __shared__ __align__(128) unsigned char qr_smem[];
   __shared__ uint64_t full[kQrRingWarps][kQrRing];
+  __shared__ __align__(16) float gains[2 * 256];
   constexpr int kAtOnce = 32 / kLanes, kGroups = kQrRingWarps * kAtOnce;
   constexpr int kPasses = (kQrBackHeads + kAtOnce - 1) / kAtOnce;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -448,7 +488,8 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
     for (int i = 0; i < kQrRing; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
-  __syncwarp();
+  share_gains(a, gains);
+  __syncthreads();
   // lanes 0..4 each copy a run of an item's heads: the rows of q and k, the gradients of all three
   const int size = int(sizeof(T));
   QrRun run;
@@ -471,31 +512,26 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
   bool bad = false, range = false;
-  int64_t m_next = 0, c_next = 0, p_next = 0;
-  auto ask = [&](int64_t i) {
-    if (i >= items) return;
-    split_index(i, chunks, items < (int64_t(1) << 31), m_next, c_next);
-    p_next = a.R ? a.pos[m_next] : 0;
-  };
+  QrAhead<false> one, two;
+  two.ask(a, first, items, chunks);
+  one = two;
+  one.turn(a, l);
+  two.ask(a, first + step, items, chunks);
   for (int k = 0; k < kQrRing - 1; ++k)
     if (first + k * step < items) issue(first + k * step, k);
-  ask(first);
   int n = 0;
   for (int64_t i = first; i < items; i += step, ++n) {
     const int st = n % kQrRing;
-    const int64_t m = m_next, p = p_next;
-    const int h0 = int(c_next) * kQrBackHeads;
+    const QrAhead<false> now = one;
+    one = two;
+    one.turn(a, l);
+    two.ask(a, i + 2 * step, items, chunks);
+    const int64_t m = now.m;
+    const int h0 = int(now.c) * kQrBackHeads;
     __syncwarp();                                      // the item before has been read: its place takes the next copy
     if (i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
-    const bool ok = p >= 0 && (a.R == 0 || p < a.P);
+    const bool ok = now.fits(a);
     if (!ok) range = true;
-    float4 cs = zero, sn = zero;
-    if (l.turned && ok) {
-      cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u);
-      sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u);
-      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
-    }
-    ask(i + step);
     float* oq = a.dxq + m * a.lddq;
     float* okk = a.dxk + m * a.lddk - int64_t(a.Hq) * a.D;
     float* ov = a.dxv + m * a.lddv - int64_t(nk) * a.D;
@@ -520,19 +556,21 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
         if (!value) {
           x[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + l.lo);
           y[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + l.hi);
-          if (l.turned) rotate(e[j], f[j], cs, sn, a.interleaved != 0);
+          if (l.turned) rotate(e[j], f[j], now.cs, neg4(now.sn), a.interleaved != 0);
         }
       }
-      const bool query = h < a.Hq;
-      ss[j] = head_sum<kLanes>(dot4(x[j], x[j], dot4(y[j], y[j], 0.f)));
-      tt[j] = head_sum<kLanes>(dot4(mul4(e[j], pick4(query, l.gq0, l.gk0)), x[j],
-                                    dot4(mul4(f[j], pick4(query, l.gq1, l.gk1)), y[j], 0.f)));
+      const float* g = gains + (h < a.Hq ? 0 : a.D);
+      ss[j] = head_sum<kLanes>(dot8(x[j], x[j], y[j], y[j]));
+      tt[j] = head_sum<kLanes>(dot8(mul4(e[j], *reinterpret_cast<const float4*>(g + l.lo)), x[j],
+                                    mul4(f[j], *reinterpret_cast<const float4*>(g + l.hi)), y[j]));
     }
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
       const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
+      const float* g = gains + (h < a.Hq ? 0 : a.D);
       if (slot < kQrBackHeads && h < heads && l.on && ok)
-        head_back(a, l, h, nk, x[j], y[j], e[j], f[j], ss[j], tt[j], inv_d, oq, okk, ov, sq0, sq1, sk0, sk1, bad);
+        head_back(a, l, h, nk, x[j], y[j], e[j], f[j], *reinterpret_cast<const float4*>(g + l.lo),
+                  *reinterpret_cast<const float4*>(g + l.hi), ss[j], tt[j], inv_d, oq, okk, ov, sq0, sq1, sk0, sk1, bad);
     }
   }
   if (bad) raise_status(kDevNonFinite);

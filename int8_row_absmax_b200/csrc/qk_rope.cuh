@@ -198,24 +198,38 @@ qk_norm_rope_kernel(const QrArgs a) {
 // ahead of its work), so that 128 KB an SM are on their way whatever the registers allow.
 constexpr int kQrRing = 3, kQrRingHeads = 8, kQrRingWarps = 8;
 
+// An item of a warp: chunk c of token m; stepping from one to the next takes no division.
+struct QrItem {
+  int m, c, dm, dc;
+  __device__ __forceinline__ QrItem(int64_t first, int64_t step, int chunks)
+      : m(int(first / chunks)), c(int(first % chunks)), dm(int(step / chunks)), dc(int(step % chunks)) {}
+  __device__ __forceinline__ void next(int chunks) {
+    m += dm;
+    c += dc;
+    if (c >= chunks) {
+      c -= chunks;
+      ++m;
+    }
+  }
+};
 // What an item needs besides its rows.
 template <bool kAppend>
 struct QrAhead {
-  int64_t m, c, p, at;
+  int m, c, p;
+  int64_t at;
   float4 cs, sn;
-  __device__ __forceinline__ void ask(const QrArgs& a, int64_t i, int64_t items, int chunks) {
-    m = c = p = 0;
-    at = -1;
-    if (i >= items) return;
-    split_index(i, chunks, items < (int64_t(1) << 31), m, c);
-    if (a.R) p = a.pos[m];
-    if (kAppend) at = a.slots[m];
+  __device__ __forceinline__ void ask(const QrArgs& a, const QrItem& i, bool live) {
+    m = i.m;
+    c = i.c;
+    p = live && a.R ? a.pos[m] : 0;
+    if (kAppend) at = live ? a.slots[m] : -1;
   }
   __device__ __forceinline__ bool fits(const QrArgs& a) const { return p >= 0 && (a.R == 0 || p < a.P); }
   __device__ __forceinline__ void turn(const QrArgs& a, const QrLane& l) {
     if (!l.turned || !fits(a)) return;
-    cs = *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * l.u);
-    sn = *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * l.u);
+    const float* t = a.table + int64_t(p) * a.R + 4 * l.u;
+    cs = *reinterpret_cast<const float4*>(t);
+    sn = *reinterpret_cast<const float4*>(t + (a.R >> 1));
   }
 };
 
@@ -225,9 +239,9 @@ struct QrRun {
   const unsigned char* src;
   int64_t row;
   int lo, hi, size, to;
-  __device__ __forceinline__ void copy(unsigned char* stage, int64_t m, int h0, int h1, uint64_t* bar) const {
+  __device__ __forceinline__ void copy(unsigned char* stage, int m, int h0, int h1, uint64_t* bar) const {
     const int a = max(lo, h0), b = min(hi, h1);
-    if (a < b) bulk_g2s(stage + to + (a - h0) * size, src + m * row + int64_t(a - lo) * size, uint32_t((b - a) * size), bar);
+    if (a < b) bulk_g2s(stage + to + (a - h0) * size, src + int64_t(m) * row + (a - lo) * size, uint32_t((b - a) * size), bar);
   }
 };
 
@@ -259,38 +273,41 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
   run.hi = lane == 0 ? a.Hq : lane == 1 ? nk : lane == 2 ? heads : 0;
   run.size = a.D * 4;
   run.to = 0;
-  auto issue = [&](int64_t i, int st) {
-    int64_t m, c;
-    split_index(i, chunks, items < (int64_t(1) << 31), m, c);
-    const int h0 = int(c) * kQrRingHeads, h1 = min(h0 + kQrRingHeads, heads);
+  auto issue = [&](const QrItem& i, int st) {
+    const int h0 = i.c * kQrRingHeads, h1 = min(h0 + kQrRingHeads, heads);
     if (lane == 0) mbar_arrive_expect_tx(&full[warp][st], uint32_t((h1 - h0) * a.D * 4));
     __syncwarp();
-    run.copy(reinterpret_cast<unsigned char*>(ring + st * kQrRingHeads * a.D), m, h0, h1, &full[warp][st]);
+    run.copy(reinterpret_cast<unsigned char*>(ring + st * kQrRingHeads * a.D), i.m, h0, h1, &full[warp][st]);
   };
   bool bad = false, range = false;
   // Ahead of the work: an item's token, position and slot two items, its table row (which
   // follows the position) one.
+  static_assert(kQrRing == 3, "copies and questions run two items ahead");
+  QrItem item(first, step, chunks);
   QrAhead<kAppend> one, two;
-  two.ask(a, first, items, chunks);
-  one = two;
+  one.ask(a, item, first < items);
+  if (first < items) issue(item, 0);
   one.turn(a, l);
-  two.ask(a, first + step, items, chunks);
-  for (int k = 0; k < kQrRing - 1; ++k)
-    if (first + k * step < items) issue(first + k * step, k);
+  item.next(chunks);
+  two.ask(a, item, first + step < items);
+  if (first + step < items) issue(item, 1);
   int n = 0;
   for (int64_t i = first; i < items; i += step, ++n) {
     const int st = n % kQrRing;
     const QrAhead<kAppend> now = one;
+    const bool more = i + 2 * step < items;
+    item.next(chunks);
     one = two;
     one.turn(a, l);
-    two.ask(a, i + 2 * step, items, chunks);
-    const int64_t m = now.m, at = now.at;
-    const int h0 = int(now.c) * kQrRingHeads;
+    two.ask(a, item, more);
+    const int m = now.m;
+    const int64_t at = now.at;
+    const int h0 = now.c * kQrRingHeads;
     __syncwarp();                                      // the item before has been read: its place takes the next copy
-    if (i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
+    if (more) issue(item, (n + 2) % kQrRing);
     const bool ok = now.fits(a);
     if (!ok) range = true;
-    T* oq = static_cast<T*>(a.oq) + m * a.Hq * a.D;
+    T* oq = static_cast<T*>(a.oq) + int64_t(m) * (a.Hq * a.D);
     T *ok_, *ov;
     bool store = true;
     int stride = a.D;
@@ -304,8 +321,9 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
       ok_ = static_cast<T*>(a.ok) + to - int64_t(a.Hq) * stride;
       ov = static_cast<T*>(a.ov) + to - int64_t(nk) * stride;
     } else {
-      ok_ = static_cast<T*>(a.ok) + (m * a.Hkv - a.Hq) * a.D;
-      ov = static_cast<T*>(a.ov) + (m * a.Hkv - nk) * a.D;
+      const int64_t to = int64_t(m) * (a.Hkv * a.D);
+      ok_ = static_cast<T*>(a.ok) + to - a.Hq * a.D;
+      ov = static_cast<T*>(a.ov) + to - nk * a.D;
     }
     if (__any_sync(0xffffffffu, !mbar_wait_near(&full[warp][st], uint32_t(n / kQrRing) & 1u))) {
       if (lane == 0) raise_status(kDevTimeout);        // and no copy left in flight
@@ -315,14 +333,14 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     }
     const float* rows = ring + st * kQrRingHeads * a.D;
     // all passes' sums first, so that their exchanges overlap
-    constexpr int kPasses = kQrRingHeads / kAtOnce;
+    constexpr int kPasses = (kQrRingHeads + kAtOnce - 1) / kAtOnce;
     float4 x[kPasses], y[kPasses];
     float ss[kPasses];
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
       const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
       x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h < heads && l.on) {
+      if (slot < kQrRingHeads && h < heads && l.on) {
         x[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + (h < nk ? l.lo : 8 * u));
         y[j] = *reinterpret_cast<const float4*>(rows + slot * a.D + (h < nk ? l.hi : 8 * u + 4));
       }
@@ -330,8 +348,8 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < kPasses; ++j) {
-      const int h = h0 + j * kAtOnce + lane / kLanes;
-      if (h >= heads || !l.on || !ok) continue;
+      const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
+      if (slot >= kQrRingHeads || h >= heads || !l.on || !ok) continue;
       if (!(ss[j] <= 3.4028235e38f)) bad = true;       // a sum of squares: not finite if an element is not
       int c0 = 8 * u, c1 = 8 * u + 4;
       if (h < nk) {
@@ -500,36 +518,38 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
   run.hi = lane == 0 || lane == 2 ? a.Hq : lane == 4 ? heads : lane < 4 ? nk : 0;
   run.size = a.D * (lane < 2 ? 4 : size);
   run.to = lane < 2 ? 0 : x_bytes;
-  auto issue = [&](int64_t i, int st) {
-    int64_t m, c;
-    split_index(i, chunks, items < (int64_t(1) << 31), m, c);
-    const int h0 = int(c) * kQrBackHeads, h1 = min(h0 + kQrBackHeads, heads);
+  auto issue = [&](const QrItem& i, int st) {
+    const int h0 = i.c * kQrBackHeads, h1 = min(h0 + kQrBackHeads, heads);
     if (lane == 0)
       mbar_arrive_expect_tx(&full[warp][st], uint32_t(max(0, min(h1, nk) - h0) * a.D * 4 + (h1 - h0) * a.D * size));
     __syncwarp();
-    run.copy(ring + st * stage, m, h0, h1, &full[warp][st]);
+    run.copy(ring + st * stage, i.m, h0, h1, &full[warp][st]);
   };
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
   bool bad = false, range = false;
+  static_assert(kQrRing == 3, "copies and questions run two items ahead");
+  QrItem item(first, step, chunks);
   QrAhead<false> one, two;
-  two.ask(a, first, items, chunks);
-  one = two;
+  one.ask(a, item, first < items);
+  if (first < items) issue(item, 0);
   one.turn(a, l);
-  two.ask(a, first + step, items, chunks);
-  for (int k = 0; k < kQrRing - 1; ++k)
-    if (first + k * step < items) issue(first + k * step, k);
+  item.next(chunks);
+  two.ask(a, item, first + step < items);
+  if (first + step < items) issue(item, 1);
   int n = 0;
   for (int64_t i = first; i < items; i += step, ++n) {
     const int st = n % kQrRing;
     const QrAhead<false> now = one;
+    const bool more = i + 2 * step < items;
+    item.next(chunks);
     one = two;
     one.turn(a, l);
-    two.ask(a, i + 2 * step, items, chunks);
-    const int64_t m = now.m;
-    const int h0 = int(now.c) * kQrBackHeads;
+    two.ask(a, item, more);
+    const int m = now.m;
+    const int h0 = now.c * kQrBackHeads;
     __syncwarp();                                      // the item before has been read: its place takes the next copy
-    if (i + (kQrRing - 1) * step < items) issue(i + (kQrRing - 1) * step, (n + kQrRing - 1) % kQrRing);
+    if (more) issue(item, (n + 2) % kQrRing);
     const bool ok = now.fits(a);
     if (!ok) range = true;
     float* oq = a.dxq + m * a.lddq;

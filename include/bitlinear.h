@@ -406,7 +406,7 @@ bl_status bl_rope_table(float* table, int64_t P, int R, double base, cudaStream_
 
 /* Rows of queries, keys and values as the projections write them. */
 typedef struct {
-  int64_t M;                  /* tokens */
+  int64_t M;                  /* tokens, < 2^29 */
   int32_t Hq, Hkv, D;
   const float *q, *k, *v;     /* [M, Hq D], [M, Hkv D], [M, Hkv D] float32, 16-byte aligned */
   int64_t ldq, ldk, ldv;      /* floats between tokens, multiples of 4 (one fused projection: all the same) */
@@ -422,7 +422,8 @@ typedef struct {
 /* Per-head RMSNorm of queries and keys with the position rotation in the same
  * pass: y = x / sqrt(mean(x^2) + eps) * g over each head's D elements, then the
  * pairs (a, b) of its first R elements become (a cos - b sin, a sin + b cos).
- * Values are converted only.  q [M, Hq, D], k and v [M, Hkv, D]: contiguous
+ * Values are converted only.  A query or key head whose squares overflow float32
+ * counts as not finite.  q [M, Hq, D], k and v [M, Hkv, D]: contiguous
  * outputs of type t (any bl_dtype), 16-byte aligned.  Here D may be up to 256.
  * Rows of a token whose position is out of range are not written. */
 bl_status bl_qk_norm_rope(const bl_qkv_rows* rows, bl_dtype t, void* q, void* k, void* v, cudaStream_t stream);
@@ -433,7 +434,7 @@ typedef struct {
   bl_dtype t;                 /* BL_T_F16 or BL_T_BF16 */
   void *k, *v;                /* [pages, Hkv, page, D] contiguous, 16-byte aligned */
   int64_t pages;
-  int32_t page;               /* tokens per page, >= 1 */
+  int32_t page;               /* tokens per page, >= 1; page * D < 2^31 */
   int32_t Hkv, D;
 } bl_kv_pages;
 
@@ -468,7 +469,7 @@ typedef struct {
   int32_t Hq, Hkv, D;
   const void *q, *k, *v;      /* [Tq, Hq, D], [Tk, Hkv, D], [Tk, Hkv, D]; heads D apart, 16-byte aligned */
   int64_t ldq, ldk, ldv;      /* elements between tokens, multiples of 8 */
-  int64_t Tq, Tk;             /* rows of the buffers (< 2^30) */
+  int64_t Tq, Tk;             /* rows of the buffers (< 2^29) */
   const int32_t *cu_q, *cu_k; /* [B + 1], not falling, within 0 .. Tq and 0 .. Tk */
   int32_t B;
   int32_t max_q, max_k;       /* at least the longest Lq and Lk (max_k: the backward only) */

@@ -15,7 +15,7 @@ namespace bl {
 namespace {
 
 constexpr int kAttnMaxD = 128, kRopeMaxD = 256;
-constexpr int64_t kAttnMaxRows = int64_t(1) << 30;      // sums of two positions stay within 31 bits
+constexpr int64_t kAttnMaxRows = int64_t(1) << 29;      // sums of three positions stay within 31 bits
 
 bool half_type(bl_dtype t) { return t == BL_T_F16 || t == BL_T_BF16; }
 bool any_type(bl_dtype t) { return t == BL_T_F32 || half_type(t); }
@@ -54,7 +54,7 @@ bool launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cud
 // ---- norms and rotation ----------------------------------------------------------
 bl_status check_rows(const bl_qkv_rows* r, bool values) {
   if (!r) return BL_ERR_INVALID_ARG;
-  if (r->M < 0 || !int32_max(r->M) || r->Hq < 1 || r->Hkv < 1 || r->Hq > 65535 || r->Hkv > 65535 ||
+  if (r->M < 0 || r->M >= kAttnMaxRows || r->Hq < 1 || r->Hkv < 1 || r->Hq > 65535 || r->Hkv > 65535 ||
       r->Hq % r->Hkv != 0)
     return BL_ERR_INVALID_ARG;
   if (r->D < 8 || r->D % 8 != 0 || r->D > kRopeMaxD) return BL_ERR_INVALID_ARG;
@@ -163,7 +163,7 @@ bl_status launch_norm_rope_back(const QrArgs& a, int grid, cudaStream_t st) {
 bl_status check_cache(const bl_kv_pages* c) {
   if (!c || !c->k || !c->v || !half_type(c->t)) return BL_ERR_INVALID_ARG;
   if (c->pages < 1 || !int32_max(c->pages) || c->page < 1 || c->Hkv < 1 || c->Hkv > 65535) return BL_ERR_INVALID_ARG;
-  if (c->D < 8 || c->D % 8 != 0) return BL_ERR_INVALID_ARG;
+  if (c->D < 8 || c->D % 8 != 0 || !int32_max(int64_t(c->page) * c->D)) return BL_ERR_INVALID_ARG;
   if (!is_aligned(c->k, 16) || !is_aligned(c->v, 16)) return BL_ERR_ALIGNMENT;
   return BL_OK;
 }
@@ -204,8 +204,8 @@ AttnArgs attn_args(const bl_attn_call* c) {
   a.Hkv = c->Hkv;
   a.D = c->D;
   a.B = c->B;
-  a.max_q = c->max_q;
-  a.max_k = c->max_k;
+  a.max_q = c->max_q < 1 ? 1 : c->max_q;                 // at least one block, to find sequences that are longer
+  a.max_k = c->max_k < 1 ? 1 : c->max_k;
   a.window = c->window >= c->Tk ? 0 : c->window;         // no window at all, then
   a.sinks = c->sinks;
   a.scale = c->scale;
@@ -261,7 +261,7 @@ constexpr size_t kAbNormBytes = 256;
 // the parts would cost more than the evener load gives: not split).
 int dkv_splits(const bl_attn_call* c) {
   const int group = c->Hq / c->Hkv;
-  const int64_t ctas = int64_t(c->Hkv) * c->B * ceil_div(c->max_k, 128);
+  const int64_t ctas = int64_t(c->Hkv) * c->B * ceil_div(c->max_k < 1 ? 1 : c->max_k, 128);
   if (ctas < 1 || ctas >= 148) return 1;
   const int64_t want = 296 / ctas < group ? 296 / ctas : group;
   const int64_t heads = ceil_div(group, want);
@@ -445,7 +445,7 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
 bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStream_t stream) {
   const bl_status st = check_attn(call);
   if (st != BL_OK) return st;
-  if (call->B == 0 || call->Tq == 0 || call->max_q == 0) return BL_OK;
+  if (call->B == 0 || call->Tq == 0) return BL_OK;
   if (!out) return BL_ERR_INVALID_ARG;
   if (!is_aligned(out, 16) || !is_aligned(lse, 4)) return BL_ERR_ALIGNMENT;
   AttnArgs a = attn_args(call);

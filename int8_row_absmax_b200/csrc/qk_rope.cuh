@@ -105,6 +105,16 @@ __device__ __forceinline__ float4 scale4(float4 a, float s) { return mul4(a, mak
 __device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
   return join4(fma2(lo2(a), lo2(b), lo2(c)), fma2(hi2(a), hi2(b), hi2(c)));
 }
+constexpr float kMaxF32 = 3.4028235e38f;
+// Whether a head's row is not finite, from its sum of squares; for values, whose large
+// squares may overflow while they are fine, from the elements then.
+__device__ __forceinline__ bool not_finite(float ss, bool value, float4 x, float4 y) {
+  if (ss <= kMaxF32) return false;
+  auto in = [](float4 a) {
+    return fabsf(a.x) <= kMaxF32 && fabsf(a.y) <= kMaxF32 && fabsf(a.z) <= kMaxF32 && fabsf(a.w) <= kMaxF32;
+  };
+  return !value || !in(x) || !in(y);
+}
 __device__ __forceinline__ float4 neg4(float4 a) { return make_float4(-a.x, -a.y, -a.z, -a.w); }
 
 // Rotates the pairs of (lo, hi) by (c, s): split pairs are (lo.x, hi.x) ...,
@@ -161,7 +171,7 @@ qk_norm_rope_kernel(const QrArgs a) {
     if (!ok || at >= (kAppend ? a.nslots : 1)) range = true;
     const float ss = head_sum<kLanes>(dot8(x, x, y, y));
     if (!live || !ok || !l.on) continue;
-    if (!(ss <= 3.4028235e38f)) bad = true;            // a sum of squares: not finite if an element is not
+    if (not_finite(ss, value, x, y)) bad = true;
     if (!value) {
       const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
       const float* g = query ? a.gq : a.gk;
@@ -350,7 +360,7 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     for (int j = 0; j < kPasses; ++j) {
       const int slot = j * kAtOnce + lane / kLanes, h = h0 + slot;
       if (slot >= kQrRingHeads || h >= heads || !l.on || !ok) continue;
-      if (!(ss[j] <= 3.4028235e38f)) bad = true;       // a sum of squares: not finite if an element is not
+      if (not_finite(ss[j], h >= nk, x[j], y[j])) bad = true;
       int c0 = 8 * u, c1 = 8 * u + 4;
       if (h < nk) {
         const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
@@ -384,7 +394,7 @@ __device__ __forceinline__ void head_back(const QrArgs& a, const QrLane& l, int 
   const bool query = h < a.Hq;
   const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
   const float t = tt * inv_d * r;
-  if (!(ss <= 3.4028235e38f) || !(fabsf(t) <= 3.4028235e38f)) bad = true;
+  if (!(ss <= kMaxF32) || !(fabsf(t) <= kMaxF32)) bad = true;
   x = scale4(x, r);
   y = scale4(y, r);
   const float4 nt = make_float4(-t, -t, -t, -t);

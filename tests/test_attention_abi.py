@@ -55,7 +55,7 @@ def call(**kw):
     return ctypes.byref(attn.AttnCall(**d))
 
 
-BAD_ROWS = [(dict(M=-1), INVALID), (dict(Hq=5), INVALID), (dict(Hkv=0), INVALID), (dict(D=12), INVALID),
+BAD_ROWS = [(dict(M=-1), INVALID), (dict(M=1 << 29), INVALID), (dict(Hq=5), INVALID), (dict(Hkv=0), INVALID), (dict(D=12), INVALID),
             (dict(D=264), INVALID), (dict(R=12), INVALID), (dict(R=40), INVALID), (dict(R=-8), INVALID),
             (dict(interleaved=2), INVALID), (dict(eps=0.0), INVALID), (dict(eps=float("nan")), INVALID),
             (dict(P=0), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(pos=None), INVALID),
@@ -84,7 +84,8 @@ def test_norm_rope_more_refusals(lib):
     assert f(rows(), 2, 16, 24, 16, NULL) == ALIGN
     assert f(rows(M=0, q=None, k=None, v=None, pos=None, table=None), 2, NULL, NULL, NULL, NULL) == OK
     for kw, e in ((dict(t=0), INVALID), (dict(k=None), INVALID), (dict(pages=0), INVALID), (dict(page=0), INVALID),
-                  (dict(Hkv=1), INVALID), (dict(D=64), INVALID), (dict(v=24), ALIGN)):
+                  (dict(Hkv=1), INVALID), (dict(D=64), INVALID), (dict(page=1 << 26), INVALID),
+                  (dict(v=24), ALIGN)):
         assert ap(rows(), 16, pages(**kw), 16, NULL) == e
     assert ap(rows(), 16, NULL, 16, NULL) == INVALID
     assert ap(rows(), 16, pages(), NULL, NULL) == INVALID
@@ -107,7 +108,7 @@ def test_rope_table_refusals(lib):
 
 
 BAD_CALLS = [(dict(t=0), INVALID), (dict(Hq=3), INVALID), (dict(D=60), INVALID), (dict(D=136), INVALID),
-             (dict(Tq=-1), INVALID), (dict(Tk=1 << 31), INVALID), (dict(B=-1), INVALID), (dict(window=-1), INVALID),
+             (dict(Tq=-1), INVALID), (dict(Tk=1 << 29), INVALID), (dict(B=-1), INVALID), (dict(window=-1), INVALID),
              (dict(sinks=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
              (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(cu_q=None), INVALID), (dict(cu_k=None), INVALID),
              (dict(ldq=248), INVALID), (dict(ldv=120), INVALID), (dict(ldq=260), ALIGN), (dict(k=24), ALIGN),

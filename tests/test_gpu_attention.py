@@ -184,6 +184,21 @@ def test_norm_rope_reports_nonfinite(bl):
             assert torch.equal(a[[0, 1, 3]], b[[0, 1, 3]])
 
 
+@pytest.mark.parametrize("m", [3, 5000])
+def test_large_values_are_no_error(bl, m):
+    """A value's square may overflow float32: values are only converted."""
+    import torch
+    qkv, pos, gq, gk = rows(8, m, 2, 1, 32, 32)
+    qkv[1, 96:] = 1e25
+    table = bl.rope_table(5000, 32)
+    v = bl.qk_norm_rope(qkv, 2, 1, 32, pos, table, gq, gk)[2]
+    ok(bl)
+    assert torch.equal(v[1, 0], qkv[1, 96:].bfloat16())
+    qkv[1, 100] = float("-inf")
+    bl.qk_norm_rope(qkv, 2, 1, 32, pos, table, gq, gk)
+    assert bl.sync_status() == "BL_ERR_NONFINITE"
+
+
 @pytest.mark.parametrize("m,hq,hk,d,rot,inter,dtype", SHAPES)
 def test_norm_rope_backward(bl, m, hq, hk, d, rot, inter, dtype):
     qkv, pos, gq, gk = rows(m + d, m, hq, hk, d, rot)
@@ -360,6 +375,25 @@ def test_bad_bounds_are_reported(bl):
     bl.attention(q, k, v, bad, ck, 60, out=out)
     assert bl.sync_status() == "BL_ERR_RANGE"
     assert torch.equal(out[:50], want[:50]) and (out[50:] == 3).all()
+
+
+def test_nothing_but_empty_sequences(bl):
+    import torch
+    q, k, v, _, _ = packed(6, [5], [7], 2, 1, 64, "float16")
+    zero = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 2.0), torch.full((2, 5), 3.0, device="cuda")
+    bl.attention(q, k, v, zero, zero, 0, out=out, lse=lse)
+    grads = tuple(torch.full_like(t, 4.0) for t in (q, k, k))
+    bl.attention_backward(q, q, k, v, out, lse, zero, zero, 0, 0, grads=grads)
+    ok(bl)
+    assert (out == 2).all() and (lse == 3).all() and all((g == 4).all() for g in grads)
+    # keys without queries: their gradients are zero
+    cq, ck = zero[:2].contiguous(), torch.tensor([0, 7], dtype=torch.int32, device="cuda")
+    empty = q[:0].contiguous()
+    o, l = bl.attention(empty, k, v, cq, ck, 0)
+    dq, dk, dv = bl.attention_backward(o, empty, k, v, o, l, cq, ck, 0, 7)
+    ok(bl)
+    assert o.shape == (0, 2, 64) and dq.shape == o.shape and not dk.any() and not dv.any()
 
 
 def check_backward(q, k, v, cq, ck, window, sinks, out, lse, dout, grads, dtype):
@@ -667,6 +701,34 @@ def test_other_stream_and_graph(bl):
     for x, y in zip(held, run()):
         assert torch.equal(x, y)
     ok(bl)
+
+
+def test_two_streams_at_once(bl):
+    """Calls that overlap on the GPU, each with a workspace of its own."""
+    import torch
+    lens = [3000, 77, 5000]
+    a = paged(4, lens, 8, 2, 64, 16, "bfloat16")[:5]
+    b = paged(9, lens, 8, 2, 64, 16, "bfloat16")[:5]
+    f = packed(7, [900, 133], [900, 133], 4, 2, 64, "float16")
+    dout = normal(9, *f[0].shape, dtype="float16")
+    size = bl.paged_attention_workspace_size(3, 8, a[1])
+
+    def step(x, ws):
+        out, lse = bl.attention(*f, 900)
+        return [bl.paged_attention(*x, ws=ws), out, *bl.attention_backward(dout, *f[:3], out, lse, *f[3:], 900, 900)]
+    want = [step(x, bl.workspace(size, "cuda")) for x in (a, b)]
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [bl.workspace(size, "cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(10):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i] = step(x, spaces[i])
+    torch.cuda.synchronize()
+    ok(bl)
+    for x, y in zip(got, want):
+        for s, t in zip(x, y):
+            assert torch.equal(s, t)
 
 
 def test_binding_refusals(bl):

@@ -100,16 +100,26 @@ QrArgs rows_args(const bl_qkv_rows* r) {
 // Lanes that share a head: the power of two from 4 to 32 that covers D / 8.
 int rows_lanes(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// The ring kernel once its items fill the SMs' warps twice, the one of single heads
-// below, where latency counts.
+// Whether rows go through a ring kernel, whose items are up to `per` heads of a token: once
+// the items fill the warps that an SM holds of it twice, and are themselves half full.  Both
+// sides measured, ring kernel against the one of single heads, us: 48 heads of 128, 512
+// tokens 6.6 / 6.0, 768 tokens 7.4 / 7.9, 4096 tokens 29.6 / 30.3; their gradients 256 tokens
+// 9.2 / 8.9, 512 tokens 11.5 / 12.7, 4096 tokens 44 / 76; 30 heads of 64, 2048 tokens 7.2 /
+// 7.1, 26041 tokens 56 / 65; 12 heads of 32 (items 3/8 full), 130208 tokens 86 / 72.
+bool rows_by_ring(int64_t M, int heads, int per, int64_t warps) {
+  const int64_t chunks = ceil_div(heads, per);
+  return M * chunks >= 2 * warps && 2 * int64_t(heads) >= chunks * per;
+}
+
 template <typename T, bool kAppend, int kLanes>
 bl_status launch_rows(const QrArgs& a, cudaStream_t st) {
   constexpr int kPerBlock = kQrThreads / kLanes;
   const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t items = a.M * ceil_div(heads, kQrRingHeads);
-  if (items >= int64_t(num_sms()) * 4 * kQrRingWarps) {
+  const int64_t items = a.M * ceil_div(heads, QrRing<kLanes>::kHeads);
+  if (rows_by_ring(a.M, heads, QrRing<kLanes>::kHeads, int64_t(num_sms()) * 2 * kQrRingWarps)) {
     static std::atomic<uint64_t> done{0};
-    const int most = kQrRingWarps * kQrRing * kQrRingHeads * 8 * kLanes * 4, smem = most / (8 * kLanes) * a.D;
+    constexpr int kPerD = kQrRingWarps * kQrRing * QrRing<kLanes>::kHeads * 4, most = kPerD * 8 * kLanes;   // at most 96 KB
+    const int smem = kPerD * a.D;
     if (!allow_smem(qk_norm_rope_ring_kernel<T, kAppend, kLanes>, most, done)) return BL_ERR_CUDA;
     const int64_t per_sm = 220 * 1024 / smem;
     const int64_t cap = int64_t(num_sms()) * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm), grid = ceil_div(items, kQrRingWarps);
@@ -136,13 +146,12 @@ int rows_back_grid(const bl_qkv_rows* r) {
   return int(g < 1 ? 1 : g < kQrBackCtas ? g : kQrBackCtas);
 }
 
-// As launch_rows.
 template <typename T, int kLanes>
 bl_status launch_rows_back(const QrArgs& a, int grid, cudaStream_t st) {
   constexpr int kPerBlock = kQrThreads / kLanes;
-  if (a.M * ceil_div(a.Hq + 2 * int64_t(a.Hkv), kQrBackHeads) >= int64_t(grid) * kQrRingWarps * 2) {
+  if (rows_by_ring(a.M, a.Hq + 2 * a.Hkv, QrRing<kLanes>::kBackHeads, int64_t(grid) * kQrRingWarps)) {
     static std::atomic<uint64_t> done{0};
-    constexpr int kPerD = kQrRingWarps * kQrRing * kQrBackHeads * (4 + int(sizeof(T)));   // bytes per element of a head
+    constexpr int kPerD = kQrRingWarps * kQrRing * QrRing<kLanes>::kBackHeads * (4 + int(sizeof(T)));   // bytes per element of a head
     if (!allow_smem(qk_norm_rope_backward_ring_kernel<T, kLanes>, kPerD * 8 * kLanes, done)) return BL_ERR_CUDA;
     qk_norm_rope_backward_ring_kernel<T, kLanes><<<unsigned(grid), 32 * kQrRingWarps, size_t(kPerD) * a.D, st>>>(a);
   } else {
@@ -256,9 +265,10 @@ bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
 constexpr size_t kAbNormBytes = 256;
 
 // CTAs that share the query heads of one key block: one as soon as the key blocks fill
-// B200's 148 SMs, else as many as fill them twice (5 sequences of up to 777 tokens, 6/2
-// heads of 80: dK/dV 50 -> 24 us with the join; 2 x 4096 tokens, 20/5 heads of 128, where
-// the parts would cost more than the evener load gives: not split).
+// B200's 148 SMs, else as many as fill them twice.  Both sides measured, whole backward: 5
+// sequences of up to 777 tokens, 6/2 heads of 80 (70 key blocks), one CTA 74 us (dQ's tail
+// not yet overlapped), two 53, three 41; 2 x 4096 tokens, 20/5 heads of
+// 128 (320 key blocks), one 549 us, two 604: the parts cost more than the evener load gives.
 int dkv_splits(const bl_attn_call* c) {
   const int group = c->Hq / c->Hkv;
   const int64_t ctas = int64_t(c->Hkv) * c->B * ceil_div(c->max_k < 1 ? 1 : c->max_k, 128);

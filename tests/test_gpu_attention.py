@@ -63,7 +63,7 @@ SHAPES = [(1, 20, 5, 128, 128, False, "bfloat16"), (7, 4, 4, 32, 16, True, "floa
           (3, 3, 1, 8, 8, True, "bfloat16"), (5, 2, 2, 256, 64, False, "float32"), (300, 32, 8, 128, 128, True, "float16"),
           (4, 5, 1, 96, 0, False, "float32"), (2, 1, 1, 24, 8, False, "float16"), (900, 8, 8, 64, 64, False, "bfloat16"),
           # enough rows for the kernels that are fed by bulk copies, each number of lanes a head
-          (5001, 4, 2, 32, 32, False, "float16"), (4801, 3, 1, 56, 24, True, "float32"),
+          (4801, 12, 4, 32, 32, False, "float16"), (2401, 20, 5, 56, 24, True, "float32"),
           (1705, 20, 4, 128, 128, False, "bfloat16"), (1301, 18, 9, 256, 64, True, "float32"),
           (4803, 2, 1, 80, 40, False, "bfloat16"), (4802, 1, 1, 8, 8, False, "float32")]
 

@@ -35,6 +35,11 @@ What it computes, and where the method is stated (page title, then section):
   the straight-through lie": dL/dx = (dL/dy) W, dL/dW = (dL/dy)^T x,
   dL/db = sum of dL/dy, on the float32 masters, in float64.
 
+* ``attention`` (module) -- part 2, section "attention, as graph ops" (heads,
+  softmax(Q K^T / sqrt(d) + mask) V, RMSNorm) and the PyPI page's RoPE and KV
+  cache: per-head norms with the position rotation, attention with a window and
+  visible first tokens, their gradients and a paged cache's rows, in float64.
+
 Readings taken where the pages leave a step open:
 
 1. Precision.  The pages' arrays are numpy float32, so every quantizer step is
@@ -66,7 +71,8 @@ Readings taken where the pages leave a step open:
    norm's eps is its own argument, separate from the quantizers'.
 
 Every function here is pinned (``tests/test_oracle_pins.py``,
-``tests/test_oracle_checkpoint.py``, ``tests/test_oracle_backward.py``)
+``tests/test_oracle_checkpoint.py``, ``tests/test_oracle_backward.py``,
+``tests/test_oracle_attention.py``)
 against hand-worked values, closed forms, invariants or brute force; none is
 unpinned.
 """

@@ -147,8 +147,8 @@ struct PaCfg {
 
 // Position in the line of tiles: sequence b, key head and chunk (item), tile t of it.
 struct PaAt {
-  int64_t b, flat;          // flat: line index of the item's first tile
-  int item, t, len;         // item = hk * chunks + chunk
+  int64_t flat;             // line index of the item's first tile
+  int b, item, t, len;      // item = hk * chunks + chunk
   PaTiles tiles;
 };
 
@@ -162,7 +162,8 @@ paged_attn_kernel(const PaArgs a) {
   __shared__ float s_m[4][C::kHeads], s_l[4][C::kHeads];
   __shared__ int64_t s_scan[4];
   __shared__ int64_t s_find[3];                  // sequence of this CTA's first tile, line index of its first tile, its length
-  __shared__ int s_empty;                        // whether a sequence has no tokens
+  __shared__ int s_empty, s_longest;             // whether a sequence has no tokens; tiles of the longest
+  __shared__ int64_t s_line[2];                  // the line's tiles and CTAs, for the joins
   __shared__ float2 s_join[kPaThreads];
   __shared__ unsigned int s_last;
   constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
@@ -173,13 +174,17 @@ paged_attn_kernel(const PaArgs a) {
   const int items = a.Hkv * a.chunks;
   bool range = false, bad = false;
 
-  // the line: total tiles, this CTA's part, and the sequence where it begins
+  // The line: total tiles, this CTA's part, and the sequence where it begins.  Cutting it finer
+  // shortens each part by a tile's time (about 1 us) but adds parts to the join of the longest
+  // item (about 0.1 us each per 128 columns of four): a part has at least the square root of
+  // that item's tiles times the ratio.  One sequence of 12816 tokens, 15/3 heads of 80: 444 CTAs
+  // 49 us, 118 CTAs 23 us.
   int64_t total = 0, ctas = 0, lo = 0, hi = 0;
   {
     const int64_t rounds = ceil_div(a.B, kPaThreads);
     int64_t n = 0, x = 0, before = 0;                // of sequence b: line tiles, and up to it within the round
-    int len = 0;
-    if (tid == 0) s_empty = 0;
+    int len = 0, longest = 0;
+    if (tid == 0) s_empty = s_longest = 0;
     auto scan = [&](int64_t b) {                     // returns the round's tiles
       len = b < a.B ? pa_len(a, b, range) : 0;
       n = int64_t(pa_tiles(len, a.window, a.sinks).n) * items;
@@ -195,8 +200,20 @@ paged_attn_kernel(const PaArgs a) {
       for (int w = 0; w < warp; ++w) x += s_scan[w];
       return s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
     };
-    for (int64_t r = 0; r < rounds; ++r) total += scan(r * kPaThreads + tid);
+    for (int64_t r = 0; r < rounds; ++r) {
+      total += scan(r * kPaThreads + tid);
+      longest = max(longest, pa_tiles(len, a.window, a.sinks).n);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) atomicMax(&s_longest, longest);
+    __syncthreads();
+    const float least = sqrtf(float(s_longest) * float(min(a.group, C::kHeads) * (DP / 4)) * (0.1f / 128.f));
     ctas = min(int64_t(gridDim.x), total);
+    if (least > 1.f) ctas = min(ctas, max(int64_t(1), int64_t(float(total) / least)));
+    if (tid == 0) {
+      s_line[0] = total;
+      s_line[1] = ctas;
+    }
     if (int64_t(blockIdx.x) < ctas) {
       lo = div_near(int64_t(blockIdx.x) * total, ctas);
       hi = div_near((int64_t(blockIdx.x) + 1) * total, ctas);
@@ -227,7 +244,7 @@ paged_attn_kernel(const PaArgs a) {
     return;
   }
 
-  auto enter = [&](PaAt& p, int64_t b, int64_t first, int len, int64_t x) {   // line index x, in sequence b whose tiles begin at first
+  auto enter = [&](PaAt& p, int b, int64_t first, int len, int64_t x) {   // line index x, in sequence b whose tiles begin at first
     p.b = b;
     p.len = len;
     p.tiles = pa_tiles(p.len, a.window, a.sinks);
@@ -250,8 +267,7 @@ paged_attn_kernel(const PaArgs a) {
   // Thread tid looks up where row tid % 64 of a tile is, in two steps so that the page
   // number's way from memory overlaps a tile's work
   struct Pending {
-    int64_t in;                                      // the row's place within its page, -1: not visible
-    int page;
+    int in, page;                                    // the row's place within its page's head, -1: not visible; the page
   };
   auto look_up = [&](const PaAt& p) {
     Pending d;
@@ -261,16 +277,16 @@ paged_attn_kernel(const PaArgs a) {
     const int j = t * kPaTile + (tid & (kPaTile - 1));
     if (j < p.len && sees(p.len - 1, j, a.window, a.sinks)) {
       const uint32_t n = a.page == 1 ? uint32_t(j) : __umulhi(uint32_t(j), a.page_magic) >> a.page_shift;
-      d.in = int64_t(p.item / a.chunks) * a.page + (j - int(n) * a.page);
-      d.page = a.table[p.b * a.ldt + n];
+      d.in = j - int(n) * a.page;
+      d.page = a.table[int64_t(p.b) * a.ldt + n];
     }
     return d;
   };
-  auto place = [&](const Pending& d, int tile) {
+  auto place = [&](const Pending& d, int head, int tile) {
     int64_t off = -1;
     if (d.in >= 0) {
       if (d.page < 0 || d.page >= a.pages) range = true;
-      else off = (int64_t(d.page) * a.Hkv * a.page + d.in) * a.D;
+      else off = ((int64_t(d.page) * a.Hkv + head) * a.page + d.in) * a.D;
     }
     s_row[tile % C::kStages][tid & (kPaTile - 1)] = off;
   };
@@ -292,25 +308,31 @@ paged_attn_kernel(const PaArgs a) {
   };
 
   if (a.D < DP) {                                    // columns past D: zeros, never written again
-    for (int i = tid; i < C::kStages * C::kStage / 16; i += kPaThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    const int pad = (DP - a.D) / 8;
+    for (int i = tid; i < C::kStages * 2 * kPaTile * pad; i += kPaThreads) {
+      const int r = i / pad, c = a.D / 8 + i - r * pad;            // row of all stages' tiles, K and V
+      *reinterpret_cast<uint4*>(smem + (r / kPaTile) * C::kTileBytes + pa_off<DP>(r % kPaTile, c)) = make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
   }
 
   PaAt cur, load;
-  enter(cur, s_find[0], s_find[1], int(s_find[2]), lo);
+  enter(cur, int(s_find[0]), s_find[1], int(s_find[2]), lo);
   load = cur;
   const int n = int(hi - lo);                        // tiles of this CTA
   // the first tiles' rows all at once (threads 0..63 the even ones, 64..127 the odd ones)
   {
     Pending d[(C::kStages + 1) / 2];
+    int head[C::kStages];
 #pragma unroll
     for (int t = 0; t < C::kStages; ++t) {
+      head[t] = load.item / a.chunks;
       if (t < n && (tid / kPaTile) == (t & 1)) d[t / 2] = look_up(load);
       if (t < n) advance(load);
     }
 #pragma unroll
     for (int t = 0; t < C::kStages; ++t)
-      if (t < n && (tid / kPaTile) == (t & 1)) place(d[t / 2], t);
+      if (t < n && (tid / kPaTile) == (t & 1)) place(d[t / 2], head[t], t);
   }
   __syncthreads();
 #pragma unroll
@@ -331,7 +353,7 @@ paged_attn_kernel(const PaArgs a) {
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const int hg = ch * C::kHeads + u * 8 + (lane >> 2);      // head in the group: the B operand's column
-      const T* q = static_cast<const T*>(a.q) + (cur.b * a.Hq + int64_t(hk) * a.group + hg) * a.D;
+      const T* q = static_cast<const T*>(a.q) + (int64_t(cur.b) * a.Hq + hk * a.group + hg) * a.D;
 #pragma unroll
       for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
@@ -357,7 +379,7 @@ paged_attn_kernel(const PaArgs a) {
     cp_async_commit();
     // the rows of tile it + kStages, asked for a tile ago, into the place of tile it's
     if (it + C::kStages < n) {
-      if (tid < kPaTile) place(next, it + C::kStages);
+      if (tid < kPaTile) place(next, load.item / a.chunks, it + C::kStages);
       advance(load);
       if (tid < kPaTile && it + C::kStages + 1 < n) next = look_up(load);
     }
@@ -472,7 +494,7 @@ paged_attn_kernel(const PaArgs a) {
       }
       const int hk = cur.item / a.chunks, ch = cur.item - hk * a.chunks;
       const int nh = min(C::kHeads, a.group - ch * C::kHeads);       // live heads
-      OutT* out = static_cast<OutT*>(a.out) + (cur.b * a.Hq + int64_t(hk) * a.group + ch * C::kHeads) * a.D;
+      OutT* out = static_cast<OutT*>(a.out) + (int64_t(cur.b) * a.Hq + hk * a.group + ch * C::kHeads) * a.D;
       if (item_ends && seg_first == 0) {                             // the whole item is this CTA's
         for (int i = tid; i < nh * a.D; i += kPaThreads) {
           const int h = i / a.D, d = i - h * a.D;
@@ -496,8 +518,9 @@ paged_attn_kernel(const PaArgs a) {
           __stcg(reinterpret_cast<float2*>(part + C::kHeads * DP) + h, make_float2(top, sum));
         }
         // CTAs of the item: those that hold its first and its last tile, and all between
-        const int64_t c0 = div_near((cur.flat + 1) * ctas + total - 1, total) - 1;
-        const int64_t c1 = div_near((cur.flat + cur.tiles.n) * ctas + total - 1, total) - 1;
+        const int64_t tiles = s_line[0], share = s_line[1];
+        const int64_t c0 = div_near((cur.flat + 1) * share + tiles - 1, tiles) - 1;
+        const int64_t c1 = div_near((cur.flat + cur.tiles.n) * share + tiles - 1, tiles) - 1;
         __syncthreads();
         if (tid == 0) {
           // releases what the CTA has written before the barrier, and acquires what the other CTAs have

@@ -6,9 +6,9 @@
 // Bound by memory: every visible key and value is read once, 4 D bytes per token
 // and key head, for 4 D operations per query head.  So
 //   - the visible 64-token tiles of all sequences and key heads form one line that
-//     is cut into equal parts, one per CTA (three or four CTAs an SM: a tile's
-//     chain of products, exchanges and exponentials is long, other warps fill it): ragged batches and a
-//     single long sequence load every SM alike;
+//     is cut into equal parts, one per CTA (three or four CTAs an SM: a tile's chain of
+//     products, exchanges and exponentials is long, other warps fill it): ragged batches
+//     and a single long sequence load every SM alike;
 //   - tiles arrive by 16-byte asynchronous copies, kStages in flight, the page of
 //     each row looked up two tiles ahead; rows that are not visible are filled with
 //     zeros instead of being read;
@@ -25,9 +25,9 @@
 //     to finish (a counter per head part, reset by it), in the order of the line.
 //
 // Measured: 64 ragged sequences of up to 8192 tokens (32/8 heads of 128, bfloat16, pages of
-// 16) 170 us, 6.36 TB/s, 97% of the card's copy rate; two of 131071 tokens (20/5 heads of
-// 64, float16) 62 us, 5.4 TB/s: 59 parts a head are joined at its end; one of 301 tokens
-// 7.9 us: a chain of dependent reads (lengths, pages, rows, parts), nothing to overlap it.
+// 16) 171 us, 6.3 TB/s, 96% of the card's copy rate; two of 131071 tokens (20/5 heads of
+// 64, float16) 64 us, 5.2 TB/s: 59 parts a head are joined at its end; one of 301 tokens
+// 8.1 us: a chain of dependent reads (lengths, pages, rows, parts), nothing to overlap it.
 // Two CTAs an SM took 195 and 89 us: a tile's chain of products, exchanges and
 // exponentials is then the bound, not memory.
 #pragma once

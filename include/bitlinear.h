@@ -472,7 +472,7 @@ typedef struct {
   int64_t Tq, Tk;             /* rows of the buffers (< 2^29) */
   const int32_t *cu_q, *cu_k; /* [B + 1], not falling, within 0 .. Tq and 0 .. Tk */
   int32_t B;
-  int32_t max_q, max_k;       /* at least the longest Lq and Lk (max_k: the backward only) */
+  int32_t max_q, max_k;       /* at least the longest Lq and Lk (max_k: the backward only); any larger value does */
   int32_t window, sinks;      /* >= 0 */
   float scale;                /* finite, > 0 */
 } bl_attn_call;

@@ -196,6 +196,11 @@ bl_status check_attn(const bl_attn_call* c) {
   return BL_OK;
 }
 
+// A longest length as the kernels take it: at least one block, to find sequences that are
+// longer, and no more than the buffer's rows, which no sequence exceeds (row blocks are counted
+// in 32 bits on the device: a length near 2^31 would wrap, and its blocks begin at negative rows).
+int longest(int32_t most, int64_t rows) { return int(most < 1 || rows < 1 ? 1 : most < rows ? most : rows); }
+
 AttnArgs attn_args(const bl_attn_call* c) {
   AttnArgs a;
   memset(&a, 0, sizeof(a));
@@ -213,8 +218,8 @@ AttnArgs attn_args(const bl_attn_call* c) {
   a.Hkv = c->Hkv;
   a.D = c->D;
   a.B = c->B;
-  a.max_q = c->max_q < 1 ? 1 : c->max_q;                 // at least one block, to find sequences that are longer
-  a.max_k = c->max_k < 1 ? 1 : c->max_k;
+  a.max_q = longest(c->max_q, c->Tq);
+  a.max_k = longest(c->max_k, c->Tk);
   a.window = c->window >= c->Tk ? 0 : c->window;         // no window at all, then
   a.sinks = c->sinks;
   a.scale = c->scale;
@@ -271,7 +276,7 @@ constexpr size_t kAbNormBytes = 256;
 // 128 (320 key blocks), one 549 us, two 604: the parts cost more than the evener load gives.
 int dkv_splits(const bl_attn_call* c) {
   const int group = c->Hq / c->Hkv;
-  const int64_t ctas = int64_t(c->Hkv) * c->B * ceil_div(c->max_k < 1 ? 1 : c->max_k, 128);
+  const int64_t ctas = int64_t(c->Hkv) * c->B * ceil_div(longest(c->max_k, c->Tk), 128);
   if (ctas < 1 || ctas >= 148) return 1;
   const int64_t want = 296 / ctas < group ? 296 / ctas : group;
   const int64_t heads = ceil_div(group, want);

@@ -503,7 +503,8 @@ bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const
  *   q [B, Hq, D] contiguous, of the cache's type, 16-byte aligned.
  *   table [B, ldt] int32: page number of tokens n * page .. of each sequence; only
  *     the pages that the query sees are looked up.
- *   lens [B] int32, 0 <= lens[b] <= ldt * page (0: the row is 0).
+ *   lens [B] int32, 0 <= lens[b] <= ldt * page and <= 2^31 - 64 (0: the row is 0;
+ *     one out of range is taken as the nearest that is within).
  *   out [B, Hq, D] contiguous, float32 or of the cache's type; probabilities keep
  *     float32's precision.
  *   ws >= bl_paged_attention_workspace_size(B, Hq, cache) bytes, 256-byte

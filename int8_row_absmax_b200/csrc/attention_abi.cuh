@@ -339,8 +339,9 @@ bl_status launch_paged(const PaArgs& a, cudaStream_t st) {
   constexpr int smem = PaCfg<T, DP, NT>::kSmem;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(paged_attn_kernel<T, DP, NT, OutT>, smem, done)) return BL_ERR_CUDA;
-  const int64_t most = a.B * a.Hkv * a.chunks * ceil_div(a.ldt * a.page, kPaTile);
-  const int64_t grid = most < 1 ? 1 : most < PaCfg<T, DP, NT>::kCtas ? most : PaCfg<T, DP, NT>::kCtas;
+  // no more CTAs than tiles (counted in a double: the product may pass 64 bits)
+  const double tiles = double(a.B) * a.Hkv * a.chunks * double(ceil_div(a.most, kPaTile));
+  const int grid = tiles < PaCfg<T, DP, NT>::kCtas ? int(tiles) : PaCfg<T, DP, NT>::kCtas;
   paged_attn_kernel<T, DP, NT, OutT><<<unsigned(grid), kPaThreads, smem, st>>>(a);
   return launch_status();
 }
@@ -535,6 +536,7 @@ bl_status bl_paged_attention(const void* q, int64_t B, int Hq, const bl_kv_pages
   a.Hkv = cache->Hkv;
   a.D = cache->D;
   a.page = cache->page;
+  a.most = int(ldt * cache->page < kPaMaxLen ? ldt * cache->page : kPaMaxLen);
   a.window = window;
   a.sinks = sinks;
   a.scale_log2 = scale * kLog2e;

@@ -40,6 +40,7 @@ namespace bl {
 
 constexpr int kPaThreads = 128, kPaTile = 64;
 constexpr int kPaMaxCtas = 148 * 4;                  // planned for B200's 148 SMs
+constexpr int kPaMaxLen = INT32_MAX - (kPaTile - 1);  // the last tile's key numbers still fit 32 bits
 constexpr float kPaLow = -1e30f;                     // below every finite scaled score that matters
 
 struct PaArgs {
@@ -47,6 +48,7 @@ struct PaArgs {
   const int32_t *table, *lens;
   int64_t ldt, pages, B;
   int Hq, Hkv, D, page, window, sinks;
+  int most;                 // longest length: the table's ldt * page tokens, and kPaMaxLen at most
   float scale_log2;
   void* out;
   unsigned int* count;      // [kPaMaxCtas]
@@ -127,9 +129,8 @@ __device__ __forceinline__ PaTiles pa_tiles(int len, int window, int sinks) {
 }
 __device__ __forceinline__ int pa_len(const PaArgs& a, int64_t b, bool& range) {
   const int n = a.lens[b];
-  const int64_t most = a.ldt * a.page;
-  if (n < 0 || n > most) range = true;
-  return n < 0 ? 0 : n > most ? int(most) : n;
+  if (n < 0 || n > a.most) range = true;
+  return min(max(n, 0), a.most);
 }
 
 template <typename T, int DP, int NT>

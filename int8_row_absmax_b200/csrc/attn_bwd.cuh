@@ -188,7 +188,7 @@ attn_dkv_join_kernel(const AttnArgs a) {
   // 16 rows a CTA: 32 lanes a row (one quad each at D = 128), 8 rows at a time
   const int64_t one = a.Tk * a.Hkv * a.D;
   const int c = threadIdx.x & 31;
-  bool bad = false;
+  uint32_t bad = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int which = i & 1, r = j0 + int(blockIdx.y) * 16 + (i >> 1) * 8 + (threadIdx.x >> 5);
@@ -200,16 +200,17 @@ attn_dkv_join_kernel(const AttnArgs a) {
       const float4 x = *reinterpret_cast<const float4*>(a.part + (2 * z + which) * one + at);
       y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
     }
-    if (!(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY)) bad = true;
-    st4(static_cast<T*>(which ? a.dv : a.dk) + at, y);
+    const uint2 w = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
+    bad |= not_finite2<T>(w.x) | not_finite2<T>(w.y);
+    *reinterpret_cast<uint2*>(static_cast<T*>(which ? a.dv : a.dk) + at) = w;
   }
   if (bad) raise_status(kDevNonFinite);
 }
 
-// A row of an accumulator, times f, to 16-bit memory (D elements); false if not finite.
+// A row of an accumulator, times f, to 16-bit memory (D elements); false if any is stored as not finite.
 template <typename T, int DP>
 __device__ __forceinline__ bool store_row(uint32_t taddr, T* out, int D, float f, bool store, bool zero) {
-  bool good = true;
+  uint32_t bad = 0;
 #pragma unroll 1
   for (int u = 0; u < DP / 32; ++u) {
     uint32_t o[32];
@@ -223,13 +224,13 @@ __device__ __forceinline__ bool store_row(uint32_t taddr, T* out, int D, float f
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         const float f0 = zero ? 0.f : __uint_as_float(o[e + 2 * z]) * f, f1 = zero ? 0.f : __uint_as_float(o[e + 2 * z + 1]) * f;
-        if (!(fabsf(f0) + fabsf(f1) < INFINITY)) good = false;
         y[z] = pack2<T>(f0, f1);
+        bad |= not_finite2<T>(y[z]);
       }
       *reinterpret_cast<uint4*>(out + u * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
-  return good;
+  return bad == 0;
 }
 
 template <typename T, int DP>

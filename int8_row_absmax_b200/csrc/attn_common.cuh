@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -39,6 +41,13 @@ template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
 }
 template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Not zero if a value of such a word is not finite, that is, its exponent all ones: what is
+// stored is tested, so that a finite float32 that rounds to infinity counts, too.
+template <typename T> __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+  constexpr uint32_t past = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;   // 2^15 less infinity's bits
+  return ((w & 0x7FFF7FFFu) + past) & 0x80008000u;
 }
 
 // Four consecutive elements, from 8-byte (16 for float32) aligned memory.

@@ -51,3 +51,46 @@ def test_paged_longest_length(bl):
         again = bl.paged_attention(q, kc, vc, table, lens, window=window, sinks=sinks)
         assert bl.sync_status() == "BL_ERR_RANGE"
         assert torch.equal(again, got)
+
+
+def gradients(bl, dout, q, k, v, scale=None):
+    import torch
+    n = q.shape[0]
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, lse = bl.attention(q, k, v, cu, cu, n, scale=scale)
+    ok(bl)
+    return bl.attention_backward(dout, q, k, v, out, lse, cu, cu, n, n, scale=scale)
+
+
+@pytest.mark.parametrize("heads", [1, 2])                            # stored by the kernel itself; summed over two parts
+def test_gradients_that_float16_does_not_reach_are_reported(bl, heads):
+    import torch
+    q, k, v = (normal(n, 1, h, 64, dtype="float16") for n, h in ((1, heads), (2, 1), (3, 1)))
+    dout = torch.full_like(q, 65504.0 / heads)                        # one key: dV is the sum of dout over the heads
+    dv = gradients(bl, dout, q, k, v)[2]
+    ok(bl)
+    assert (dv == 65504).all()
+    dout[..., 5] = 32768.0 if heads == 2 else 65504.0
+    dv = gradients(bl, dout, q, k, v)[2]
+    # 65504 is reached, 65536 is not
+    assert bl.sync_status() == ("BL_ERR_NONFINITE" if heads == 2 else "BL_OK")
+    assert torch.isinf(dv[..., 5]).all() == (heads == 2) and (dv[..., :5] == 65504).all()
+
+
+def test_sums_over_queries_that_float16_does_not_reach_are_reported(bl):
+    import torch
+    n = 300
+    q, k, v = (torch.zeros(n, 1, 64, dtype=torch.float16, device="cuda") for _ in range(3))
+    q[..., 0], k[0, 0, 0] = 8.0, 16.0                                 # every query sees the first key with weight 1 - 2^-14
+    dv = gradients(bl, torch.full_like(q, 300.0), q, k, v)[2]
+    assert bl.sync_status() == "BL_ERR_NONFINITE"
+    assert torch.isinf(dv[0]).all() and torch.isfinite(dv[1:]).all()
+    # the second query's keys are +-60, its probabilities 1/2 each, dP = +-6400: dQ = 2 * 3200 * 60
+    q, k, v = (torch.zeros(2, 1, 64, dtype=torch.float16, device="cuda") for _ in range(3))
+    k[0], k[1], v[0], v[1] = 60.0, -60.0, 1.0, -1.0
+    dq, dk, dv = gradients(bl, torch.full_like(q, 100.0), q, k, v, scale=1.0)
+    assert bl.sync_status() == "BL_ERR_NONFINITE"
+    assert torch.isinf(dq[1]).all() and torch.isfinite(dk).all() and torch.isfinite(dv).all()
+    dq, _, _ = gradients(bl, torch.full_like(q, 100.0), q, k, v, scale=0.125)
+    ok(bl)
+    assert (dq[1] == 48000).all() and not dq[0].any()

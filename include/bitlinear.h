@@ -424,7 +424,8 @@ typedef struct {
  * pass: y = x / sqrt(mean(x^2) + eps) * g over each head's D elements, then the
  * pairs (a, b) of its first R elements become (a cos - b sin, a sin + b cos).
  * Values are converted only.  A query or key head whose squares overflow float32
- * counts as not finite.  q [M, Hq, D], k and v [M, Hkv, D]: contiguous
+ * counts as not finite, and so does an element that type t does not reach (a
+ * value beyond 65504 in float16, stored as Inf).  q [M, Hq, D], k and v [M, Hkv, D]: contiguous
  * outputs of type t (any bl_dtype), 16-byte aligned.  Here D may be up to 256.
  * Rows of a token whose position is out of range are not written. */
 bl_status bl_qk_norm_rope(const bl_qkv_rows* rows, bl_dtype t, void* q, void* k, void* v, cudaStream_t stream);

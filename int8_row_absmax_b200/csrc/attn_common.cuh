@@ -61,6 +61,16 @@ template <typename T> __device__ __forceinline__ void st4(T* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
 }
 template <> __device__ __forceinline__ void st4<float>(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+// The largest magnitude of a running one and four values; NaN stays.
+__device__ __forceinline__ float top4(float top, float4 v) {
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(v.x), "f"(v.y));
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(v.z), "f"(v.w));
+  return top;
+}
+// Whether a value of that magnitude is finite in T: below the largest one and half a step.
+template <typename T> __device__ __forceinline__ bool reached(float top) {
+  return top < (std::is_same<T, __half>::value ? 65520.f : std::is_same<T, float>::value ? INFINITY : 3.3961775e38f);
+}
 
 // 2^x; flushes subnormal results (2^-126 beside a row maximum of 1 is nothing).
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -110,15 +110,6 @@ __device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
   return join4(fma2(lo2(a), lo2(b), lo2(c)), fma2(hi2(a), hi2(b), hi2(c)));
 }
 constexpr float kMaxF32 = 3.4028235e38f;
-// Whether a head's row is not finite, from its sum of squares; for values, whose large
-// squares may overflow while they are fine, from the elements then.
-__device__ __forceinline__ bool not_finite(float ss, bool value, float4 x, float4 y) {
-  if (ss <= kMaxF32) return false;
-  auto in = [](float4 a) {
-    return fabsf(a.x) <= kMaxF32 && fabsf(a.y) <= kMaxF32 && fabsf(a.z) <= kMaxF32 && fabsf(a.w) <= kMaxF32;
-  };
-  return !value || !in(x) || !in(y);
-}
 __device__ __forceinline__ float4 neg4(float4 a) { return make_float4(-a.x, -a.y, -a.z, -a.w); }
 
 // Rotates the pairs of (lo, hi) by (c, s): split pairs are (lo.x, hi.x) ...,
@@ -153,6 +144,7 @@ qk_norm_rope_kernel(const QrArgs a) {
   const int64_t items = a.M * heads, step = int64_t(gridDim.x) * kPerBlock;
   const float inv_d = 1.f / float(a.D);
   bool bad = false, range = false;
+  float top = 0.f;                                     // of what is stored, before its rounding
   // whole warps take every turn together: the shuffles need all lanes
   for (int64_t base = int64_t(blockIdx.x) * kPerBlock; base < items; base += step) {
     const int64_t i = base + threadIdx.x / kLanes;
@@ -175,8 +167,8 @@ qk_norm_rope_kernel(const QrArgs a) {
     if (!ok || at >= (kAppend ? a.nslots : 1)) range = true;
     const float ss = head_sum<kLanes>(dot8(x, x, y, y));
     if (!live || !ok || !l.on) continue;
-    if (not_finite(ss, value, x, y)) bad = true;
     if (!value) {
+      if (!(ss <= kMaxF32)) bad = true;
       const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
       const float* g = query ? a.gq : a.gk;
       x = mul4(scale4(x, r), gain4(g, l.lo));
@@ -185,6 +177,7 @@ qk_norm_rope_kernel(const QrArgs a) {
         rotate(x, y, *reinterpret_cast<const float4*>(a.table + p * a.R + 4 * u),
                *reinterpret_cast<const float4*>(a.table + p * a.R + (a.R >> 1) + 4 * u), a.interleaved != 0);
     }
+    top = top4(top4(top, x), y);
     T* out;
     if (query) {
       out = static_cast<T*>(a.oq) + (m * a.Hq + h) * a.D;
@@ -203,7 +196,7 @@ qk_norm_rope_kernel(const QrArgs a) {
     st4(out + c0, x);
     st4(out + c1, y);
   }
-  if (bad) raise_status(kDevNonFinite);
+  if (bad || !reached<T>(top)) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
 }
 
@@ -298,6 +291,7 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     run.copy(reinterpret_cast<unsigned char*>(ring + st * kRingHeads * a.D), i.m, h0, h1, &full[warp][st]);
   };
   bool bad = false, range = false;
+  float top = 0.f;                                     // of what is stored, before its rounding
   // Ahead of the work: an item's token, position and slot two items, its table row (which
   // follows the position) one.
   static_assert(kQrRing == 3, "copies and questions run two items ahead");
@@ -367,9 +361,9 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
     for (int j = 0; j < kPasses; ++j) {
       const int h = h0 + j * kAtOnce + lane / kLanes;
       if (h >= heads || !l.on || !ok) continue;
-      if (not_finite(ss[j], h >= nk, x[j], y[j])) bad = true;
       int c0 = 8 * u, c1 = 8 * u + 4;
       if (h < nk) {
+        if (!(ss[j] <= kMaxF32)) bad = true;
         const float r = rsqrtf(fmaf(ss[j], inv_d, a.eps));
         const float* g = gains + (h < a.Hq ? 0 : a.D);
         x[j] = mul4(scale4(x[j], r), *reinterpret_cast<const float4*>(g + l.lo));
@@ -378,13 +372,14 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
         c0 = l.lo;
         c1 = l.hi;
       }
+      top = top4(top4(top, x[j]), y[j]);
       if (kAppend && h >= a.Hq && !store) continue;
       T* out = h < a.Hq ? oq + h * a.D : (h < nk ? ok_ : ov) + int64_t(h) * stride;
       st4(out + c0, x[j]);
       st4(out + c1, y[j]);
     }
   }
-  if (bad) raise_status(kDevNonFinite);
+  if (bad || !reached<T>(top)) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
 }
 

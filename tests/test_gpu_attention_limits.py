@@ -94,3 +94,46 @@ def test_sums_over_queries_that_float16_does_not_reach_are_reported(bl):
     dq, _, _ = gradients(bl, torch.full_like(q, 100.0), q, k, v, scale=0.125)
     ok(bl)
     assert (dq[1] == 48000).all() and not dq[0].any()
+
+
+NORMS = [(3, 2, 1, 32), (5000, 16, 8, 32)]                           # a kernel of single heads; one fed by bulk copies
+
+
+@pytest.mark.parametrize("m,hq,hk,d", NORMS)
+@pytest.mark.parametrize("dtype,past", [("float16", 65520.0), ("bfloat16", 3.4e38)])
+def test_values_that_the_type_does_not_reach_are_reported(bl, m, hq, hk, d, dtype, past):
+    import torch
+    from test_gpu_attention import rows
+    qkv, pos, gq, gk = rows(8, m, hq, hk, d, d)
+    table, t, v0 = bl.rope_table(5000, d), getattr(torch, dtype), (hq + hk) * d
+    biggest = torch.finfo(t).max
+
+    def both():
+        cache = [torch.zeros(m, hk, 1, d, dtype=t, device="cuda") for _ in range(2)]
+        yield lambda: bl.qk_norm_rope(qkv, hq, hk, d, pos, table, gq, gk, dtype=t)[2]
+        yield lambda: (bl.qk_norm_rope_append(qkv, hq, hk, d, pos, table, gq, gk, *cache, torch.arange(m, device="cuda")),
+                       cache[1][:, :, 0])[1]
+    for f in both():
+        qkv[m - 1, v0:v0 + 8] = biggest
+        f()
+        ok(bl)
+        qkv[m - 1, v0 + 5] = past
+        v = f()
+        assert bl.sync_status() == "BL_ERR_NONFINITE"
+        assert torch.isinf(v[m - 1, 0, 5]) and torch.isfinite(v[:m - 1]).all()
+
+
+@pytest.mark.parametrize("m,hq,hk,d", NORMS)
+@pytest.mark.parametrize("dtype,gain", [("float16", 1e5), ("bfloat16", 3.39e38), ("float32", 3.39e38)])
+def test_normed_heads_that_the_type_does_not_reach_are_reported(bl, m, hq, hk, d, dtype, gain):
+    import torch
+    from test_gpu_attention import rows
+    qkv, pos, gq, gk = rows(8, m, hq, hk, d, d)
+    qkv[m - 1, hq * d:(hq + hk) * d] = 0.0
+    qkv[m - 1, hq * d + 3] = 1.0                                      # normed: the root of d
+    gk[3] = gain
+    gk[:3], gk[4:] = 0.0, 0.0
+    qkv[:m - 1, hq * d:(hq + hk) * d].view(m - 1, hk, d)[..., 3] = 0.0
+    k = bl.qk_norm_rope(qkv, hq, hk, d, pos, None, gq, gk, dtype=getattr(torch, dtype))[1]
+    assert bl.sync_status() == "BL_ERR_NONFINITE"
+    assert torch.isinf(k[m - 1, 0, 3]) and not k[:m - 1].any()

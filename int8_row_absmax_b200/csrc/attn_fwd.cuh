@@ -44,6 +44,15 @@ struct alignas(64) AttnMaps {
   CUtensorMap q, k, v;                                 // [rows, heads, D], boxes of 128 rows x 64 elements
 };
 
+// An average of values of type T is within T's range. P is rounded and the row's sum is not, so
+// that the quotient may pass the largest number by 2^-11 of it, which float16 stores as Inf
+// already (in bfloat16 sums of such values pass float32 first): it is held at the largest number.
+// Infinities and NaN stay.
+template <typename T> __device__ __forceinline__ float within_type(float x) {
+  if (!std::is_same<T, __half>::value) return x;
+  return fabsf(x) < 66000.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+}
+
 template <int DP>
 struct AfCfg {
   static constexpr int kTile = 128 * DP * 2;           // a 128-row operand tile: DP / 64 boxes of 128 x 128 bytes
@@ -387,7 +396,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
     fine = !__any_sync(0xffffffffu, !fine);
     if (fine && r < s.nq) {
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays
-      bool bad = !(l < INFINITY);
+      uint32_t bad = l < INFINITY ? 0u : 1u;
       T* out = static_cast<T*>(a.out) + (int64_t(s.q0 + i) * a.Hq + h) * a.D;
 #pragma unroll 1
       for (int u = 0; u < DP / 32; ++u) {
@@ -404,8 +413,8 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
           for (int z = 0; z < 4; ++z) {
             const float f0 = l == 0.f ? 0.f : __uint_as_float(o[e + 2 * z]) * inv;
             const float f1 = l == 0.f ? 0.f : __uint_as_float(o[e + 2 * z + 1]) * inv;
-            if (!(fabsf(f0) + fabsf(f1) < INFINITY)) bad = true;
-            y[z] = pack2<T>(f0, f1);
+            y[z] = pack2<T>(within_type<T>(f0), within_type<T>(f1));
+            bad |= not_finite2<T>(y[z]);
           }
           *reinterpret_cast<uint4*>(out + u * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
         }

@@ -137,3 +137,26 @@ def test_normed_heads_that_the_type_does_not_reach_are_reported(bl, m, hq, hk, d
     k = bl.qk_norm_rope(qkv, hq, hk, d, pos, None, gq, gk, dtype=getattr(torch, dtype))[1]
     assert bl.sync_status() == "BL_ERR_NONFINITE"
     assert torch.isinf(k[m - 1, 0, 3]) and not k[:m - 1].any()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_averages_of_the_largest_values_stay_finite(bl, sign):
+    """P is rounded for the tensor cores, its sum is not: the average of equal values may come out up to 2^-11 larger."""
+    import torch
+    n, d = 257, 64
+    q, k = (torch.zeros(n, 1, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    q[:, 0, 0] = torch.linspace(0.01, 3, n)
+    k[0, 0, 0] = 8.0                                                  # one key far above the others, which all round alike
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for value in (65504.0, 65472.0, 1.0):
+        v = torch.full_like(k, sign * value)
+        out, _ = bl.attention(q, k, v, cu, cu, n)
+        ok(bl)
+        assert (out.float() - sign * value).abs().max() <= value * 1.5 * 2.0 ** -10    # P's rounding and the result's
+    v[5, 0, 7] = float("inf")
+    out, _ = bl.attention(q, k, v, cu, cu, n)
+    assert bl.sync_status() == "BL_ERR_NONFINITE" and torch.isinf(out[6:, 0, 7]).all()
+    big = torch.full_like(k, 3e38, dtype=torch.bfloat16)              # their sum passes float32 in no row of one key
+    out, _ = bl.attention(q[:1].bfloat16(), k[:1].bfloat16(), big[:1], cu.clamp(max=1), cu.clamp(max=1), 1)
+    ok(bl)
+    assert torch.equal(out, big[:1])

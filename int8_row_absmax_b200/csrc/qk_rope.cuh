@@ -386,8 +386,10 @@ qk_norm_rope_ring_kernel(const QrArgs a) {
 // A head's gradient from its row, its rotated-back gradient (e, f) and both sums.
 __device__ __forceinline__ void head_back(const QrArgs& a, const QrLane& l, int h, int nk, float4 x, float4 y, float4 e,
                                           float4 f, float4 g0, float4 g1, float ss, float tt, float inv_d, float* oq,
-                                          float* ok, float* ov, float4& sq0, float4& sq1, float4& sk0, float4& sk1, bool& bad) {
+                                          float* ok, float* ov, float4& sq0, float4& sq1, float4& sk0, float4& sk1, bool& bad,
+                                          float& top) {
   if (h >= nk) {
+    top = top4(top4(top, e), f);
     float* out = ov + h * a.D + 8 * l.u;
     *reinterpret_cast<float4*>(out) = e;
     *reinterpret_cast<float4*>(out + 4) = f;
@@ -396,13 +398,15 @@ __device__ __forceinline__ void head_back(const QrArgs& a, const QrLane& l, int 
   const bool query = h < a.Hq;
   const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
   const float t = tt * inv_d * r;
-  if (!(ss <= kMaxF32) || !(fabsf(t) <= kMaxF32)) bad = true;
+  if (!(ss <= kMaxF32)) bad = true;
   x = scale4(x, r);
   y = scale4(y, r);
   const float4 nt = make_float4(-t, -t, -t, -t);
   float* out = (query ? oq : ok) + h * a.D;
-  *reinterpret_cast<float4*>(out + l.lo) = scale4(fma4(x, nt, mul4(e, g0)), r);
-  *reinterpret_cast<float4*>(out + l.hi) = scale4(fma4(y, nt, mul4(f, g1)), r);
+  const float4 dx = scale4(fma4(x, nt, mul4(e, g0)), r), dy = scale4(fma4(y, nt, mul4(f, g1)), r);
+  *reinterpret_cast<float4*>(out + l.lo) = dx;
+  *reinterpret_cast<float4*>(out + l.hi) = dy;
+  top = top4(top4(top, dx), dy);
   if (query) {
     sq0 = fma4(e, x, sq0);
     sq1 = fma4(f, y, sq1);
@@ -447,6 +451,7 @@ qk_norm_rope_backward_kernel(const QrArgs a) {
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
   bool bad = false, range = false;
+  float top = 0.f;                                     // of the gradients that are stored
   int64_t m_next = 0, h_next = 0, p_next = 0;        // asked for an item ahead: the table's row follows the position
   auto ask = [&](int64_t i) {
     if (i >= items) return;
@@ -487,9 +492,9 @@ qk_norm_rope_backward_kernel(const QrArgs a) {
     const float tt = head_sum<kLanes>(dot8(mul4(e, g0), x, mul4(f, g1), y));
     if (work)
       head_back(a, l, h, nk, x, y, e, f, g0, g1, ss, tt, inv_d, a.dxq + m * a.lddq, a.dxk + m * a.lddk - int64_t(a.Hq) * a.D,
-                a.dxv + m * a.lddv - int64_t(nk) * a.D, sq0, sq1, sk0, sk1, bad);
+                a.dxv + m * a.lddv - int64_t(nk) * a.D, sq0, sq1, sk0, sk1, bad, top);
   }
-  if (bad) raise_status(kDevNonFinite);
+  if (bad || !reached<float>(top)) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
   if (a.part) gain_part<kPerBlock>(a, l, grp, sums, sq0, sq1, sk0, sk1);
 }
@@ -539,6 +544,7 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 sq0 = zero, sq1 = zero, sk0 = zero, sk1 = zero;
   bool bad = false, range = false;
+  float top = 0.f;                                     // of the gradients that are stored
   static_assert(kQrRing == 3, "copies and questions run two items ahead");
   QrItem item(first, step, chunks);
   QrAhead<false> one, two;
@@ -601,10 +607,10 @@ qk_norm_rope_backward_ring_kernel(const QrArgs a) {
       const float* g = gains + (h < a.Hq ? 0 : a.D);
       if (h < heads && l.on && ok)
         head_back(a, l, h, nk, x[j], y[j], e[j], f[j], *reinterpret_cast<const float4*>(g + l.lo),
-                  *reinterpret_cast<const float4*>(g + l.hi), ss[j], tt[j], inv_d, oq, okk, ov, sq0, sq1, sk0, sk1, bad);
+                  *reinterpret_cast<const float4*>(g + l.hi), ss[j], tt[j], inv_d, oq, okk, ov, sq0, sq1, sk0, sk1, bad, top);
     }
   }
-  if (bad) raise_status(kDevNonFinite);
+  if (bad || !reached<float>(top)) raise_status(kDevNonFinite);
   if (range) raise_status(kDevRange);
   if (!a.part) return;
   __syncthreads();                                     // the rings are read: their place takes the sums

@@ -160,3 +160,29 @@ def test_averages_of_the_largest_values_stay_finite(bl, sign):
     out, _ = bl.attention(q[:1].bfloat16(), k[:1].bfloat16(), big[:1], cu.clamp(max=1), cu.clamp(max=1), 1)
     ok(bl)
     assert torch.equal(out, big[:1])
+
+
+@pytest.mark.parametrize("m,hq,hk,d", NORMS)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_norm_gradients_report_what_is_not_finite(bl, m, hq, hk, d, dtype):
+    """A NaN or Inf in any of the gradients that come in, and a gradient that passes float32 on the way."""
+    import torch
+    from test_gpu_attention import rows
+    qkv, pos, gq, gk = rows(8, m, hq, hk, d, d)
+    table = bl.rope_table(5000, d)
+    grads = [normal(n, m, h, d, dtype=dtype) for n, h in ((3, hq), (4, hk), (5, hk))]
+    want = bl.qk_norm_rope_backward(*grads, qkv, hq, hk, d, pos, table, gq, gk)
+    ok(bl)
+    for n in range(3):
+        for bad in (float("nan"), float("-inf")):
+            use = [g.clone() for g in grads]
+            use[n][m - 1, -1, d - 1] = bad
+            dx, _, _ = bl.qk_norm_rope_backward(*use, qkv, hq, hk, d, pos, table, gq, gk)
+            assert bl.sync_status() == "BL_ERR_NONFINITE", (n, bad)
+            assert torch.equal(dx[:m - 1], want[0][:m - 1])
+    use = [g.clone() for g in grads]
+    use[0][m - 1] = 3e38                                              # finite; its products with the gains and 1/rms are not
+    small = qkv.clone()
+    small[m - 1] *= 1e-6
+    bl.qk_norm_rope_backward(*use, small, hq, hk, d, pos, table, gq, gk)
+    assert bl.sync_status() == "BL_ERR_NONFINITE"

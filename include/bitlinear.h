@@ -393,7 +393,9 @@ bl_status bl_linear_backward(const float* dY, const float* X, const float* W, in
  *     the unused rest of a page) may hold anything, NaN included.  A NaN or Inf
  *     that a row does see sets BL_ERR_NONFINITE in the status word; in
  *     bl_attention and its backward it may then reach the other rows of the same
- *     sequence.  So does a gradient that is stored as Inf because the output's
+ *     sequence.  (An Inf in a key or query that makes the score -Inf gives the
+ *     key no weight and is not reported; a row whose scores are all -Inf is.)
+ *     So does a gradient that is stored as Inf because the output's
  *     type does not reach it (beyond 65504 in float16).
  *   - Positions, slots, page numbers and lengths live on the device.  One out of
  *     range sets BL_ERR_RANGE in the status word; what it would have addressed is

@@ -38,7 +38,7 @@ constexpr int kAfThreads = 320;                        // 2 x 4 softmax warps, M
 constexpr int kAfRing = 4;                             // K and V tiles in flight
 constexpr int kAfParts = 2;                            // parts in which a row of P is handed over
 constexpr float kAfLazy = 8.f;                         // log2 of the growth that is let pass
-constexpr float kLow = -1e30f;                         // a row maximum before anything is seen
+constexpr float kLow = -3.4028235e38f;                 // a row maximum before anything is seen: the lowest finite number
 
 struct alignas(64) AttnMaps {
   CUtensorMap q, k, v;                                 // [rows, heads, D], boxes of 128 rows x 64 elements
@@ -396,7 +396,8 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
     fine = !__any_sync(0xffffffffu, !fine);
     if (fine && r < s.nq) {
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays
-      uint32_t bad = l < INFINITY ? 0u : 1u;
+      // a row that sees a key (its own position's, at least) has a sum, unless its scores passed float32
+      uint32_t bad = l < INFINITY && (l > 0.f || p < 0) ? 0u : 1u;
       T* out = static_cast<T*>(a.out) + (int64_t(s.q0 + i) * a.Hq + h) * a.D;
 #pragma unroll 1
       for (int u = 0; u < DP / 32; ++u) {

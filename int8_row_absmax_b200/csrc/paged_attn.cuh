@@ -41,7 +41,7 @@ namespace bl {
 constexpr int kPaThreads = 128, kPaTile = 64;
 constexpr int kPaMaxCtas = 148 * 4;                  // planned for B200's 148 SMs
 constexpr int kPaMaxLen = INT32_MAX - (kPaTile - 1);  // the last tile's key numbers still fit 32 bits
-constexpr float kPaLow = -1e30f;                     // below every finite scaled score that matters
+constexpr float kPaLow = -3.4028235e38f;             // a maximum before anything is seen: the lowest finite number
 
 struct PaArgs {
   const void *q, *k, *v;

@@ -186,3 +186,45 @@ def test_norm_gradients_report_what_is_not_finite(bl, m, hq, hk, d, dtype):
     small[m - 1] *= 1e-6
     bl.qk_norm_rope_backward(*use, small, hq, hk, d, pos, table, gq, gk)
     assert bl.sync_status() == "BL_ERR_NONFINITE"
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3)])
+def test_scores_far_below_zero(bl, window, sinks):
+    """Scores down to -2^113 are scores like others: a row's largest takes it all."""
+    import torch
+    n, d = 300, 64
+    q, k = (torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[..., 0] = 2.0 ** 58
+    at = (np.arange(n) * 37) % 251 + 1                                # whole numbers below 2^8, alike 251 apart only
+    k[:, 0, 0] = torch.from_numpy(-(2.0 ** 50) * at).cuda()
+    v = normal(1, n, 1, d, dtype="bfloat16")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, lse = bl.attention(q, k, v, cu, cu, n, window=window, sinks=sinks)
+    ok(bl)
+    see = A.visible(n, n, window, sinks)
+    weight = np.where(see, at, 1000)
+    weight = weight == weight.min(1, keepdims=True)
+    want = (weight / weight.sum(1, keepdims=True)) @ f8(v[:, 0])
+    assert (np.abs(f8(out[:, 0]) - want) <= 1.01 * HALF["bfloat16"] * np.abs(want)).all()
+    assert (np.abs(f8(lse[0]) / (-(2.0 ** 105) * np.where(see, at, 1000).min(1)) - 1) <= 4 * E).all()
+    pages = torch.arange(-(-n // 16), dtype=torch.int32, device="cuda")
+    cache = [torch.nn.functional.pad(t, (0, 0, 0, 0, 0, 4)).reshape(-1, 16, 1, d).transpose(1, 2).contiguous() for t in (k, v)]
+    lens = torch.arange(1, n + 1, dtype=torch.int32, device="cuda")
+    got = bl.paged_attention(q, *cache, pages.expand(n, -1).contiguous(), lens, window=window, sinks=sinks)
+    ok(bl)
+    assert (np.abs(f8(got[:, 0]) - want) <= 8 * E * np.abs(want)).all()
+
+
+def test_scores_that_pass_float32_are_reported(bl):
+    import torch
+    n, d = 3, 64
+    q, k = (torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[1, 0, 0], k[:, 0, 0] = 1e20, -1e20                              # the second row's scores are all -1e40
+    v, cu = normal(1, n, 1, d, dtype="bfloat16"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, _ = bl.attention(q, k, v, cu, cu, n)
+    assert bl.sync_status() == "BL_ERR_NONFINITE"
+    assert torch.equal(out[0], v[0])
+    cache = [torch.nn.functional.pad(t, (0, 0, 0, 0, 0, 13)).reshape(1, 16, 1, d).transpose(1, 2).contiguous() for t in (k, v)]
+    bl.paged_attention(q[1:2].contiguous(), *cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                       torch.tensor([2], dtype=torch.int32, device="cuda"))
+    assert bl.sync_status() == "BL_ERR_NONFINITE"

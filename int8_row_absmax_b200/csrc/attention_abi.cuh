@@ -266,8 +266,10 @@ bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
   return a.D <= 64 ? launch_attn_fwd<T, 64>(a, st) : launch_attn_fwd<T, 128>(a, st);
 }
 
-// The backward's workspace: the two norms (float16), delta [Hq, Tq], the parts of dK and dV.
-constexpr size_t kAbNormBytes = 256;
+// The backward's workspace: two norms of each sequence and key head (float16), delta [Hq, Tq],
+// the parts of dK and dV.
+size_t norm_bytes(const bl_attn_call* c) { return align_up(c->t == BL_T_F16 ? size_t(c->B) * size_t(c->Hkv) * 8 : 1); }
+size_t delta_bytes(const bl_attn_call* c) { return align_up(size_t(c->Tq) * size_t(c->Hq) * 4); }
 
 // CTAs that share the query heads of one key block: one as soon as the key blocks fill
 // B200's 148 SMs, else as many as fill them twice.  Both sides measured, whole backward: 5
@@ -305,12 +307,12 @@ bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
       !allow_smem(attn_dq_kernel<T, DP>, AbCfg<DP>::kDqSmem, done_q))
     return BL_ERR_CUDA;
   const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
-  if (!int32_max(gq) || !int32_max(gk * a.splits)) return BL_ERR_UNSUPPORTED;
-  if (f16 && cudaMemsetAsync(norms, 0, 8, st) != cudaSuccess) return BL_ERR_CUDA;
-  if (queries) {
-    const int64_t rows = a.Tq * a.Hq;
-    attn_delta_kernel<T, DP><<<grid_for(rows, 256 / (DP / 8), 8), 256, 0, st>>>(a, norms);
-  }
+  const int64_t query_parts = ceil_div(a.max_q, AdCfg<DP>::tokens(a.Hq / a.Hkv));
+  const int64_t key_parts = f16 ? ceil_div(a.max_k, AdCfg<DP>::kMost) : 1;
+  const int64_t gd = int64_t(a.Hkv) * a.B * (query_parts > key_parts ? query_parts : key_parts);
+  if (!int32_max(gq) || !int32_max(gk * a.splits) || !int32_max(gd)) return BL_ERR_UNSUPPORTED;
+  if (f16 && cudaMemsetAsync(norms, 0, size_t(a.B) * size_t(a.Hkv) * 8, st) != cudaSuccess) return BL_ERR_CUDA;
+  if (queries) attn_delta_kernel<T, DP><<<unsigned(gd), 256, 0, st>>>(a, norms);
   if (queries && gq > 0) attn_dq_kernel<T, DP><<<unsigned(gq), kAbThreads, AbCfg<DP>::kDqSmem, st>>>(maps, a, norms);
   if (keys && gk > 0) {
     // dK/dV needs nothing of dQ's: its CTAs take the SMs as those of dQ leave them
@@ -472,7 +474,7 @@ bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStre
 
 size_t bl_attention_backward_workspace_size(const bl_attn_call* call) {
   if (check_attn(call) != BL_OK || call->B == 0) return 0;
-  return kAbNormBytes + align_up(size_t(call->Tq) * size_t(call->Hq) * 4) + dkv_part_bytes(call);
+  return norm_bytes(call) + delta_bytes(call) + dkv_part_bytes(call);
 }
 
 bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
@@ -494,10 +496,10 @@ bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const
   a.dk = dk;
   a.dv = dv;
   float* norms = static_cast<float*>(ws);
-  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + kAbNormBytes);
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + norm_bytes(call));
   a.splits = dkv_splits(call);
   a.split_heads = int(ceil_div(call->Hq / call->Hkv, a.splits));
-  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kAbNormBytes + align_up(size_t(call->Tq) * size_t(call->Hq) * 4));
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + norm_bytes(call) + delta_bytes(call));
   return call->t == BL_T_F16 ? run_attn_backward<__half>(a, norms, stream)
                              : run_attn_backward<__nv_bfloat16>(a, norms, stream);
 }

@@ -29,9 +29,11 @@
 // 1.07 PFLOP/s of the seven done; the card sustains 1.39 under its power limit): dQ 0.25,
 // dK/dV 0.31, delta 0.016.
 //
-// float16: P is stored 2^14 times larger and dS 2^k times, k from the largest norms of
-// the rows of dO and V (|dP - delta| <= 2 |dO| |V|), so that neither leaves the normal
-// numbers; bfloat16 needs neither.
+// float16: P is stored 2^14 times larger and dS 2^k times, k from the largest norms of the
+// rows of dO and V (|dP - delta| <= 2 |dO| |V|): neither overflows, and a dS down to 2^-28 of
+// that bound is a normal number. k is one for each sequence and key head, the pairs that a CTA
+// of dK/dV adds up: a sequence's gradients do not depend on what it is packed with. bfloat16
+// needs neither.
 #pragma once
 
 #include "attn_fwd.cuh"
@@ -56,81 +58,80 @@ struct AbCfg {
 
 template <typename T> __device__ __forceinline__ constexpr float p_scale_log2() { return std::is_same<T, __half>::value ? 14.f : 0.f; }
 
-// 2^k for dS (float16), from the largest squared row norms of dO and V.
-template <typename T> __device__ __forceinline__ float ds_scale(const float* norms) {
+// 2^k for dS (float16), from the largest squared row norms of dO and V of sequence b and key head hk.
+template <typename T> __device__ __forceinline__ float ds_scale(const AttnArgs& a, const float* norms, int b, int hk) {
   if (!std::is_same<T, __half>::value) return 1.f;
+  norms += 2 * (int64_t(b) * a.Hkv + hk);
   const float most = 2.02f * sqrtf(norms[0]) * sqrtf(norms[1]);
   if (!(most > 0.f && most < INFINITY)) return 1.f;
   return exp2f(fminf(fmaxf(floorf(log2f(32768.f / most)), -100.f), 100.f));
 }
 
-// Whether key row r is one that some query of its sequence may see.
-__device__ __forceinline__ bool seen_key(const AttnArgs& a, int r) {
-  if (r < a.cu_k[0] || r >= a.cu_k[a.B]) return false;
-  if (a.window == 0) return true;
-  int lo = 0, hi = a.B;                                 // cu_k[lo] <= r < cu_k[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_k[mid] <= r) lo = mid;
-    else hi = mid;
-  }
-  const int j = r - a.cu_k[lo], off = (a.cu_k[lo + 1] - a.cu_k[lo]) - (a.cu_q[lo + 1] - a.cu_q[lo]);
-  return j < a.sinks || j > off - a.window;
-}
-
 // delta[h, row] = sum dO O, one group of DP / 8 lanes a row; for float16 also the largest
-// squared norms of the rows of dO and V (order does not matter to a maximum).
+// squared norms of the rows of dO and V (order does not matter to a maximum).  A CTA takes the
+// heads of one key head over some tokens of one sequence, about four rows a group, and as many
+// of the sequence's keys: one atomic a CTA and norm, on words that only its (sequence, key head)
+// has.  Rows dealt out over all sequences alike took 10 us more for 64 sequences of 128 tokens,
+// 8 heads of 64 (55 us in all): atomics wherever a group's row passes into another sequence.
+template <int DP> struct AdCfg {
+  static constexpr int kLanes = DP / 8, kRows = 256 / kLanes, kMost = 4 * kRows;   // rows at a time; keys of a CTA
+  __host__ __device__ static int tokens(int group) { return group < kMost ? kMost / group : 1; }   // of a CTA
+};
 template <typename T, int DP>
 __global__ void __launch_bounds__(256)
 attn_delta_kernel(const AttnArgs a, float* norms) {
-  constexpr int kLanes = DP / 8, kRows = 256 / kLanes;
-  const int u = threadIdx.x % kLanes, in = threadIdx.x / kLanes;
+  using C = AdCfg<DP>;
+  constexpr bool kNorms = std::is_same<T, __half>::value;
+  const int u = threadIdx.x % C::kLanes, in = threadIdx.x / C::kLanes;
   const bool on = 8 * u < a.D;
-  float top_o = 0.f, top_v = 0.f;
-  const int64_t rows = a.Tq * a.Hq, step = int64_t(gridDim.x) * kRows;
+  const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv)), b = rest % a.B, c = rest / a.B;
+  const int group = a.Hq / a.Hkv, tokens = C::tokens(group);
+  Seq s;
+  if (!load_seq(a, b, s, true)) return;
   auto sum = [&](float x) {
-    for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = C::kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
   };
-  for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < rows; r0 += step) {
-    const int64_t r = r0 + in;
+  float top_o = 0.f, top_v = 0.f;
+  const int i0 = c * tokens, rows = min(tokens, s.nq - i0) * group;
+  for (int r0 = 0; r0 < rows; r0 += C::kRows) {
+    const int r = r0 + in, i = i0 + r / group, h = hk * group + r % group;
+    const int64_t at = (int64_t(s.q0 + i) * a.Hq + h) * a.D + 8 * u;
     uint4 x = make_uint4(0, 0, 0, 0), y = x;
     if (on && r < rows) {
-      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + r * a.D + 8 * u);
-      y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + r * a.D + 8 * u);
+      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + at);
+      y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + at);
     }
     float d = 0.f, n = 0.f;
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = unpack2<T>(xs[i]), g = unpack2<T>(ys[i]);
+    for (int e = 0; e < 4; ++e) {
+      const float2 p = unpack2<T>(xs[e]), g = unpack2<T>(ys[e]);
       d = fmaf(p.x, g.x, fmaf(p.y, g.y, d));
       n = fmaf(g.x, g.x, fmaf(g.y, g.y, n));
     }
     d = sum(d);
-    if (std::is_same<T, __half>::value) {
-      n = sum(n);
-      const int64_t q = r / a.Hq;
-      if (q >= a.cu_q[0] && q < a.cu_q[a.B] && n < INFINITY) top_o = fmaxf(top_o, n);
-    }
-    if (u == 0 && r < rows) a.delta[(r % a.Hq) * a.Tq + r / a.Hq] = d;
+    if (kNorms) n = sum(n);
+    if (kNorms && i + s.nk - s.nq >= 0 && n < INFINITY) top_o = fmaxf(top_o, n);   // rows that see a key
+    if (u == 0 && r < rows) a.delta[int64_t(h) * a.Tq + s.q0 + i] = d;
   }
-  if (std::is_same<T, __half>::value) {
-    const int64_t vr = a.Tk * a.Hkv;
-    for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < vr; r0 += step) {
-      const int64_t r = r0 + in;
+  if (kNorms) {
+    const int j0 = int(min(int64_t(c) * C::kMost, int64_t(s.nk))), keys = min(C::kMost, s.nk - j0);   // c may count queries
+    for (int r0 = 0; r0 < keys; r0 += C::kRows) {
+      const int j = j0 + r0 + in;
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (on && r < vr)
-        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + (r / a.Hkv) * a.ldv + (r % a.Hkv) * a.D + 8 * u);
+      if (on && r0 + in < keys)
+        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + int64_t(s.k0 + j) * a.ldv + hk * a.D + 8 * u);
       float n = 0.f;
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack2<T>(xs[i]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack2<T>(xs[e]);
         n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
       }
       n = sum(n);
-      if (n < INFINITY && n > top_v && seen_key(a, int(r / a.Hkv))) top_v = n;
+      const bool seen = a.window == 0 || j < a.sinks || j > s.nk - s.nq - a.window;   // by some query
+      if (seen && n < INFINITY) top_v = fmaxf(top_v, n);
     }
     __shared__ float tops[2][8];
     top_o = warp_max(top_o);
@@ -143,7 +144,7 @@ attn_delta_kernel(const AttnArgs a, float* norms) {
     if (threadIdx.x < 2) {                              // squares: not negative, so their bits are ordered
       float t = 0.f;
       for (int w = 0; w < 8; ++w) t = fmaxf(t, tops[threadIdx.x][w]);
-      unsigned int* to = reinterpret_cast<unsigned int*>(norms) + threadIdx.x;
+      unsigned int* to = reinterpret_cast<unsigned int*>(norms) + 2 * (int64_t(b) * a.Hkv + hk) + threadIdx.x;
       if (__float_as_uint(t) > *reinterpret_cast<volatile unsigned int*>(to)) atomicMax(to, __float_as_uint(t));
     }
   }
@@ -260,10 +261,11 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   const int unit = int(blockIdx.x % unsigned(a.Hkv * a.splits)), rest = int(blockIdx.x / unsigned(a.Hkv * a.splits));
   const int hk = unit / a.splits, z = unit - hk * a.splits, group = a.Hq / a.Hkv;
   const int j0 = rest / a.B * 128, h0 = hk * group + z * a.split_heads, heads = min(a.split_heads, group - z * a.split_heads);
+  const int b = rest % a.B;
   Seq s;
   // Launched while dQ's CTAs still run, and reads nothing of theirs (delta is from the kernel before
   // them); but it ends after they have ended, so that what follows it on the stream follows both.
-  if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) {
+  if (!load_seq(a, b, s, true) || j0 >= s.nk) {
     griddep_wait();
     return;
   }
@@ -438,7 +440,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t S = tmem + lanes + half * 64, dP = S + 128;
     const float c = a.scale * kLog2e;
-    const float mult = ds_scale<T>(norms), f = mult * exp2f(-p_scale_log2<T>());
+    const float mult = ds_scale<T>(a, norms, b, hk), f = mult * exp2f(-p_scale_log2<T>());
     bool fine = true;
     for (int it = 0; it < n; ++it) {
       const int i0 = first + it % per * 128;
@@ -534,7 +536,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const int row = (warp & 3) * 32 + lane, j = j0 + row;
     const bool keys = warp >= 4;
     const uint32_t acc = tmem + (uint32_t((warp & 3) * 32) << 16) + (keys ? 384 : 256);
-    const float f = keys ? a.scale / ds_scale<T>(norms) : exp2f(-p_scale_log2<T>());
+    const float f = keys ? a.scale / ds_scale<T>(a, norms, b, hk) : exp2f(-p_scale_log2<T>());
     const int64_t at = (int64_t(s.k0 + j) * a.Hkv + hk) * a.D;
     T* out = static_cast<T*>(keys ? a.dk : a.dv) + at;
     if (a.splits > 1)
@@ -565,9 +567,9 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
 
   const int nblk = (a.max_q + 127) / 128;
   const int h = int(blockIdx.x % unsigned(a.Hq)), rest = int(blockIdx.x / unsigned(a.Hq));
-  const int i0 = (nblk - 1 - rest / a.B) * 128, hk = h / (a.Hq / a.Hkv);
+  const int i0 = (nblk - 1 - rest / a.B) * 128, hk = h / (a.Hq / a.Hkv), b = rest % a.B;
   Seq s;
-  if (!load_seq(a, rest % a.B, s, true) || i0 >= s.nq) return;
+  if (!load_seq(a, b, s, true) || i0 >= s.nq) return;
   s.q0 = uniform(s.q0);
   s.nq = uniform(s.nq);
   s.k0 = uniform(s.k0);
@@ -689,7 +691,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       lse = l == -INFINITY ? kNoRow : l * kLog2e;
       delta = a.delta[int64_t(h) * a.Tq + s.q0 + i];
     }
-    const float mult = ds_scale<T>(norms);
+    const float mult = ds_scale<T>(a, norms, b, hk);
     bool fine = true;
     for (int it = 0; it < n; ++it) {
       const int j0 = blocks.at(it);
@@ -712,11 +714,11 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       if (masked) {
         const int top = pos - j0 - half * 64, bot = lo - j0 - half * 64, lead = a.window ? a.sinks - j0 - half * 64 : 0;
 #pragma unroll
-        for (int b = 0; b < 64; b += 32) {
-          const uint32_t seen = seen_bits(b, top, bot, lead);
+        for (int f = 0; f < 64; f += 32) {
+          const uint32_t seen = seen_bits(f, top, bot, lead);
 #pragma unroll
           for (int u = 0; u < 32; ++u)
-            if (!(seen & (1u << u))) p[b + u] = 0.f;
+            if (!(seen & (1u << u))) p[f + u] = 0.f;
         }
       }
       fine = mbar_wait_near(&dp_full, uint32_t(it) & 1u) && !*err;
@@ -760,7 +762,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
     const int row = warp * 32 + lane, i = i0 + row;
     T* out = static_cast<T*>(a.dq) + (int64_t(s.q0 + i) * a.Hq + h) * a.D;
     const uint32_t acc = tmem + (uint32_t(warp * 32) << 16) + 384;
-    if (!store_row<T, DP>(acc, out, a.D, a.scale / ds_scale<T>(norms), i < s.nq, n == 0) && i < s.nq) raise_status(kDevNonFinite);
+    if (!store_row<T, DP>(acc, out, a.D, a.scale / ds_scale<T>(a, norms, b, hk), i < s.nq, n == 0) && i < s.nq) raise_status(kDevNonFinite);
   }
   tc_fence_before();
   __syncthreads();

@@ -228,3 +228,54 @@ def test_scores_that_pass_float32_are_reported(bl):
     bl.paged_attention(q[1:2].contiguous(), *cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
                        torch.tensor([2], dtype=torch.int32, device="cuda"))
     assert bl.sync_status() == "BL_ERR_NONFINITE"
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_gradients_do_not_depend_on_what_a_sequence_is_packed_with(bl, dtype):
+    """Sequences and heads whose gradients are 2^20 apart: each comes out as if it were alone, bit for bit."""
+    import torch
+    lens, h, d = [512, 300, 129], 3, 64                               # a head a key head: nothing is shared out
+    q, k, v, cu, _ = packed(5, lens, lens, h, h, d, dtype)
+    size = torch.ones(sum(lens), h, 1, device="cuda")
+    size[512:812], size[812:, 1] = 2.0 ** 10, 2.0 ** 10
+    size[:512] = 2.0 ** -10
+    dout = (normal(6, *q.shape) * size).to(q.dtype)
+    out, lse = bl.attention(q, k, v, cu, cu, 512, window=200, sinks=2)
+    grads = bl.attention_backward(dout, q, k, v, out, lse, cu, cu, 512, 512, window=200, sinks=2)
+    ok(bl)
+    check_backward(q, k, v, cu, cu, 200, 2, out, lse, dout, grads, dtype)
+    for b, n in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        for head in range(h):
+            f = lambda t: t[rows, head:head + 1].contiguous()  # noqa: E731,B023
+            alone = bl.attention_backward(f(dout), f(q), f(k), f(v), f(out), lse[head:head + 1, rows].contiguous(), one, one, n, n,
+                                          window=200, sinks=2)
+            for x, y in zip(grads, alone):
+                assert torch.equal(f(x), y)
+    ok(bl)
+
+
+def test_gradients_of_many_short_sequences(bl):
+    import torch
+    rng = np.random.default_rng(1)
+    lq = rng.integers(0, 4, 700).tolist()
+    lk = [n + int(rng.integers(0, 3)) for n in lq]
+    q, k, v, cq, ck = packed(5, lq, lk, 6, 3, 32, "float16")
+    dout = (normal(6, *q.shape) * torch.logspace(-2, 2, q.shape[0], device="cuda")[:, None, None]).half()
+    out, lse = bl.attention(q, k, v, cq, ck, 3)
+    grads = bl.attention_backward(dout, q, k, v, out, lse, cq, ck, 3, 5)
+    ok(bl)
+    check_forward(q, k, v, cq, ck, 0, 0, out, lse, "float16")
+    check_backward(q, k, v, cq, ck, 0, 0, out, lse, dout, grads, "float16")
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_gradients_of_many_heads_a_key_head(bl, dtype):
+    """More heads than rows that a CTA of the row sums takes; more keys than queries, and fewer."""
+    q, k, v, cq, ck = packed(5, [9, 70, 200], [300, 70, 40], 96, 1, 64, dtype)
+    dout = normal(6, *q.shape, dtype=dtype)
+    out, lse = bl.attention(q, k, v, cq, ck, 200)
+    grads = bl.attention_backward(dout, q, k, v, out, lse, cq, ck, 200, 300)
+    ok(bl)
+    check_backward(q, k, v, cq, ck, 0, 0, out, lse, dout, grads, dtype)

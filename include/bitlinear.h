@@ -489,6 +489,18 @@ typedef struct {
  * left out. */
 bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStream_t stream);
 
+/* bl_attention whose rows that belong to no sequence (before cu_q[0], behind
+ * cu_q[B]; all of them where B = 0) are cleared in the same launch, for the outputs
+ * named in `clear`: out becomes 0, lse -inf.  For outputs that come from an
+ * allocator: what such a row holds would otherwise go on into the sums over rows
+ * that follow (a gain's gradient, a projection's).  clear = 0: bl_attention. */
+#define BL_CLEAR_OUT 0x01
+#define BL_CLEAR_LSE 0x02
+#define BL_CLEAR_DQ 0x04
+#define BL_CLEAR_DK 0x08
+#define BL_CLEAR_DV 0x10
+bl_status bl_attention_ex(const bl_attn_call* call, void* out, float* lse, int clear, cudaStream_t stream);
+
 /* Its gradients from out, lse and dout [Tq, Hq, D] (contiguous, type t):
  * P = exp(scale Q K^T - lse), dV = P^T dO, dS = P (dO V^T - rowsum(dO O)),
  * dQ = scale dS K, dK = scale dS^T Q, dK and dV summed over the query heads that
@@ -500,6 +512,12 @@ bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStre
 size_t bl_attention_backward_workspace_size(const bl_attn_call* call);
 bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
                                 void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* bl_attention_backward whose rows of no sequence are cleared: dq (BL_CLEAR_DQ), dk
+ * (BL_CLEAR_DK), dv (BL_CLEAR_DV). */
+bl_status bl_attention_backward_ex(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
+                                   void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, int clear,
+                                   cudaStream_t stream);
 
 /* Attention of one new token per sequence over a paged cache (its own key and
  * value stored already): the query of sequence b stands at position lens[b] - 1

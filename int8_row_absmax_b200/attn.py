@@ -52,8 +52,10 @@ SIGNATURES = {
     "bl_qk_norm_rope_backward_workspace_size": (_SZ, [_ROWS]),
     "bl_qk_norm_rope_backward": (_I, [_ROWS, _I, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
     "bl_attention": (_I, [_CALL, _P, _P, _P]),
+    "bl_attention_ex": (_I, [_CALL, _P, _P, _I, _P]),
     "bl_attention_backward_workspace_size": (_SZ, [_CALL]),
     "bl_attention_backward": (_I, [_CALL, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bl_attention_backward_ex": (_I, [_CALL, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _P]),
     "bl_paged_attention_workspace_size": (_SZ, [_I64, _I, _PAGES]),
     "bl_paged_attention": (_I, [_P, _I64, _I, _PAGES, _P, _I64, _P, _I32, _I32, _F, _I, _P, _P, _SZ, _P]),
 }
@@ -97,21 +99,25 @@ def qk_norm_rope(qkv, heads: int, kv_heads: int, dim: int, pos, table, gq=None, 
                  dtype=torch.bfloat16, interleaved: bool = False):
     """RMSNorm of each query and key head (gains gq, gk [dim]), rotated by its position; values converted.
     qkv: the projection's float32 rows [M, (heads + 2 kv_heads) dim], or a tuple of three [M, .] tensors.
-    Returns q [M, heads, dim], k and v [M, kv_heads, dim] of `dtype`.  table None: no rotation."""
+    Returns q [M, heads, dim], k and v [M, kv_heads, dim] of `dtype`.  table None: no rotation.  Rows of a
+    position outside the table are undefined (sync_status() then says BL_ERR_RANGE)."""
     return _native().qk_norm_rope(qkv, heads, kv_heads, dim, pos, table, gq, gk, eps, _code(dtype), interleaved)
 
 
 def qk_norm_rope_append(qkv, heads: int, kv_heads: int, dim: int, pos, table, gq, gk, kcache, vcache, slots,
                         eps: float = 1e-6, interleaved: bool = False):
     """qk_norm_rope with the keys and values stored in a paged cache [pages, kv_heads, page, dim] at
-    slots [M] int64 (page number * page + place; negative: not stored).  Returns q of the cache's type."""
+    slots [M] int64 (page number * page + place; negative: not stored).  Returns q of the cache's type (rows
+    of a position outside the table are undefined)."""
     return _native().qk_norm_rope_append(qkv, heads, kv_heads, dim, pos, table, gq, gk, kcache, vcache, slots, eps,
                                          interleaved)
 
 
 def qk_norm_rope_backward(dq, dk, dv, qkv, heads: int, kv_heads: int, dim: int, pos, table, gq=None, gk=None,
                           eps: float = 1e-6, interleaved: bool = False, ws=None):
-    """Gradients of qk_norm_rope: (dqkv float32 [M, (heads + 2 kv_heads) dim], dgq, dgk float32 [dim])."""
+    """Gradients of qk_norm_rope: (dqkv float32 [M, (heads + 2 kv_heads) dim], dgq, dgk float32 [dim]).
+    dgq and dgk are sums over all M rows, padding included: its dq and dk have to be zero, as
+    attention_backward leaves them.  Rows of a position outside the table are undefined and not summed."""
     return _native().qk_norm_rope_backward(dq, dk, dv, qkv, heads, kv_heads, dim, pos, table, gq, gk, eps, interleaved,
                                            ws)
 
@@ -120,13 +126,16 @@ def attention(q, k, v, cu_q, cu_k, max_q: int, window: int = 0, sinks: int = 0, 
     """softmax(scale q k^T over the visible keys) v over sequences packed end to end: q [Tq, heads, D],
     k and v [Tk, kv_heads, D] (float16 or bfloat16), cu_q and cu_k [B + 1] int32 offsets, max_q at least the
     longest query length.  A query sees the keys up to its own position within `window` tokens (0: all) and
-    the first `sinks` tokens.  Returns (out [Tq, heads, D], lse float32 [heads, Tq])."""
+    the first `sinks` tokens.  Returns (out [Tq, heads, D], lse float32 [heads, Tq]).  Rows of no sequence
+    (before cu_q[0], behind cu_q[-1]) keep what `out` and `lse` hold when given, else they are 0 and -inf;
+    those of a sequence that is left out (BL_ERR_RANGE) are undefined."""
     return _native().attention(q, k, v, cu_q, cu_k, max_q, window, sinks, scale, out, lse)
 
 
 def attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, max_q: int, max_k: int, window: int = 0, sinks: int = 0,
                        scale=None, ws=None, grads=None):
-    """Gradients (dq, dk, dv) of attention() from its out and lse; written into `grads` when given."""
+    """Gradients (dq, dk, dv) of attention() from its out and lse; written into `grads` when given (rows of no
+    sequence then keep what they hold, else they are 0)."""
     dq, dk, dv = (None, None, None) if grads is None else grads
     return _native().attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, max_q, max_k, window, sinks, scale, ws, dq,
                                         dk, dv)

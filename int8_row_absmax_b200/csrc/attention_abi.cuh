@@ -241,7 +241,7 @@ bool make_map_rows(CUtensorMap* map, bool f16, const void* base, int64_t ld, int
 }
 
 template <typename T, int DP>
-bl_status launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
+bl_status launch_attn_fwd(AttnArgs a, cudaStream_t st) {
   constexpr bool f16 = std::is_same<T, __half>::value;
   AttnMaps maps;
   if (!make_map_rows(&maps.q, f16, a.q, a.ldq, a.Hq, a.D, a.Tq)) return BL_ERR_CUDA;
@@ -257,13 +257,21 @@ bl_status launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
   if (!allow_smem(attn_fwd_kernel<T, DP>, smem, done)) return BL_ERR_CUDA;
   const bool two = (a.Hq / a.Hkv) % 2 == 0;
   const int64_t grid = int64_t(two ? a.Hq / 2 : a.Hq) * a.B * ceil_div(a.max_q, two ? 128 : 256);
-  if (!int32_max(grid)) return BL_ERR_UNSUPPORTED;
-  attn_fwd_kernel<T, DP><<<unsigned(grid), kAfThreads, smem, st>>>(maps, a);
+  if (!int32_max(grid + kClearCtas)) return BL_ERR_UNSUPPORTED;
+  a.work = int(grid);
+  attn_fwd_kernel<T, DP><<<unsigned(a.work + (a.clear ? kClearCtas : 0)), kAfThreads, smem, st>>>(maps, a);
   return launch_status();
 }
 template <typename T>
 bl_status run_attn(const AttnArgs& a, cudaStream_t st) {
   return a.D <= 64 ? launch_attn_fwd<T, 64>(a, st) : launch_attn_fwd<T, 128>(a, st);
+}
+
+// Clears the rows of no sequence by itself.
+bl_status clear_alone(AttnArgs a, cudaStream_t st) {
+  a.work = 0;
+  attn_clear_kernel<<<kClearCtas, 256, 0, st>>>(a);
+  return launch_status();
 }
 
 // The backward's workspace: two norms of each sequence and key head (float16), delta [Hq, Tq],
@@ -290,7 +298,7 @@ size_t dkv_part_bytes(const bl_attn_call* c) {
 }
 
 template <typename T, int DP>
-bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
+bl_status launch_attn_bwd(AttnArgs a, float* norms, cudaStream_t st) {
   constexpr bool f16 = std::is_same<T, __half>::value;
   AttnBwdMaps maps;
   const bool queries = a.Tq > 0, keys = a.Tk > 0;
@@ -310,9 +318,11 @@ bl_status launch_attn_bwd(const AttnArgs& a, float* norms, cudaStream_t st) {
   const int64_t query_parts = ceil_div(a.max_q, AdCfg<DP>::tokens(a.Hq / a.Hkv));
   const int64_t key_parts = f16 ? ceil_div(a.max_k, AdCfg<DP>::kMost) : 1;
   const int64_t gd = int64_t(a.Hkv) * a.B * (query_parts > key_parts ? query_parts : key_parts);
-  if (!int32_max(gq) || !int32_max(gk * a.splits) || !int32_max(gd)) return BL_ERR_UNSUPPORTED;
+  if (!int32_max(gq) || !int32_max(gk * a.splits) || !int32_max(gd + kClearCtas)) return BL_ERR_UNSUPPORTED;
+  a.work = int(gd);
   if (f16 && cudaMemsetAsync(norms, 0, size_t(a.B) * size_t(a.Hkv) * 8, st) != cudaSuccess) return BL_ERR_CUDA;
-  if (queries) attn_delta_kernel<T, DP><<<unsigned(gd), 256, 0, st>>>(a, norms);
+  if (queries) attn_delta_kernel<T, DP><<<unsigned(a.work + (a.clear ? kClearCtas : 0)), 256, 0, st>>>(a, norms);
+  else if (a.clear && clear_alone(a, st) != BL_OK) return BL_ERR_CUDA;
   if (queries && gq > 0) attn_dq_kernel<T, DP><<<unsigned(gq), kAbThreads, AbCfg<DP>::kDqSmem, st>>>(maps, a, norms);
   if (keys && gk > 0) {
     // dK/dV needs nothing of dQ's: its CTAs take the SMs as those of dQ leave them
@@ -461,14 +471,21 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
 }
 
 bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStream_t stream) {
+  return bl_attention_ex(call, out, lse, 0, stream);
+}
+
+bl_status bl_attention_ex(const bl_attn_call* call, void* out, float* lse, int clear, cudaStream_t stream) {
   const bl_status st = check_attn(call);
   if (st != BL_OK) return st;
-  if (call->B == 0 || call->Tq == 0) return BL_OK;
-  if (!out) return BL_ERR_INVALID_ARG;
+  if ((clear & ~(BL_CLEAR_OUT | BL_CLEAR_LSE)) != 0) return BL_ERR_INVALID_ARG;
+  if (call->Tq == 0 || (call->B == 0 && clear == 0)) return BL_OK;
+  if (!out || ((clear & BL_CLEAR_LSE) && !lse)) return BL_ERR_INVALID_ARG;
   if (!is_aligned(out, 16) || !is_aligned(lse, 4)) return BL_ERR_ALIGNMENT;
   AttnArgs a = attn_args(call);
   a.out = out;
   a.lse = lse;
+  a.clear = clear;
+  if (call->B == 0) return clear_alone(a, stream);
   return call->t == BL_T_F16 ? run_attn<__half>(a, stream) : run_attn<__nv_bfloat16>(a, stream);
 }
 
@@ -479,9 +496,27 @@ size_t bl_attention_backward_workspace_size(const bl_attn_call* call) {
 
 bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
                                 void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return bl_attention_backward_ex(call, out, lse, dout, dq, dk, dv, ws, ws_bytes, 0, stream);
+}
+
+bl_status bl_attention_backward_ex(const bl_attn_call* call, const void* out, const float* lse, const void* dout,
+                                   void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, int clear, cudaStream_t stream) {
   bl_status st = check_attn(call);
   if (st != BL_OK) return st;
-  if (call->B == 0 || (call->Tq == 0 && call->Tk == 0)) return BL_OK;
+  if ((clear & ~(BL_CLEAR_DQ | BL_CLEAR_DK | BL_CLEAR_DV)) != 0) return BL_ERR_INVALID_ARG;
+  if ((call->B == 0 && clear == 0) || (call->Tq == 0 && call->Tk == 0)) return BL_OK;
+  if (call->B == 0) {                                    // nothing is read, and no workspace needed
+    if ((call->Tq > 0 && (clear & BL_CLEAR_DQ) && !dq) ||
+        (call->Tk > 0 && (((clear & BL_CLEAR_DK) && !dk) || ((clear & BL_CLEAR_DV) && !dv))))
+      return BL_ERR_INVALID_ARG;
+    if (!is_aligned(dq, 16) || !is_aligned(dk, 16) || !is_aligned(dv, 16)) return BL_ERR_ALIGNMENT;
+    AttnArgs a = attn_args(call);
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.clear = clear;
+    return clear_alone(a, stream);
+  }
   if ((call->Tq > 0 && (!out || !lse || !dout || !dq)) || (call->Tk > 0 && (!dk || !dv))) return BL_ERR_INVALID_ARG;
   if (!is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(dout, 16) || !is_aligned(dq, 16) ||
       !is_aligned(dk, 16) || !is_aligned(dv, 16))
@@ -495,6 +530,7 @@ bl_status bl_attention_backward(const bl_attn_call* call, const void* out, const
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
+  a.clear = clear;
   float* norms = static_cast<float*>(ws);
   a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + norm_bytes(call));
   a.splits = dkv_splits(call);

@@ -81,6 +81,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(256)
 attn_delta_kernel(const AttnArgs a, float* norms) {
   using C = AdCfg<DP>;
+  if (blockIdx.x >= unsigned(a.work)) return clear_rest(a, 256);
   constexpr bool kNorms = std::is_same<T, __half>::value;
   const int u = threadIdx.x % C::kLanes, in = threadIdx.x / C::kLanes;
   const bool on = 8 * u < a.D;

@@ -174,6 +174,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
   constexpr int kBoxes = DP / 64;
   constexpr float kShift = std::is_same<T, __half>::value ? 7.f : 0.f;
   volatile int* err = &s_err;
+  if (blockIdx.x >= unsigned(a.work)) return clear_rest(a, kAfThreads);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   // the work: heads (or a pair of them) fastest, long row blocks first

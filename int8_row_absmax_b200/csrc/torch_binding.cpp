@@ -269,7 +269,9 @@ py::tuple attention(const Tensor& q, const Tensor& k, const Tensor& v, const Ten
   void* po = need(o, "out", q.scalar_type(), q.sizes(), dev);
   auto* pl = static_cast<float*>(need(l, "lse", at::kFloat, {q.size(1), q.size(0)}, dev));
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
-  check("bl_attention", bl_attention(&c, po, pl, stream_of(dev)));
+  // rows of no sequence: what a caller's tensor holds stays, what comes from the allocator is cleared
+  const int clear = (out ? 0 : BL_CLEAR_OUT) | (lse ? 0 : BL_CLEAR_LSE);
+  check("bl_attention", bl_attention_ex(&c, po, pl, clear, stream_of(dev)));
   return py::make_tuple(o, l);
 }
 
@@ -291,7 +293,8 @@ py::tuple attention_backward(const Tensor& dout, const Tensor& q, const Tensor& 
   size_t have = 0;
   void* w = workspace(ws, own, ws ? 0 : bl_attention_backward_workspace_size(&c), dev, have);
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
-  check("bl_attention_backward", bl_attention_backward(&c, po, pl, pg, pq, pk, pv, w, have, stream_of(dev)));
+  const int clear = (gq ? 0 : BL_CLEAR_DQ) | (gk ? 0 : BL_CLEAR_DK) | (gv ? 0 : BL_CLEAR_DV);
+  check("bl_attention_backward", bl_attention_backward_ex(&c, po, pl, pg, pq, pk, pv, w, have, clear, stream_of(dev)));
   return py::make_tuple(dq, dk, dv);
 }
 

@@ -28,3 +28,22 @@ def test_a_longest_length_past_the_buffer_counts_as_the_buffer(lib, most):
     """Blocks of rows are counted from the longest length in 32 bits: it is bounded by the buffer's rows first."""
     size = lib.bl_attention_backward_workspace_size
     assert size(call(max_q=most, max_k=most)) == size(call())
+
+
+def test_clearing_refusals(lib):
+    """Which outputs may be cleared by which call, and that what is to be cleared is there."""
+    f, b = lib.bl_attention_ex, lib.bl_attention_backward_ex
+    none = dict(B=0, q=None, k=None, v=None, cu_q=None, cu_k=None)
+    assert f(call(), 16, 16, 4, None) == 1 and f(call(), 16, 16, 64, None) == 1 and f(call(), 16, None, 2, None) == 1
+    assert f(call(**none), None, 16, 1, None) == 1 and f(call(**none), 16, None, 3, None) == 1
+    assert f(call(**none), 24, 16, 3, None) == 2
+    assert f(call(**none), None, None, 0, None) == 0 and f(call(Tq=0, q=None), None, None, 3, None) == 0
+    args = [16, 16, 16, 16, 16, 16, 256, 1 << 30]
+    assert b(call(), *args, 1, None) == 1 and b(call(), *args, 32, None) == 1
+    for at, bit in ((3, 4), (4, 8), (5, 16)):
+        bad = list(args)
+        bad[at] = None
+        assert b(call(**none), *bad, bit, None) == 1
+        bad[at] = 24
+        assert b(call(**none), *bad, bit, None) == 2
+    assert b(call(**none), *[None] * 7, 0, 0, None) == 0

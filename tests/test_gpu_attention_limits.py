@@ -279,3 +279,67 @@ def test_gradients_of_many_heads_a_key_head(bl, dtype):
     grads = bl.attention_backward(dout, q, k, v, out, lse, cq, ck, 200, 300)
     ok(bl)
     check_backward(q, k, v, cq, ck, 0, 0, out, lse, dout, grads, dtype)
+
+
+def dirty(*shapes):
+    """Fills the allocator's free blocks of these sizes with NaN."""
+    import torch
+    held = [torch.full(s, float("nan"), dtype=t, device="cuda") for s, t in shapes for _ in range(8)]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("dtype,hq,hk", [("bfloat16", 4, 2), ("float16", 3, 3)])
+def test_rows_of_no_sequence_are_clear_in_new_outputs(bl, dtype, hq, hk):
+    """Padding before and behind the sequences: outputs of the allocator hold zeros there (lse -inf), and a gain's
+    gradient, summed over all rows, is that of the sequences alone."""
+    import torch
+    d, lo, n, more = 64, 40, 300, 5000
+    T = lo + n + more
+    Y = normal(1, T, (hq + 2 * hk) * d)
+    table, gq, gk = bl.rope_table(T, d), 1 + 0.1 * normal(2, d), 1 + 0.1 * normal(3, d)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    q, k, v = bl.qk_norm_rope(Y, hq, hk, d, pos, table, gq, gk, dtype=getattr(torch, dtype))
+    cu = torch.tensor([lo, lo + 120, lo + n], dtype=torch.int32, device="cuda")
+    one = cu - lo
+    w = normal(4, *q.shape, dtype=dtype)
+    shapes = [((T, h, d), q.dtype) for h in (hq, hk)] + [((hq, T), torch.float32)]
+    dirty(*shapes)
+    out, lse = bl.attention(q, k, v, cu, cu, 180)
+    ok(bl)
+    own = slice(lo, lo + n)
+    f = lambda t: t[own].contiguous()  # noqa: E731
+    o1, l1 = bl.attention(f(q), f(k), f(v), one, one, 180)
+    assert torch.equal(out[own], o1) and torch.equal(lse[:, own], l1)
+    for rest in (slice(0, lo), slice(lo + n, T)):
+        assert not out[rest].any() and (lse[:, rest] == -float("inf")).all()
+    dirty(*shapes)
+    grads = bl.attention_backward(w, q, k, v, out, lse, cu, cu, 180, 180)
+    alone = bl.attention_backward(f(w), f(q), f(k), f(v), o1, l1, one, one, 180, 180)
+    ok(bl)
+    for a, b in zip(grads, alone):
+        assert torch.equal(a[own], b) and not a[:lo].any() and not a[lo + n:].any()
+    dY, dgq, dgk = bl.qk_norm_rope_backward(*grads, Y, hq, hk, d, pos, table, gq, gk)
+    eY, egq, egk = bl.qk_norm_rope_backward(*alone, f(Y), hq, hk, d, f(pos), table, gq, gk)
+    ok(bl)
+    assert torch.equal(dY[own], eY) and not dY[:lo].any() and not dY[lo + n:].any()
+    for x, y in ((dgq, egq), (dgk, egk)):                             # other partial sums, of at most n * heads terms
+        assert (x - y).abs().max() <= 2 * n * hq * E * y.abs().max() * 8
+
+
+def test_no_sequence_at_all_gives_clear_outputs(bl):
+    import torch
+    q, k = normal(1, 50, 4, 64, dtype="bfloat16"), normal(2, 70, 2, 64, dtype="bfloat16")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    shapes = [((50, 4, 64), q.dtype), ((70, 2, 64), q.dtype), ((4, 50), torch.float32)]
+    for c in (cu, torch.zeros(3, dtype=torch.int32, device="cuda")):    # none; two empty ones
+        dirty(*shapes)
+        out, lse = bl.attention(q, k, k, c, c, 0)
+        assert not out.any() and (lse == -float("inf")).all()
+        dirty(*shapes)
+        grads = bl.attention_backward(q, q, k, k, out, lse, c, c, 0, 0)
+        ok(bl)
+        assert not any(g.any() for g in grads)
+    held = torch.full_like(q, 3.0)
+    assert (bl.attention(q, k, k, cu, cu, 0, out=held)[0] == 3).all()
+    ok(bl)

@@ -16,11 +16,8 @@ the C ABI itself.
 from __future__ import annotations
 
 import ctypes
-import os
 
-import torch
-
-from . import _check, _P, _I64, _SZ, _F, _I, PKG_DIR, load
+from . import _check, _P, _I64, _SZ, _F, _I, _torch, load
 
 _I32 = ctypes.c_int32
 
@@ -60,24 +57,27 @@ SIGNATURES = {
     "bl_paged_attention": (_I, [_P, _I64, _I, _PAGES, _P, _I64, _P, _I32, _I32, _F, _I, _P, _P, _SZ, _P]),
 }
 
-_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}     # bl_dtype
+_TYPES = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}     # bl_dtype, by the dtype's name
 _binding = None
 
 
 def _native():
-    """The tensor binding (raises if it has not been built)."""
+    """The tensor binding (raises if it has not been built for the PyTorch and Python that run)."""
     global _binding
     if _binding is None:
+        from . import build
         load()
-        if not os.path.exists(os.path.join(PKG_DIR, "_binding.so")):
-            raise RuntimeError("_binding.so is missing: build it with python -m int8_row_absmax_b200.build")
+        _torch()
+        if not build.binding_fits():
+            raise RuntimeError("_binding.so is missing or built for another PyTorch or Python: build it with "
+                               "python -m int8_row_absmax_b200.build")
         from . import _binding as module
         _binding = module
     return _binding
 
 
 def _code(dtype):
-    code = _TYPES.get(dtype)
+    code = _TYPES.get(str(dtype))
     if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
     return code
@@ -85,7 +85,7 @@ def _code(dtype):
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, device=None):
     """cos | sin of position * base^(-2i/rot), float32 [positions, rot]."""
-    lib = load()
+    torch, lib = _torch(), load()
     table = torch.empty((positions, rot), dtype=torch.float32, device="cuda" if device is None else device)
     if not table.is_cuda:
         raise ValueError("the table must be on a CUDA device")
@@ -96,12 +96,13 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, device=None):
 
 
 def qk_norm_rope(qkv, heads: int, kv_heads: int, dim: int, pos, table, gq=None, gk=None, eps: float = 1e-6,
-                 dtype=torch.bfloat16, interleaved: bool = False):
+                 dtype=None, interleaved: bool = False):
     """RMSNorm of each query and key head (gains gq, gk [dim]), rotated by its position; values converted.
     qkv: the projection's float32 rows [M, (heads + 2 kv_heads) dim], or a tuple of three [M, .] tensors.
-    Returns q [M, heads, dim], k and v [M, kv_heads, dim] of `dtype`.  table None: no rotation.  Rows of a
+    Returns q [M, heads, dim], k and v [M, kv_heads, dim] of `dtype` (bfloat16 by default).  table None: no rotation.  Rows of a
     position outside the table are undefined (sync_status() then says BL_ERR_RANGE)."""
-    return _native().qk_norm_rope(qkv, heads, kv_heads, dim, pos, table, gq, gk, eps, _code(dtype), interleaved)
+    return _native().qk_norm_rope(qkv, heads, kv_heads, dim, pos, table, gq, gk, eps,
+                                  2 if dtype is None else _code(dtype), interleaved)
 
 
 def qk_norm_rope_append(qkv, heads: int, kv_heads: int, dim: int, pos, table, gq, gk, kcache, vcache, slots,
@@ -149,9 +150,10 @@ def paged_attention_workspace_size(batch: int, heads: int, kcache) -> int:
 
 
 def paged_attention(q, kcache, vcache, pages, lens, window: int = 0, sinks: int = 0, scale=None,
-                    out_dtype=torch.float32, ws=None, out=None):
+                    out_dtype=None, ws=None, out=None):
     """Attention of one new token per sequence over a paged cache [pages, kv_heads, page, D]: q [B, heads, D]
     of the cache's type, pages [B, n] int32 page numbers, lens [B] int32 tokens of each sequence (the new one
-    included).  out float32 or the cache's type, [B, heads, D].  ws: workspace(paged_attention_workspace_size(
+    included).  out float32 (the default) or the cache's type, [B, heads, D].  ws: workspace(paged_attention_workspace_size(
     ...)), kept by the caller between calls; allocated and cleared in the call when None."""
-    return _native().paged_attention(q, kcache, vcache, pages, lens, window, sinks, scale, _code(out_dtype), ws, out)
+    return _native().paged_attention(q, kcache, vcache, pages, lens, window, sinks, scale,
+                                     0 if out_dtype is None else _code(out_dtype), ws, out)

@@ -3,12 +3,15 @@ its attention operators over it.
 
     python -m int8_row_absmax_b200.build        # -> int8_row_absmax_b200/libbitlinear.so, _binding.so
 
-One nvcc invocation over one translation unit, and one of the host compiler.  No fast-math: the quantizers
+The library needs nvcc alone; the binding, which only PyTorch programs use, is left out
+where PyTorch or the headers of PyTorch or Python are missing.  One nvcc invocation over one translation unit, and one of the host compiler.  No fast-math: the quantizers
 need IEEE division and round-half-even, and -fmad=false keeps the dequant
 epilogue from being contracted into an FMA.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -58,16 +61,47 @@ def run(cmd, verbose: bool = False) -> None:
         print(res.stdout + res.stderr)
 
 
+def torch_root():
+    """The folder of the installed PyTorch, or None (PyTorch itself is not imported)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
+def built_for() -> str:
+    """What a binding has to be built for: the PyTorch and Python that run.  Part of the binding's bytes."""
+    return f"built for PyTorch {importlib.metadata.version('torch')}, Python {sys.version_info[0]}.{sys.version_info[1]};"
+
+
+def binding_fits() -> bool:
+    """Whether the binding is there and was built for the PyTorch and Python that run."""
+    if not os.path.exists(BINDING):
+        return False
+    with open(BINDING, "rb") as f:
+        return built_for().encode() in f.read()
+
+
+def binding_lacks():
+    """What the binding's build lacks here, in words, or None."""
+    root = torch_root()
+    if root is None:
+        return "PyTorch is not installed"
+    for header in (os.path.join(root, "include", "ATen", "ATen.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return f"{header} is missing"
+    return None
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """The tensor binding, against the PyTorch that is installed."""
-    if not force and up_to_date(BINDING, binding_sources()):
+    if not force and up_to_date(BINDING, binding_sources()) and binding_fits():
         return BINDING
     import torch
-    root = os.path.dirname(torch.__file__)
+    root = torch_root()
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include")]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
     run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_binding",
-         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBL_BUILT_FOR="{built_for()}"',
          "-I", os.path.join(ROOT, "include"), "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"],
          *(x for d in inc for x in ("-isystem", d)), BINDING_SRC, "-o", BINDING + ".tmp", "-L", PKG,
          "-l:libbitlinear.so", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
@@ -83,7 +117,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
              "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
              *extra, "-o", OUT + ".tmp", SRC], verbose)
         os.replace(OUT + ".tmp", OUT)
-    build_binding(force, verbose)
+    lacks = binding_lacks()
+    if lacks is not None:
+        print(f"the tensor binding is not built: {lacks}", file=sys.stderr)
+        return OUT
+    try:
+        build_binding(force, verbose)
+    except RuntimeError as e:
+        raise RuntimeError(f"{OUT} is built, its tensor binding is not: {e}") from e
     return OUT
 
 

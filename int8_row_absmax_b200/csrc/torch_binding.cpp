@@ -341,6 +341,7 @@ PYBIND11_MODULE(_binding, m) {
       PyErr_SetObject(cls.ptr(), cls(e.fn, e.code).ptr());
     }
   });
+  m.attr("built_for") = BL_BUILT_FOR;                  // looked for in the file before it is loaded
   m.def("qk_norm_rope", &qk_norm_rope);
   m.def("qk_norm_rope_append", &qk_norm_rope_append);
   m.def("qk_norm_rope_backward", &qk_norm_rope_backward);

@@ -62,16 +62,18 @@ _binding = None
 
 
 def _native():
-    """The tensor binding (raises if it has not been built for the PyTorch and Python that run)."""
+    """The tensor binding over the loaded library (raises if it has not been built for the PyTorch and Python
+    that run)."""
     global _binding
     if _binding is None:
         from . import build
-        load()
+        lib = load()
         _torch()
         if not build.binding_fits():
             raise RuntimeError("_binding.so is missing or built for another PyTorch or Python: build it with "
                                "python -m int8_row_absmax_b200.build")
         from . import _binding as module
+        module.use(lib._handle)
         _binding = module
     return _binding
 

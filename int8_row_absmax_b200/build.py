@@ -103,9 +103,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_binding",
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBL_BUILT_FOR="{built_for()}"',
          "-I", os.path.join(ROOT, "include"), "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"],
-         *(x for d in inc for x in ("-isystem", d)), BINDING_SRC, "-o", BINDING + ".tmp", "-L", PKG,
-         "-l:libbitlinear.so", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
-         "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], verbose)
+         *(x for d in inc for x in ("-isystem", d)), BINDING_SRC, "-o", BINDING + ".tmp",
+         "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ldl"], verbose)
     os.replace(BINDING + ".tmp", BINDING)
     return BINDING
 

@@ -1,5 +1,5 @@
 // Argument marshalling of the attention operators for PyTorch tensors: checks, outputs from
-// torch's allocator, and one call into libbitlinear.so on the tensors' device and its current
+// torch's allocator, and one call into the loaded library on the tensors' device and its current
 // stream.  Small calls are bound by the host's time; the same marshalling through ctypes took
 // 7 to 10 us a call more.  Nothing is computed here.
 #include <torch/csrc/autograd/python_variable.h>
@@ -10,9 +10,12 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <dlfcn.h>
+
 #include <cmath>
 #include <optional>
 #include <sstream>
+#include <stdexcept>
 #include <string>
 
 #include "bitlinear.h"
@@ -22,6 +25,36 @@ using at::Tensor;
 using MaybeTensor = std::optional<Tensor>;
 
 namespace {
+
+// The library's functions, found in the library that the package has loaded (and no other: each
+// copy of it has a status word of its own).
+struct Library {
+  decltype(&::bl_qk_norm_rope) qk_norm_rope;
+  decltype(&::bl_qk_norm_rope_append) qk_norm_rope_append;
+  decltype(&::bl_qk_norm_rope_backward) qk_norm_rope_backward;
+  decltype(&::bl_qk_norm_rope_backward_workspace_size) qk_norm_rope_backward_workspace_size;
+  decltype(&::bl_attention_ex) attention_ex;
+  decltype(&::bl_attention_backward_ex) attention_backward_ex;
+  decltype(&::bl_attention_backward_workspace_size) attention_backward_workspace_size;
+  decltype(&::bl_paged_attention) paged_attention;
+  decltype(&::bl_paged_attention_workspace_size) paged_attention_workspace_size;
+} lib = {};
+template <typename F> void find(void* handle, const char* name, F& f) {
+  f = reinterpret_cast<F>(dlsym(handle, name));
+  if (!f) throw std::runtime_error(std::string(name) + " is not in the loaded library");
+}
+void use(uintptr_t handle) {
+  void* h = reinterpret_cast<void*>(handle);
+  find(h, "bl_qk_norm_rope", lib.qk_norm_rope);
+  find(h, "bl_qk_norm_rope_append", lib.qk_norm_rope_append);
+  find(h, "bl_qk_norm_rope_backward", lib.qk_norm_rope_backward);
+  find(h, "bl_qk_norm_rope_backward_workspace_size", lib.qk_norm_rope_backward_workspace_size);
+  find(h, "bl_attention_ex", lib.attention_ex);
+  find(h, "bl_attention_backward_ex", lib.attention_backward_ex);
+  find(h, "bl_attention_backward_workspace_size", lib.attention_backward_workspace_size);
+  find(h, "bl_paged_attention", lib.paged_attention);
+  find(h, "bl_paged_attention_workspace_size", lib.paged_attention_workspace_size);
+}
 
 struct StatusError {
   const char* fn;
@@ -153,7 +186,7 @@ py::tuple qk_norm_rope(const py::object& qkv, int64_t heads, int64_t kv_heads, i
   const at::ScalarType type = scalar_of(dtype);
   Tensor q = make({r.M, heads, dim}, type, dev), k = make({r.M, kv_heads, dim}, type, dev), v = make({r.M, kv_heads, dim}, type, dev);
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
-  check("bl_qk_norm_rope", bl_qk_norm_rope(&r, bl_dtype(dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(), stream_of(dev)));
+  check("bl_qk_norm_rope", lib.qk_norm_rope(&r, bl_dtype(dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(), stream_of(dev)));
   return py::make_tuple(q, k, v);
 }
 
@@ -181,7 +214,7 @@ Tensor qk_norm_rope_append(const py::object& qkv, int64_t heads, int64_t kv_head
   const auto* at_ = static_cast<const int64_t*>(need(slots, "slots", at::kLong, {r.M}, dev));
   Tensor q = make({r.M, heads, dim}, kcache.scalar_type(), dev);
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
-  check("bl_qk_norm_rope_append", bl_qk_norm_rope_append(&r, q.data_ptr(), &c, at_, stream_of(dev)));
+  check("bl_qk_norm_rope_append", lib.qk_norm_rope_append(&r, q.data_ptr(), &c, at_, stream_of(dev)));
   return q;
 }
 
@@ -199,11 +232,11 @@ py::tuple qk_norm_rope_backward(const Tensor& dq, const Tensor& dk, const Tensor
   const int64_t wq = heads * dim, wk = kv_heads * dim, wide = wq + 2 * wk;
   Tensor dx = make({r.M, wide}, at::kFloat, dev), dgq = make({dim}, at::kFloat, dev), dgk = make({dim}, at::kFloat, dev), own;
   size_t have = 0;
-  void* w = workspace(ws, own, ws ? 0 : bl_qk_norm_rope_backward_workspace_size(&r), dev, have);
+  void* w = workspace(ws, own, ws ? 0 : lib.qk_norm_rope_backward_workspace_size(&r), dev, have);
   float* x = static_cast<float*>(dx.data_ptr());
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
   check("bl_qk_norm_rope_backward",
-        bl_qk_norm_rope_backward(&r, bl_dtype(code), pq, pk, pv, x, wide, x + wq, wide, x + wq + wk, wide,
+        lib.qk_norm_rope_backward(&r, bl_dtype(code), pq, pk, pv, x, wide, x + wq, wide, x + wq + wk, wide,
                                  static_cast<float*>(dgq.data_ptr()), static_cast<float*>(dgk.data_ptr()), w, have,
                                  stream_of(dev)));
   return py::make_tuple(dx, dgq, dgk);
@@ -271,7 +304,7 @@ py::tuple attention(const Tensor& q, const Tensor& k, const Tensor& v, const Ten
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
   // rows of no sequence: what a caller's tensor holds stays, what comes from the allocator is cleared
   const int clear = (out ? 0 : BL_CLEAR_OUT) | (lse ? 0 : BL_CLEAR_LSE);
-  check("bl_attention", bl_attention_ex(&c, po, pl, clear, stream_of(dev)));
+  check("bl_attention", lib.attention_ex(&c, po, pl, clear, stream_of(dev)));
   return py::make_tuple(o, l);
 }
 
@@ -291,10 +324,10 @@ py::tuple attention_backward(const Tensor& dout, const Tensor& q, const Tensor& 
   void* pk = need(dk, "dk", type, k.sizes(), dev);
   void* pv = need(dv, "dv", type, k.sizes(), dev);
   size_t have = 0;
-  void* w = workspace(ws, own, ws ? 0 : bl_attention_backward_workspace_size(&c), dev, have);
+  void* w = workspace(ws, own, ws ? 0 : lib.attention_backward_workspace_size(&c), dev, have);
   const c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev)};
   const int clear = (gq ? 0 : BL_CLEAR_DQ) | (gk ? 0 : BL_CLEAR_DK) | (gv ? 0 : BL_CLEAR_DV);
-  check("bl_attention_backward", bl_attention_backward_ex(&c, po, pl, pg, pq, pk, pv, w, have, clear, stream_of(dev)));
+  check("bl_attention_backward", lib.attention_backward_ex(&c, po, pl, pg, pq, pk, pv, w, have, clear, stream_of(dev)));
   return py::make_tuple(dq, dk, dv);
 }
 
@@ -319,12 +352,12 @@ Tensor paged_attention(const Tensor& q, const Tensor& kcache, const Tensor& vcac
   if (ws) {
     w = workspace(ws, own, 0, dev, have);
   } else {                                             // its counters have to be zero
-    have = bl_paged_attention_workspace_size(b, int32_of(h, "heads"), &c);
+    have = lib.paged_attention_workspace_size(b, int32_of(h, "heads"), &c);
     own = at::zeros({int64_t(have)}, at::TensorOptions().dtype(at::kByte).device(q.device()));
     w = own.data_ptr();
   }
   check("bl_paged_attention",
-        bl_paged_attention(pq, b, int32_of(h, "heads"), &c, pp, pages.size(1), pl, int32_of(window, "window"),
+        lib.paged_attention(pq, b, int32_of(h, "heads"), &c, pp, pages.size(1), pl, int32_of(window, "window"),
                            int32_of(sinks, "sinks"), scale ? float(*scale) : float(1.0 / std::sqrt(double(c.D))),
                            bl_dtype(out_dtype), po, w, have, stream_of(dev)));
   return o;
@@ -342,6 +375,7 @@ PYBIND11_MODULE(_binding, m) {
     }
   });
   m.attr("built_for") = BL_BUILT_FOR;                  // looked for in the file before it is loaded
+  m.def("use", &use);
   m.def("qk_norm_rope", &qk_norm_rope);
   m.def("qk_norm_rope_append", &qk_norm_rope_append);
   m.def("qk_norm_rope_backward", &qk_norm_rope_backward);

@@ -65,3 +65,18 @@ def test_a_binding_for_another_pytorch_is_built_again_and_not_loaded(monkeypatch
     monkeypatch.setattr(attn, "_torch", lambda: None)
     with pytest.raises(RuntimeError, match="another PyTorch"):
         attn._native()
+
+
+def test_the_binding_calls_the_library_that_was_loaded(tmp_path):
+    """A copy under another path: no second library beside it, whose status word nobody would read."""
+    import shutil
+    blbuild.build()
+    copy = shutil.copy(blbuild.OUT, tmp_path / "libother.so")
+    r = python("import torch, int8_row_absmax_b200 as bl\n"
+               "from int8_row_absmax_b200 import attn\n"
+               "attn._torch = lambda: torch\n"
+               f"bl.load({str(copy)!r})\n"
+               "attn._native()\n"
+               "maps = open('/proc/self/maps').read()\n"
+               "assert 'libother.so' in maps and 'libbitlinear.so' not in maps")
+    assert r.returncode == 0, r.stderr

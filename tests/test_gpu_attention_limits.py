@@ -343,3 +343,22 @@ def test_no_sequence_at_all_gives_clear_outputs(bl):
     held = torch.full_like(q, 3.0)
     assert (bl.attention(q, k, k, cu, cu, 0, out=held)[0] == 3).all()
     ok(bl)
+
+
+def test_the_status_word_read_is_that_of_the_calls(bl, tmp_path):
+    """In a process of its own, with a copy of the library: an error of an attention call is seen."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    copy = shutil.copy(bl.LIB_PATH, tmp_path / "libother.so")
+    code = ("import torch, int8_row_absmax_b200 as bl\n"
+            f"bl.load({str(copy)!r})\n"
+            "q = torch.zeros(4, 1, 64, dtype=torch.float16, device='cuda')\n"
+            "cu = torch.tensor([0, 4], dtype=torch.int32, device='cuda')\n"
+            "bl.attention(q, q, q, cu, cu, 4)\n"
+            "assert bl.sync_status() == 'BL_OK'\n"
+            "bl.attention(q, q, q, cu, cu, 2)\n"
+            "assert bl.sync_status() == 'BL_ERR_RANGE'\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(bl.PKG_DIR), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

@@ -449,6 +449,11 @@ typedef struct {
 bl_status bl_qk_norm_rope_append(const bl_qkv_rows* rows, void* q, const bl_kv_pages* cache, const int64_t* slots,
                                  cudaStream_t stream);
 
+/* The kernel that bl_qk_norm_rope and _append (backward = 0) or _backward (1) run for
+ * these rows: 1 the one of many rows, fed by bulk copies, 0 the one of single heads, -1
+ * if there are no rows or they are refused.  *ctas (if not NULL) receives its CTAs. */
+int bl_qk_norm_rope_plan(const bl_qkv_rows* rows, int backward, int* ctas);
+
 /* Gradients of bl_qk_norm_rope with respect to its input rows and gains:
  *   dq [M, Hq, D], dk, dv [M, Hkv, D]: contiguous, type t (any bl_dtype).
  *   dxq, dxk, dxv: float32 rows, strides lddq, lddk, lddv (multiples of 4; a

@@ -46,6 +46,7 @@ SIGNATURES = {
     "bl_rope_table": (_I, [_P, _I64, _I, ctypes.c_double, _P]),
     "bl_qk_norm_rope": (_I, [_ROWS, _I, _P, _P, _P, _P]),
     "bl_qk_norm_rope_append": (_I, [_ROWS, _P, _PAGES, _P, _P]),
+    "bl_qk_norm_rope_plan": (_I, [_ROWS, _I, ctypes.POINTER(_I)]),
     "bl_qk_norm_rope_backward_workspace_size": (_SZ, [_ROWS]),
     "bl_qk_norm_rope_backward": (_I, [_ROWS, _I, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
     "bl_attention": (_I, [_CALL, _P, _P, _P]),

@@ -111,21 +111,34 @@ bool rows_by_ring(int64_t M, int heads, int per, int64_t warps) {
   return M * chunks >= 2 * warps && 2 * int64_t(heads) >= chunks * per;
 }
 
+// The kernel and CTAs of a call.  A ring kernel's CTAs share the items out evenly, so they are no
+// more than run at once: two an SM, by registers (120 of 256 threads) at every head size, though
+// the rings of small heads would leave room for more. Two against as many as the rings' room
+// allows (three here), us: 8192 tokens, 48 heads of 80: 51.9 / 58.7; of 96: 52.3 / 59.2; 16384
+// tokens, 48 heads of 40: 49.4 / 56.7.
+struct RowsPlan {
+  bool ring;
+  unsigned grid;
+};
+RowsPlan rows_plan(int64_t M, int heads, int D) {
+  const int lanes = rows_lanes(D), per = 128 / lanes;
+  const int64_t ctas = int64_t(num_sms()) * 2;
+  if (!rows_by_ring(M, heads, per, ctas * kQrRingWarps)) return {false, grid_for(M * heads, kQrThreads / lanes, 16)};
+  const int64_t grid = ceil_div(M * ceil_div(heads, per), kQrRingWarps);
+  return {true, unsigned(grid < ctas ? grid : ctas)};
+}
+
 template <typename T, bool kAppend, int kLanes>
 bl_status launch_rows(const QrArgs& a, cudaStream_t st) {
-  constexpr int kPerBlock = kQrThreads / kLanes;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t items = a.M * ceil_div(heads, QrRing<kLanes>::kHeads);
-  if (rows_by_ring(a.M, heads, QrRing<kLanes>::kHeads, int64_t(num_sms()) * 2 * kQrRingWarps)) {
+  static_assert(QrRing<kLanes>::kHeads == 128 / kLanes, "as the plan counts items");
+  const RowsPlan p = rows_plan(a.M, a.Hq + 2 * a.Hkv, a.D);
+  if (p.ring) {
     static std::atomic<uint64_t> done{0};
-    constexpr int kPerD = kQrRingWarps * kQrRing * QrRing<kLanes>::kHeads * 4, most = kPerD * 8 * kLanes;   // at most 96 KB
-    const int smem = kPerD * a.D;
-    if (!allow_smem(qk_norm_rope_ring_kernel<T, kAppend, kLanes>, most, done)) return BL_ERR_CUDA;
-    const int64_t per_sm = 220 * 1024 / smem;
-    const int64_t cap = int64_t(num_sms()) * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm), grid = ceil_div(items, kQrRingWarps);
-    qk_norm_rope_ring_kernel<T, kAppend, kLanes><<<unsigned(grid < cap ? grid : cap), 32 * kQrRingWarps, smem, st>>>(a);
+    constexpr int kPerD = kQrRingWarps * kQrRing * QrRing<kLanes>::kHeads * 4;   // bytes per element of a head: 96 KB at most
+    if (!allow_smem(qk_norm_rope_ring_kernel<T, kAppend, kLanes>, kPerD * 8 * kLanes, done)) return BL_ERR_CUDA;
+    qk_norm_rope_ring_kernel<T, kAppend, kLanes><<<p.grid, 32 * kQrRingWarps, kPerD * a.D, st>>>(a);
   } else {
-    qk_norm_rope_kernel<T, kAppend, kLanes><<<grid_for(a.M * heads, kPerBlock, 16), kQrThreads, 0, st>>>(a);
+    qk_norm_rope_kernel<T, kAppend, kLanes><<<p.grid, kQrThreads, 0, st>>>(a);
   }
   return launch_status();
 }
@@ -141,31 +154,36 @@ bl_status launch_norm_rope(const QrArgs& a, cudaStream_t st) {
 
 // CTAs of the backward (and rows of its partial sums): planned for 148 SMs.
 constexpr int kQrBackCtas = 148 * 2;
-int rows_back_grid(const bl_qkv_rows* r) {
-  const int64_t g = ceil_div(r->M * (r->Hq + 2 * int64_t(r->Hkv)), int64_t(kQrThreads / rows_lanes(r->D)));
+int rows_back_grid(int64_t M, int heads, int D) {
+  const int64_t g = ceil_div(M * heads, int64_t(kQrThreads / rows_lanes(D)));
   return int(g < 1 ? 1 : g < kQrBackCtas ? g : kQrBackCtas);
+}
+RowsPlan rows_back_plan(int64_t M, int heads, int D) {
+  const int grid = rows_back_grid(M, heads, D);
+  return {rows_by_ring(M, heads, 64 / rows_lanes(D), int64_t(grid) * kQrRingWarps), unsigned(grid)};
 }
 
 template <typename T, int kLanes>
-bl_status launch_rows_back(const QrArgs& a, int grid, cudaStream_t st) {
-  constexpr int kPerBlock = kQrThreads / kLanes;
-  if (rows_by_ring(a.M, a.Hq + 2 * a.Hkv, QrRing<kLanes>::kBackHeads, int64_t(grid) * kQrRingWarps)) {
+bl_status launch_rows_back(const QrArgs& a, cudaStream_t st) {
+  static_assert(QrRing<kLanes>::kBackHeads == 64 / kLanes, "as the plan counts items");
+  const RowsPlan p = rows_back_plan(a.M, a.Hq + 2 * a.Hkv, a.D);
+  if (p.ring) {
     static std::atomic<uint64_t> done{0};
     constexpr int kPerD = kQrRingWarps * kQrRing * QrRing<kLanes>::kBackHeads * (4 + int(sizeof(T)));   // bytes per element of a head
     if (!allow_smem(qk_norm_rope_backward_ring_kernel<T, kLanes>, kPerD * 8 * kLanes, done)) return BL_ERR_CUDA;
-    qk_norm_rope_backward_ring_kernel<T, kLanes><<<unsigned(grid), 32 * kQrRingWarps, size_t(kPerD) * a.D, st>>>(a);
+    qk_norm_rope_backward_ring_kernel<T, kLanes><<<p.grid, 32 * kQrRingWarps, size_t(kPerD) * a.D, st>>>(a);
   } else {
-    qk_norm_rope_backward_kernel<T, kLanes><<<unsigned(grid), kQrThreads, size_t(kPerBlock) * 2 * a.D * 4, st>>>(a);
+    qk_norm_rope_backward_kernel<T, kLanes><<<p.grid, kQrThreads, size_t(kQrThreads / kLanes) * 2 * a.D * 4, st>>>(a);
   }
   return launch_status();
 }
 template <typename T>
-bl_status launch_norm_rope_back(const QrArgs& a, int grid, cudaStream_t st) {
+bl_status launch_norm_rope_back(const QrArgs& a, cudaStream_t st) {
   switch (rows_lanes(a.D)) {
-    case 4: return launch_rows_back<T, 4>(a, grid, st);
-    case 8: return launch_rows_back<T, 8>(a, grid, st);
-    case 16: return launch_rows_back<T, 16>(a, grid, st);
-    default: return launch_rows_back<T, 32>(a, grid, st);
+    case 4: return launch_rows_back<T, 4>(a, st);
+    case 8: return launch_rows_back<T, 8>(a, st);
+    case 16: return launch_rows_back<T, 16>(a, st);
+    default: return launch_rows_back<T, 32>(a, st);
   }
 }
 
@@ -420,9 +438,17 @@ bl_status bl_qk_norm_rope_append(const bl_qkv_rows* rows, void* q, const bl_kv_p
                               : launch_norm_rope<__nv_bfloat16, true>(a, stream);
 }
 
+int bl_qk_norm_rope_plan(const bl_qkv_rows* rows, int backward, int* ctas) {
+  if (check_rows(rows, false) != BL_OK || rows->M == 0) return -1;
+  const int heads = rows->Hq + 2 * rows->Hkv;
+  const RowsPlan p = backward ? rows_back_plan(rows->M, heads, rows->D) : rows_plan(rows->M, heads, rows->D);
+  if (ctas) *ctas = int(p.grid);
+  return p.ring ? 1 : 0;
+}
+
 size_t bl_qk_norm_rope_backward_workspace_size(const bl_qkv_rows* rows) {
   if (check_rows(rows, false) != BL_OK || rows->M == 0) return 0;
-  return align_up(size_t(rows_back_grid(rows)) * 2 * size_t(rows->D) * 4);
+  return align_up(size_t(rows_back_grid(rows->M, rows->Hq + 2 * rows->Hkv, rows->D)) * 2 * size_t(rows->D) * 4);
 }
 
 bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const void* dq, const void* dk, const void* dv,
@@ -445,7 +471,7 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
       !is_aligned(dxk, 16) || !is_aligned(dxv, 16))
     return BL_ERR_ALIGNMENT;
   QrArgs a = rows_args(rows);
-  const int grid = rows_back_grid(rows);
+  const int grid = rows_back_grid(a.M, a.Hq + 2 * a.Hkv, a.D);
   if (dgq || dgk) {
     st = check_ws(ws, ws_bytes, bl_qk_norm_rope_backward_workspace_size(rows));
     if (st != BL_OK) return st;
@@ -460,9 +486,9 @@ bl_status bl_qk_norm_rope_backward(const bl_qkv_rows* rows, bl_dtype t, const vo
   a.lddq = lddq;
   a.lddk = lddk;
   a.lddv = lddv;
-  st = t == BL_T_F32   ? launch_norm_rope_back<float>(a, grid, stream)
-       : t == BL_T_F16 ? launch_norm_rope_back<__half>(a, grid, stream)
-                       : launch_norm_rope_back<__nv_bfloat16>(a, grid, stream);
+  st = t == BL_T_F32   ? launch_norm_rope_back<float>(a, stream)
+       : t == BL_T_F16 ? launch_norm_rope_back<__half>(a, stream)
+                       : launch_norm_rope_back<__nv_bfloat16>(a, stream);
   if (st != BL_OK) return st;
   if (a.part && !launch_early(gain_sum_kernel, dim3(unsigned(ceil_div(2 * a.D, 32))), 256, 0, stream, a.part, grid, a.D,
                               dgq, dgk))

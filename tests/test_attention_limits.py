@@ -47,3 +47,27 @@ def test_clearing_refusals(lib):
         bad[at] = 24
         assert b(call(**none), *bad, bit, None) == 2
     assert b(call(**none), *[None] * 7, 0, 0, None) == 0
+
+
+def rows(**kw):
+    d = dict(M=2, Hq=32, Hkv=8, D=128, q=256, k=256, v=256, ldq=1 << 20, ldk=1 << 20, ldv=1 << 20, pos=256, table=256, P=10, R=0,
+             interleaved=0, gq=None, gk=None, eps=1e-6)
+    d.update(kw)
+    return ctypes.byref(attn.QkvRows(**d))
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("d", [8, 24, 32, 40, 56, 64, 80, 96, 128, 160, 256])
+def test_many_rows_take_no_more_ctas_than_run_at_once(lib, d, backward):
+    """Items are shared out evenly over the CTAs: with more than the two an SM that registers allow, some of equal
+    size would run alone at the end.  (Without a GPU the plan is that of 148 SMs.)"""
+    ctas = ctypes.c_int()
+    assert lib.bl_qk_norm_rope_plan(rows(M=100_000, D=d), backward, ctypes.byref(ctas)) == 1
+    assert ctas.value == 2 * 148
+    assert lib.bl_qk_norm_rope_plan(rows(D=d), backward, ctypes.byref(ctas)) == 0 and 1 <= ctas.value <= 96
+
+
+def test_plans_of_rows_that_are_refused(lib):
+    plan = lib.bl_qk_norm_rope_plan
+    assert plan(None, 0, None) == -1 and plan(rows(D=12), 0, None) == -1 and plan(rows(M=0), 1, None) == -1
+    assert plan(rows(v=None), 1, None) == 0

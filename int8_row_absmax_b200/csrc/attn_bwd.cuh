@@ -524,16 +524,14 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
 
   // every product done: warps 0..3 store dV, warps 4..7 dK
   __syncthreads();
-  bool good = !*err;
   if (warp == 8) {
     if (!mbar_wait_near(&drain, 0u)) *err = 1;
     __syncwarp();
     if (*err && lane == 0) raise_status(kDevTimeout);
   }
   __syncthreads();
-  good = !*err;
   tc_fence_after();
-  if (warp < 8 && good) {
+  if (warp < 8 && !*err) {
     const int row = (warp & 3) * 32 + lane, j = j0 + row;
     const bool keys = warp >= 4;
     const uint32_t acc = tmem + (uint32_t((warp & 3) * 32) << 16) + (keys ? 384 : 256);

@@ -333,9 +333,10 @@ bl_status launch_attn_bwd(AttnArgs a, float* norms, cudaStream_t st) {
       !allow_smem(attn_dq_kernel<T, DP>, AbCfg<DP>::kDqSmem, done_q))
     return BL_ERR_CUDA;
   const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
-  const int64_t query_parts = ceil_div(a.max_q, AdCfg<DP>::tokens(a.Hq / a.Hkv));
-  const int64_t key_parts = f16 ? ceil_div(a.max_k, AdCfg<DP>::kMost) : 1;
-  const int64_t gd = int64_t(a.Hkv) * a.B * (query_parts > key_parts ? query_parts : key_parts);
+  using Ad = AdCfg<T, DP>;                               // the row sums: CTAs by sequence and key head, or rows as they come
+  const int64_t query_parts = ceil_div(a.max_q, Ad::tokens(a.Hq / a.Hkv)), key_parts = ceil_div(a.max_k, Ad::kMost);
+  const int64_t gd = Ad::kNorms ? int64_t(a.Hkv) * a.B * (query_parts > key_parts ? query_parts : key_parts)
+                                : int64_t(grid_for(a.Tq * a.Hq, Ad::kRows, 8));
   if (!int32_max(gq) || !int32_max(gk * a.splits) || !int32_max(gd + kClearCtas)) return BL_ERR_UNSUPPORTED;
   a.work = int(gd);
   if (f16 && cudaMemsetAsync(norms, 0, size_t(a.B) * size_t(a.Hkv) * 8, st) != cudaSuccess) return BL_ERR_CUDA;

@@ -68,69 +68,72 @@ template <typename T> __device__ __forceinline__ float ds_scale(const AttnArgs& 
 }
 
 // delta[h, row] = sum dO O, one group of DP / 8 lanes a row; for float16 also the largest
-// squared norms of the rows of dO and V (order does not matter to a maximum).  A CTA takes the
-// heads of one key head over some tokens of one sequence, about four rows a group, and as many
-// of the sequence's keys: one atomic a CTA and norm, on words that only its (sequence, key head)
-// has.  Rows dealt out over all sequences alike took 10 us more for 64 sequences of 128 tokens,
-// 8 heads of 64 (55 us in all): atomics wherever a group's row passes into another sequence.
-template <int DP> struct AdCfg {
-  static constexpr int kLanes = DP / 8, kRows = 256 / kLanes, kMost = 4 * kRows;   // rows at a time; keys of a CTA
+// squared norms of the rows of dO and V (order does not matter to a maximum).  bfloat16 takes
+// all rows alike.  For float16 a CTA takes the heads of one key head over some tokens of one
+// sequence, about two rows a group, and as many of the sequence's keys: one atomic a CTA and
+// norm, on words that only its (sequence, key head) has.  (Four rows: 9.9 against 8.0 us for 5
+// sequences of up to 777 tokens, 6/2 heads; 23.6 against 27.6 for 2 x 4096, 20/5 heads.)  Rows dealt out over all sequences there,
+// too, took 10 us more for 64 sequences of 128 tokens, 8 heads of 64 (55 us in all): atomics
+// wherever a group's row passes into another sequence; in bfloat16 looking up the sequence costs
+// 13.5 -> 18.6 us (4096 tokens, 32 heads of 128).
+template <typename T, int DP> struct AdCfg {
+  static constexpr bool kNorms = std::is_same<T, __half>::value;
+  static constexpr int kLanes = DP / 8, kRows = 256 / kLanes, kMost = 2 * kRows;   // rows at a time; keys of a CTA
   __host__ __device__ static int tokens(int group) { return group < kMost ? kMost / group : 1; }   // of a CTA
 };
+// The sum of a head's products x y, in all lanes of its group, and where asked for that of y's squares.
+template <typename T, int kLanes>
+__device__ __forceinline__ float2 row_sums(uint4 x, uint4 y, bool squares) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  float d = 0.f, n = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 p = unpack2<T>(xs[e]), g = unpack2<T>(ys[e]);
+    d = fmaf(p.x, g.x, fmaf(p.y, g.y, d));
+    n = fmaf(g.x, g.x, fmaf(g.y, g.y, n));
+  }
+  for (int o = kLanes / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  for (int o = kLanes / 2; squares && o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return make_float2(d, n);
+}
 template <typename T, int DP>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, AdCfg<T, DP>::kNorms ? 6 : 8)  // bfloat16, 6: 17.7 us for 14.2 (4096 tokens, 32 heads of 128)
 attn_delta_kernel(const AttnArgs a, float* norms) {
-  using C = AdCfg<DP>;
+  using C = AdCfg<T, DP>;
   if (blockIdx.x >= unsigned(a.work)) return clear_rest(a, 256);
-  constexpr bool kNorms = std::is_same<T, __half>::value;
   const int u = threadIdx.x % C::kLanes, in = threadIdx.x / C::kLanes;
   const bool on = 8 * u < a.D;
-  const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv)), b = rest % a.B, c = rest / a.B;
-  const int group = a.Hq / a.Hkv, tokens = C::tokens(group);
-  Seq s;
-  if (!load_seq(a, b, s, true)) return;
-  auto sum = [&](float x) {
-    for (int o = C::kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+  auto ask = [&](const void* p, int64_t at, bool live) {
+    return live && on ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at + 8 * u) : make_uint4(0, 0, 0, 0);
   };
-  float top_o = 0.f, top_v = 0.f;
-  const int i0 = c * tokens, rows = min(tokens, s.nq - i0) * group;
-  for (int r0 = 0; r0 < rows; r0 += C::kRows) {
-    const int r = r0 + in, i = i0 + r / group, h = hk * group + r % group;
-    const int64_t at = (int64_t(s.q0 + i) * a.Hq + h) * a.D + 8 * u;
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (on && r < rows) {
-      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o) + at);
-      y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + at);
+  if constexpr (!C::kNorms) {
+    const int64_t rows = a.Tq * a.Hq;
+    for (int64_t r0 = int64_t(blockIdx.x) * C::kRows; r0 < rows; r0 += int64_t(a.work) * C::kRows) {
+      const int64_t r = r0 + in;
+      const float d = row_sums<T, C::kLanes>(ask(a.o, r * a.D, r < rows), ask(a.dout, r * a.D, r < rows), false).x;
+      int64_t token, h;
+      split_index(r, a.Hq, rows < (int64_t(1) << 31), token, h);
+      if (u == 0 && r < rows) a.delta[h * a.Tq + token] = d;
     }
-    float d = 0.f, n = 0.f;
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 p = unpack2<T>(xs[e]), g = unpack2<T>(ys[e]);
-      d = fmaf(p.x, g.x, fmaf(p.y, g.y, d));
-      n = fmaf(g.x, g.x, fmaf(g.y, g.y, n));
+  } else {
+    const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv)), b = rest % a.B, c = rest / a.B;
+    const int group = a.Hq / a.Hkv, tokens = C::tokens(group);
+    Seq s;
+    if (!load_seq(a, b, s, true)) return;
+    float top_o = 0.f, top_v = 0.f;
+    const int i0 = c * tokens, rows = min(tokens, s.nq - i0) * group;
+    for (int r0 = 0; r0 < rows; r0 += C::kRows) {
+      const int r = r0 + in, i = i0 + r / group, h = hk * group + r % group;
+      const int64_t at = (int64_t(s.q0 + i) * a.Hq + h) * a.D;
+      const float2 t = row_sums<T, C::kLanes>(ask(a.o, at, r < rows), ask(a.dout, at, r < rows), true);
+      if (i + s.nk - s.nq >= 0 && t.y < INFINITY) top_o = fmaxf(top_o, t.y);          // rows that see a key
+      if (u == 0 && r < rows) a.delta[int64_t(h) * a.Tq + s.q0 + i] = t.x;
     }
-    d = sum(d);
-    if (kNorms) n = sum(n);
-    if (kNorms && i + s.nk - s.nq >= 0 && n < INFINITY) top_o = fmaxf(top_o, n);   // rows that see a key
-    if (u == 0 && r < rows) a.delta[int64_t(h) * a.Tq + s.q0 + i] = d;
-  }
-  if (kNorms) {
     const int j0 = int(min(int64_t(c) * C::kMost, int64_t(s.nk))), keys = min(C::kMost, s.nk - j0);   // c may count queries
     for (int r0 = 0; r0 < keys; r0 += C::kRows) {
       const int j = j0 + r0 + in;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (on && r0 + in < keys)
-        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + int64_t(s.k0 + j) * a.ldv + hk * a.D + 8 * u);
-      float n = 0.f;
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 p = unpack2<T>(xs[e]);
-        n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
-      }
-      n = sum(n);
+      const uint4 x = ask(a.v, int64_t(s.k0 + j) * a.ldv + hk * a.D, r0 + in < keys);
+      const float n = row_sums<T, C::kLanes>(x, x, false).x;
       const bool seen = a.window == 0 || j < a.sinks || j > s.nk - s.nq - a.window;   // by some query
       if (seen && n < INFINITY) top_v = fmaxf(top_v, n);
     }

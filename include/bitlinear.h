@@ -381,8 +381,8 @@ bl_status bl_linear_backward(const float* dY, const float* X, const float* W, in
  *   - Element types: float32 for what the BitLinears write and read, float16 or
  *     bfloat16 for queries, keys, values and their gradients.  Sums, softmax
  *     statistics and norms are float32; products contract with FMA.
- *   - D is the head size, a multiple of 8 (8 <= D <= 128); Hq is a multiple of
- *     Hkv, and query head h reads key/value head h / (Hq / Hkv).
+ *   - D is the head size, a multiple of 8 (8 <= D <= 128); Hq (<= 65535) is a
+ *     multiple of Hkv, and query head h reads key/value head h / (Hq / Hkv).
  *   - Visibility: the token at position p of a sequence sees the keys j <= p with
  *     j > p - window or j < sinks; window = 0 means no window (sinks is then
  *     without effect).  A row that sees no key gives 0 (its lse -inf, its
@@ -480,7 +480,7 @@ typedef struct {
   int64_t ldq, ldk, ldv;      /* elements between tokens, multiples of 8 */
   int64_t Tq, Tk;             /* rows of the buffers (< 2^29) */
   const int32_t *cu_q, *cu_k; /* [B + 1], not falling, within 0 .. Tq and 0 .. Tk */
-  int32_t B;
+  int32_t B;                  /* <= 65535 */
   int32_t max_q, max_k;       /* at least the longest Lq and Lk (max_k: the backward only); any larger value does */
   int32_t window, sinks;      /* >= 0 */
   float scale;                /* finite, > 0 */
@@ -510,8 +510,10 @@ bl_status bl_attention_ex(const bl_attn_call* call, void* out, float* lse, int c
  * P = exp(scale Q K^T - lse), dV = P^T dO, dS = P (dO V^T - rowsum(dO O)),
  * dQ = scale dS K, dK = scale dS^T Q, dK and dV summed over the query heads that
  * share a key head.  dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]: contiguous, type t.
- * Every sum is taken in a fixed order.  Rows that belong to no sequence are left
- * as they were.
+ * P and dS are rounded to type t before the products that they enter (in float16
+ * scaled by powers of two, dS by one for each sequence and key head); sums are
+ * float32.  Every sum is taken in a fixed order.  Rows that belong to no sequence
+ * are left as they were.
  *   ws >= bl_attention_backward_workspace_size(call) bytes, 256-byte aligned (its
  *   contents need no clearing). */
 size_t bl_attention_backward_workspace_size(const bl_attn_call* call);

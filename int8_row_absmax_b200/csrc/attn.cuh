@@ -24,6 +24,7 @@ struct AttnArgs {
   float* part;                // [splits][dK, dV][Tk, Hkv, D], where splits > 1
   int clear;                  // BL_CLEAR_*: outputs whose rows of no sequence become zero (lse: -inf)
   int work;                   // CTAs before those that clear
+  int parts;                  // float16 row sums: CTAs of a sequence and key head
 };
 
 struct Seq {

@@ -116,26 +116,29 @@ attn_delta_kernel(const AttnArgs a, float* norms) {
       if (u == 0 && r < rows) a.delta[h * a.Tq + token] = d;
     }
   } else {
-    const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv)), b = rest % a.B, c = rest / a.B;
+    const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv)), b = rest % a.B;
     const int group = a.Hq / a.Hkv, tokens = C::tokens(group);
     Seq s;
     if (!load_seq(a, b, s, true)) return;
     float top_o = 0.f, top_v = 0.f;
-    const int i0 = c * tokens, rows = min(tokens, s.nq - i0) * group;
-    for (int r0 = 0; r0 < rows; r0 += C::kRows) {
-      const int r = r0 + in, i = i0 + r / group, h = hk * group + r % group;
-      const int64_t at = (int64_t(s.q0 + i) * a.Hq + h) * a.D;
-      const float2 t = row_sums<T, C::kLanes>(ask(a.o, at, r < rows), ask(a.dout, at, r < rows), true);
-      if (i + s.nk - s.nq >= 0 && t.y < INFINITY) top_o = fmaxf(top_o, t.y);          // rows that see a key
-      if (u == 0 && r < rows) a.delta[int64_t(h) * a.Tq + s.q0 + i] = t.x;
-    }
-    const int j0 = int(min(int64_t(c) * C::kMost, int64_t(s.nk))), keys = min(C::kMost, s.nk - j0);   // c may count queries
-    for (int r0 = 0; r0 < keys; r0 += C::kRows) {
-      const int j = j0 + r0 + in;
-      const uint4 x = ask(a.v, int64_t(s.k0 + j) * a.ldv + hk * a.D, r0 + in < keys);
-      const float n = row_sums<T, C::kLanes>(x, x, false).x;
-      const bool seen = a.window == 0 || j < a.sinks || j > s.nk - s.nq - a.window;   // by some query
-      if (seen && n < INFINITY) top_v = fmaxf(top_v, n);
+    const int steps = max((s.nq + tokens - 1) / tokens, (s.nk + C::kMost - 1) / C::kMost);
+    for (int c = rest / a.B; c < steps; c += a.parts) {
+      const int i0 = min(c * tokens, s.nq), rows = min(tokens, s.nq - i0) * group;
+      for (int r0 = 0; r0 < rows; r0 += C::kRows) {
+        const int r = r0 + in, i = i0 + r / group, h = hk * group + r % group;
+        const int64_t at = (int64_t(s.q0 + i) * a.Hq + h) * a.D;
+        const float2 t = row_sums<T, C::kLanes>(ask(a.o, at, r < rows), ask(a.dout, at, r < rows), true);
+        if (i + s.nk - s.nq >= 0 && t.y < INFINITY) top_o = fmaxf(top_o, t.y);          // rows that see a key
+        if (u == 0 && r < rows) a.delta[int64_t(h) * a.Tq + s.q0 + i] = t.x;
+      }
+      const int j0 = int(min(int64_t(c) * C::kMost, int64_t(s.nk))), keys = min(C::kMost, s.nk - j0);   // c may count queries
+      for (int r0 = 0; r0 < keys; r0 += C::kRows) {
+        const int j = j0 + r0 + in;
+        const uint4 x = ask(a.v, int64_t(s.k0 + j) * a.ldv + hk * a.D, r0 + in < keys);
+        const float n = row_sums<T, C::kLanes>(x, x, false).x;
+        const bool seen = a.window == 0 || j < a.sinks || j > s.nk - s.nq - a.window;   // by some query
+        if (seen && n < INFINITY) top_v = fmaxf(top_v, n);
+      }
     }
     __shared__ float tops[2][8];
     top_o = warp_max(top_o);

@@ -198,3 +198,24 @@ def test_strided_rows_past_32_bit_offsets(bl):
     assert np.isfinite(f8(g1[0])).all()
     del wide, views
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_loose_longest_lengths_of_many_sequences(bl, dtype):
+    """Lengths known only as at most the buffer's, a thousand sequences: the calls take them, and soon."""
+    import torch
+    lens = np.random.default_rng(1).integers(1, 40, 1000).tolist()
+    q, k, v, cu, _ = packed(1, lens, lens, 32, 8, 64, dtype)
+    dout = normal(2, *q.shape, dtype=dtype)
+    out, lse = bl.attention(q, k, v, cu, cu, 40)
+    want = bl.attention_backward(dout, q, k, v, out, lse, cu, cu, 40, 40)
+    loose = q.shape[0]
+    got = bl.attention(q, k, v, cu, cu, loose)
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    for a, b in zip(bl.attention_backward(dout, q, k, v, out, lse, cu, cu, loose, loose), want):
+        assert torch.equal(a, b)
+    ok(bl)
+    one = slice(int(cu[500]), int(cu[501]))
+    first = torch.tensor([0, lens[500]], dtype=torch.int32, device="cuda")
+    check_forward(q[one], k[one], v[one], first, first, 0, 0, out[one], lse[:, one], dtype)
+    check_backward(q[one], k[one], v[one], first, first, 0, 0, out[one], lse[:, one], dout[one], [g[one] for g in want], dtype)

@@ -25,9 +25,9 @@
 // brought, dK/dV of 2 x 4096 tokens, 20/5 heads of 128: dO's place freed after dV and
 // lse asked for a block ahead 529 -> 317 us, a third stage of Q and P in two parts 307.
 //
-// Measured there, bfloat16: 0.56 ms in all (770 TFLOP/s of the formula's five products,
-// 1.07 PFLOP/s of the seven done; the card sustains 1.39 under its power limit): dQ 0.25,
-// dK/dV 0.31, delta 0.016.
+// Measured there, bfloat16: 0.55 ms in all in bursts (780 TFLOP/s of the formula's five
+// products, 1.09 PFLOP/s of the seven done): dQ 0.25, dK/dV 0.31, part of it in dQ's tail, row
+// sums 0.016. Back to back 0.63 ms, under the card's power limit (1.39 PFLOP/s sustained).
 //
 // float16: P is stored 2^14 times larger and dS 2^k times, k from the largest norms of the
 // rows of dO and V (|dP - delta| <= 2 |dO| |V|): neither overflows, and a dS down to 2^-28 of

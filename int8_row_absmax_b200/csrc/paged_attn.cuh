@@ -179,7 +179,9 @@ paged_attn_kernel(const PaArgs a) {
   // shortens each part by a tile's time (about 1 us) but adds parts to the join of the longest
   // item (about 0.1 us each per 128 columns of four): a part has at least the square root of
   // that item's tiles times the ratio.  One sequence of 12816 tokens, 15/3 heads of 80: 444 CTAs
-  // 49 us, 118 CTAs 23 us.
+  // 49 us, 118 CTAs 23 us.  What the rule costs: at D = 64 with up to 8 heads a key head its values
+  // no longer fit the registers of four CTAs an SM (36 bytes spilled); two sequences of 131071
+  // tokens, whose parts it leaves as they are, went from 62.6 to 64.6 us.
   int64_t total = 0, ctas = 0, lo = 0, hi = 0;
   {
     const int64_t rounds = ceil_div(a.B, kPaThreads);

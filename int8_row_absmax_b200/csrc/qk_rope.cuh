@@ -16,7 +16,8 @@
 // tokens of 48 heads of 128), so many rows come by bulk copies into a ring per warp; then
 // the instructions per item count: stepping without divisions 60 -> 51 us, 6.0 TB/s (92%
 // of the card's copy rate), 4-head items instead of 8 86 us.  Its gradient, 4096 tokens:
-// 44 us, 5.4 TB/s with the gains' sum.  Float32 outputs reach 5.2 TB/s.
+// 45 us, 5.3 TB/s with the gains' sum.  Float32 outputs reach 5.2 TB/s.  At heads that do
+// not fill their lanes instructions bind sooner: 48 heads of 80, 52 us, 3.6 TB/s.
 #pragma once
 
 #include "attn_common.cuh"

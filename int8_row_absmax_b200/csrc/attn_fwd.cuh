@@ -347,7 +347,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
       const float mx = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;
       if (cnt == 0) {
         m = fmaxf(mx, kLow);
-      } else if (__any_sync(0xffffffffu, mx > m + kAfLazy)) {
+      } else if (__any_sync(0xffffffffu, p >= 0 && mx > m + kAfLazy)) {   // (a row behind the sequence's end is another's)
         const float up = fmaxf(mx, m), f = exp2_approx(m - up);
         m = up;
         l *= f;

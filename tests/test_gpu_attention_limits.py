@@ -362,3 +362,25 @@ def test_the_status_word_read_is_that_of_the_calls(bl, tmp_path):
             "assert bl.sync_status() == 'BL_ERR_RANGE'\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(bl.PKG_DIR), capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,window,sinks", [("bfloat16", 2, 2, 96, 128, 65), ("float16", 12, 3, 96, 200, 4),
+                                                        ("bfloat16", 8, 2, 64, 0, 0), ("float16", 3, 1, 128, 0, 0)])
+def test_results_do_not_depend_on_what_a_sequence_is_packed_with(bl, dtype, hq, hk, d, window, sinks):
+    """The rows behind a sequence's end lie in its last tile: large ones, or infinities, change no bit of its results."""
+    import torch
+    lq, lk = [266, 26, 150, 140], [266, 529, 290, 900]
+    q, k, v, cq, ck = packed(3, lq, lk, hq, hk, d, dtype, scale=3.0)
+    q[292:442] *= 8                                                   # the third sequence's scores: far larger
+    alone = []
+    for b in range(4):
+        f = lambda t, c: t[int(c[b]):int(c[b + 1])].contiguous()  # noqa: E731,B023
+        one = [torch.tensor([0, n[b]], dtype=torch.int32, device="cuda") for n in (lq, lk)]
+        alone.append(bl.attention(f(q, cq), f(k, ck), f(v, ck), *one, lq[b], window=window, sinks=sinks))
+    wide = [torch.cat([t, torch.full((200, *t.shape[1:]), float("inf"), dtype=t.dtype, device="cuda")]) for t in (q, k, v)]
+    for x in ((q, k, v), wide):
+        out, lse = bl.attention(*x, cq, ck, 266, window=window, sinks=sinks)
+        ok(bl)
+        for b in range(4):
+            rows = slice(int(cq[b]), int(cq[b + 1]))
+            assert torch.equal(out[rows], alone[b][0]) and torch.equal(lse[:, rows], alone[b][1])

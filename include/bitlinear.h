@@ -512,8 +512,8 @@ bl_status bl_attention_ex(const bl_attn_call* call, void* out, float* lse, int c
  * share a key head.  dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]: contiguous, type t.
  * P and dS are rounded to type t before the products that they enter (in float16
  * scaled by powers of two, dS by one for each sequence and key head); sums are
- * float32.  Every sum is taken in a fixed order.  Rows that belong to no sequence
- * are left as they were.
+ * float32.  P carries the rounding of lse, a relative 2^-23 |lse|.  Every sum is
+ * taken in a fixed order.  Rows that belong to no sequence are left as they were.
  *   ws >= bl_attention_backward_workspace_size(call) bytes, 256-byte aligned (its
  *   contents need no clearing). */
 size_t bl_attention_backward_workspace_size(const bl_attn_call* call);

@@ -38,6 +38,9 @@ constexpr int kAfThreads = 320;                        // 2 x 4 softmax warps, M
 constexpr int kAfRing = 4;                             // K and V tiles in flight
 constexpr int kAfParts = 2;                            // parts in which a row of P is handed over
 constexpr float kAfLazy = 8.f;                         // log2 of the growth that is let pass
+// A row maximum m = round(c x) beyond which the exact product c x less m, what the exponentials
+// take, may pass P's room: m's last place is a half there. A maximum of kLow needs nothing.
+constexpr float kAfFar = 4194304.f;
 constexpr float kLow = -3.4028235e38f;                 // a row maximum before anything is seen: the lowest finite number
 
 struct alignas(64) AttnMaps {
@@ -309,7 +312,7 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + 256 + t * 128;
     const float c = a.scale * kLog2e;
-    float m = kLow, l = 0.f;
+    float m = kLow, l = 0.f, lim = INFINITY;           // maximum, sum, what a block's maximum has to pass to raise m
     int cnt = 0;
     bool fine = true;
     for (int j = 0; j < blocks.n && r < s.nq; ++j) {
@@ -345,29 +348,38 @@ attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) top4[e] = fmaxf(x[124 + e], top4[e]);
       const float mx = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;
-      if (cnt == 0) {
-        m = fmaxf(mx, kLow);
-      } else if (__any_sync(0xffffffffu, p >= 0 && mx > m + kAfLazy)) {   // (a row behind the sequence's end is another's)
+      float less = m;                                    // what the exponents take off
+      if (cnt == 0 || __any_sync(0xffffffffu, mx > lim)) {
         const float up = fmaxf(mx, m), f = exp2_approx(m - up);
-        m = up;
-        l *= f;
-        fine = mbar_wait_near(&o_full[t], uint32_t(cnt - 1) & 1u);
-        if (__any_sync(0xffffffffu, !fine)) {
-          *err = 1;
-          break;
-        }
-        tc_fence_after();
+        m = less = up;
+        const bool far = p >= 0 && fabsf(m) > kAfFar && m > kLow;
+        lim = p < 0 ? INFINITY : far ? -INFINITY : m + kAfLazy;   // (a row behind the sequence's end is another's)
+        if (cnt > 0) {
+          l *= f;
+          fine = mbar_wait_near(&o_full[t], uint32_t(cnt - 1) & 1u);
+          if (__any_sync(0xffffffffu, !fine)) {
+            *err = 1;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
-        for (int u = 0; u < DP / 32; ++u) {
-          uint32_t o[32];
-          tmem_ld32(ot + u * 32, o);
-          tmem_ld_wait();
+          for (int u = 0; u < DP / 32; ++u) {
+            uint32_t o[32];
+            tmem_ld32(ot + u * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st32(ot + u * 32, o);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(ot + u * 32, o);
+          }
+        }
+        if (__any_sync(0xffffffffu, far)) {              // the difference first
+          const float by = far ? c : 1.f, off = far ? m : 0.f, back = far ? 1.f / c : 1.f;
+#pragma unroll
+          for (int u = 0; u < 128; ++u) x[u] = (x[u] * by - off) * back;
+          less = m - off;
         }
       }
-      const float sub = kShift - m;
+      const float sub = kShift - less;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int part = 0; part < kAfParts; ++part) {      // the tensor core starts on the first keys meanwhile

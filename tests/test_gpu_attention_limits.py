@@ -384,3 +384,25 @@ def test_results_do_not_depend_on_what_a_sequence_is_packed_with(bl, dtype, hq, 
         for b in range(4):
             rows = slice(int(cq[b]), int(cq[b + 1]))
             assert torch.equal(out[rows], alone[b][0]) and torch.equal(lse[:, rows], alone[b][1])
+
+
+@pytest.mark.parametrize("dtype,size", [("float16", 2.0 ** 10), ("float16", 2.0 ** 15), ("bfloat16", 2.0 ** 12), ("bfloat16", 2.0 ** 20),
+                                        ("bfloat16", 2.0 ** 40), ("bfloat16", 2.0 ** 100)])
+@pytest.mark.parametrize("sign,window", [(1, 0), (-1, 0), (1, 100), (-1, 100)])
+def test_scores_of_any_size(bl, dtype, size, sign, window):
+    """Scores up to 2^29 (float16) and 2^114 apart: the exact product of a score and its scale, less the rounded row
+    maximum, would pass what a probability has room for."""
+    import torch
+    n, d = 300, 64
+    q, k = (torch.zeros(n, 1, d, dtype=getattr(torch, dtype), device="cuda") for _ in range(2))
+    at = (np.arange(n) * 37) % 251 + 1
+    q[..., 0], k[:, 0, 0] = size, torch.from_numpy(64.0 * sign * at).cuda()
+    v = normal(1, n, 1, d, dtype=dtype)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, lse = bl.attention(q, k, v, cu, cu, n, window=window, scale=1.0)
+    ok(bl)
+    score = np.where(A.visible(n, n, window), sign * at * 64.0 * size, -np.inf)
+    best = score == score.max(1, keepdims=True)                       # the next one is 2^16 less at least
+    want = (best / best.sum(1, keepdims=True)) @ f8(v[:, 0])
+    assert (np.abs(f8(out[:, 0]) - want) <= 1.01 * HALF[dtype] * np.abs(want)).all()
+    assert (np.abs(f8(lse[0]) / (score.max(1) + np.log(best.sum(1))) - 1) <= 4 * E).all()

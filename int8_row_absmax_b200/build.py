@@ -69,7 +69,12 @@ def torch_root():
 
 def built_for() -> str:
     """What a binding has to be built for: the PyTorch and Python that run.  Part of the binding's bytes."""
-    return f"built for PyTorch {importlib.metadata.version('torch')}, Python {sys.version_info[0]}.{sys.version_info[1]};"
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:                      # a PyTorch that was not installed as a package
+        import torch
+        version = torch.__version__
+    return f"built for PyTorch {version}, Python {sys.version_info[0]}.{sys.version_info[1]};"
 
 
 def binding_fits() -> bool:

@@ -310,9 +310,11 @@ int dkv_splits(const bl_attn_call* c) {
   const int64_t heads = ceil_div(group, want);
   return int(ceil_div(group, heads));
 }
+// Parts by sequence and key, not by the buffer's row: fewer than 148 key blocks are shared out, so
+// that they never pass 39 MB, whatever the buffers hold besides.
 size_t dkv_part_bytes(const bl_attn_call* c) {
   const int splits = dkv_splits(c);
-  return splits > 1 ? align_up(size_t(splits) * 2 * size_t(c->Tk) * size_t(c->Hkv) * size_t(c->D) * 4) : 0;
+  return splits > 1 ? align_up(size_t(splits) * 2 * size_t(c->B) * size_t(longest(c->max_k, c->Tk)) * size_t(c->Hkv) * size_t(c->D) * 4) : 0;
 }
 
 template <typename T, int DP>

@@ -21,7 +21,7 @@ struct AttnArgs {
   float* delta;
   void *dq, *dk, *dv;
   int splits, split_heads;    // dK/dV: CTAs that share a key block's query heads, heads of each
-  float* part;                // [splits][dK, dV][Tk, Hkv, D], where splits > 1
+  float* part;                // [splits][dK, dV][B, max_k, Hkv, D], where splits > 1
   int clear;                  // BL_CLEAR_*: outputs whose rows of no sequence become zero (lse: -inf)
   int work;                   // CTAs before those that clear
   int parts;                  // float16 row sums: CTAs of a sequence and key head
@@ -30,6 +30,12 @@ struct AttnArgs {
 struct Seq {
   int q0, nq, k0, nk;
 };
+// The place of key j of sequence b and key head hk in the part that CTA z of those that share its
+// heads takes of dK (which = 0) or dV (1).
+__device__ __forceinline__ float* part_row(const AttnArgs& a, int z, int which, int b, int j, int hk) {
+  const int64_t keys = int64_t(a.B) * a.max_k;
+  return a.part + (((2 * z + which) * keys + int64_t(b) * a.max_k + j) * a.Hkv + hk) * a.D;
+}
 // Sequence b's rows; false (and the range flag) if its bounds cannot be.
 __device__ __forceinline__ bool load_seq(const AttnArgs& a, int b, Seq& s, bool keys) {
   s.q0 = a.cu_q[b];

@@ -190,11 +190,11 @@ __global__ void __launch_bounds__(256)
 attn_dkv_join_kernel(const AttnArgs a) {
   griddep_wait();                                      // launched early: the parts are the kernel before's
   const int hk = int(blockIdx.x % unsigned(a.Hkv)), rest = int(blockIdx.x / unsigned(a.Hkv));
-  const int j0 = rest / a.B * 128;
+  const int j0 = rest / a.B * 128, b = rest % a.B;
   Seq s;
-  if (!load_seq(a, rest % a.B, s, true) || j0 >= s.nk) return;
+  if (!load_seq(a, b, s, true) || j0 >= s.nk) return;
+  const int64_t step = 2 * int64_t(a.B) * a.max_k * a.Hkv * a.D;         // from one CTA's part to the next one's
   // 16 rows a CTA: 32 lanes a row (one quad each at D = 128), 8 rows at a time
-  const int64_t one = a.Tk * a.Hkv * a.D;
   const int c = threadIdx.x & 31;
   uint32_t bad = 0;
 #pragma unroll
@@ -203,9 +203,10 @@ attn_dkv_join_kernel(const AttnArgs a) {
     if (r >= s.nk || 4 * c >= a.D) continue;
     const int64_t at = (int64_t(s.k0 + r) * a.Hkv + hk) * a.D + 4 * c;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* part = part_row(a, 0, which, b, r, hk) + 4 * c;
 #pragma unroll 4
     for (int z = 0; z < a.splits; ++z) {
-      const float4 x = *reinterpret_cast<const float4*>(a.part + (2 * z + which) * one + at);
+      const float4 x = *reinterpret_cast<const float4*>(part + z * step);
       y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
     }
     const uint2 w = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
@@ -545,7 +546,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const int64_t at = (int64_t(s.k0 + j) * a.Hkv + hk) * a.D;
     T* out = static_cast<T*>(keys ? a.dk : a.dv) + at;
     if (a.splits > 1)
-      store_row_f32<DP>(acc, a.part + (2 * z + (keys ? 0 : 1)) * (a.Tk * a.Hkv * a.D) + at, a.D, f, j < s.nk, n == 0);
+      store_row_f32<DP>(acc, part_row(a, z, keys ? 0 : 1, b, j, hk), a.D, f, j < s.nk, n == 0);
     else if (!store_row<T, DP>(acc, out, a.D, f, j < s.nk, n == 0) && j < s.nk) raise_status(kDevNonFinite);
   }
   tc_fence_before();

@@ -71,3 +71,14 @@ def test_plans_of_rows_that_are_refused(lib):
     plan = lib.bl_qk_norm_rope_plan
     assert plan(None, 0, None) == -1 and plan(rows(D=12), 0, None) == -1 and plan(rows(M=0), 1, None) == -1
     assert plan(rows(v=None), 1, None) == 0
+
+
+def test_workspace_does_not_grow_with_rows_that_no_sequence_has(lib):
+    """A buffer for many tokens with a small batch in it: the parts of dK and dV take the sequences' keys."""
+    size = lib.bl_attention_backward_workspace_size
+    small = dict(Hq=32, Hkv=4, D=128, ldq=4096, ldk=512, ldv=512, max_q=200, max_k=200, B=2)
+    parts = size(call(**small, Tq=0, q=None, Tk=400))
+    assert parts > 2 * 8 * 2 * 200 * 4 * 128 * 4
+    assert size(call(**small, Tq=0, q=None, Tk=1 << 28)) == parts
+    for b, most in ((1, 1 << 28), (147, 128), (3, 6000), (1, 18000)):
+        assert size(call(**{**small, "B": b, "max_k": most, "Hkv": 1, "Hq": 32, "ldk": 128, "ldv": 128}, Tq=0, q=None, Tk=1 << 28)) < 40 << 20

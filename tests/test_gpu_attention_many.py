@@ -150,7 +150,7 @@ def test_tens_of_blocks(bl, n, hq, hk, d, window, sinks, dtype):
     check_backward(q, k, v, cq, ck, window, sinks, out, lse, dout, grads, dtype)
 
 
-@pytest.mark.parametrize("hq,hk", [(32, 32), (32, 4)])               # 4: the parts of dK and dV pass 2^31 elements, too
+@pytest.mark.parametrize("hq,hk", [(32, 32), (32, 4)])               # 4: a key block's heads are shared out
 def test_packed_rows_past_32_bit_offsets(bl, hq, hk):
     """Sequences behind 2^31 elements of rows that belong to none: bit for bit what they are at the buffers' start."""
     import torch

@@ -498,7 +498,8 @@ bl_status bl_attention(const bl_attn_call* call, void* out, float* lse, cudaStre
  * cu_q[B]; all of them where B = 0) are cleared in the same launch, for the outputs
  * named in `clear`: out becomes 0, lse -inf.  For outputs that come from an
  * allocator: what such a row holds would otherwise go on into the sums over rows
- * that follow (a gain's gradient, a projection's).  clear = 0: bl_attention. */
+ * that follow (a gain's gradient, a projection's).  Other bits are refused, and so
+ * is an output to be cleared that is NULL.  clear = 0: bl_attention. */
 #define BL_CLEAR_OUT 0x01
 #define BL_CLEAR_LSE 0x02
 #define BL_CLEAR_DQ 0x04

@@ -102,8 +102,8 @@ def qk_norm_rope(qkv, heads: int, kv_heads: int, dim: int, pos, table, gq=None, 
                  dtype=None, interleaved: bool = False):
     """RMSNorm of each query and key head (gains gq, gk [dim]), rotated by its position; values converted.
     qkv: the projection's float32 rows [M, (heads + 2 kv_heads) dim], or a tuple of three [M, .] tensors.
-    Returns q [M, heads, dim], k and v [M, kv_heads, dim] of `dtype` (bfloat16 by default).  table None: no rotation.  Rows of a
-    position outside the table are undefined (sync_status() then says BL_ERR_RANGE)."""
+    Returns q [M, heads, dim], k and v [M, kv_heads, dim] of `dtype` (bfloat16 by default).  table None: no
+    rotation.  Rows of a position outside the table are undefined (sync_status() then says BL_ERR_RANGE)."""
     return _native().qk_norm_rope(qkv, heads, kv_heads, dim, pos, table, gq, gk, eps,
                                   2 if dtype is None else _code(dtype), interleaved)
 
@@ -120,7 +120,7 @@ def qk_norm_rope_append(qkv, heads: int, kv_heads: int, dim: int, pos, table, gq
 def qk_norm_rope_backward(dq, dk, dv, qkv, heads: int, kv_heads: int, dim: int, pos, table, gq=None, gk=None,
                           eps: float = 1e-6, interleaved: bool = False, ws=None):
     """Gradients of qk_norm_rope: (dqkv float32 [M, (heads + 2 kv_heads) dim], dgq, dgk float32 [dim]).
-    dgq and dgk are sums over all M rows, padding included: its dq and dk have to be zero, as
+    dgq and dgk are sums over all M rows, padding included, whose dq and dk have to be zero, as
     attention_backward leaves them.  Rows of a position outside the table are undefined and not summed."""
     return _native().qk_norm_rope_backward(dq, dk, dv, qkv, heads, kv_heads, dim, pos, table, gq, gk, eps, interleaved,
                                            ws)
@@ -156,7 +156,8 @@ def paged_attention(q, kcache, vcache, pages, lens, window: int = 0, sinks: int 
                     out_dtype=None, ws=None, out=None):
     """Attention of one new token per sequence over a paged cache [pages, kv_heads, page, D]: q [B, heads, D]
     of the cache's type, pages [B, n] int32 page numbers, lens [B] int32 tokens of each sequence (the new one
-    included).  out float32 (the default) or the cache's type, [B, heads, D].  ws: workspace(paged_attention_workspace_size(
-    ...)), kept by the caller between calls; allocated and cleared in the call when None."""
+    included).  out float32 (the default) or the cache's type, [B, heads, D].  ws:
+    workspace(paged_attention_workspace_size(...)), kept by the caller between calls; allocated and cleared in
+    the call when None."""
     return _native().paged_attention(q, kcache, vcache, pages, lens, window, sinks, scale,
                                      0 if out_dtype is None else _code(out_dtype), ws, out)

@@ -406,3 +406,34 @@ def test_scores_of_any_size(bl, dtype, size, sign, window):
     want = (best / best.sum(1, keepdims=True)) @ f8(v[:, 0])
     assert (np.abs(f8(out[:, 0]) - want) <= 1.01 * HALF[dtype] * np.abs(want)).all()
     assert (np.abs(f8(lse[0]) / (score.max(1) + np.log(best.sum(1))) - 1) <= 4 * E).all()
+
+
+def test_a_captured_step_takes_other_bounds(bl):
+    """One graph for every batch that fits the buffers: bounds are read on the device, and the rows that they leave are
+    cleared on each replay."""
+    import torch
+    T, hq, hk, d = 700, 4, 2, 64
+    q, k, v = (normal(n, T, h, d, dtype="float16") for n, h in ((1, hq), (2, hk), (3, hk)))
+    dout = normal(4, T, hq, d, dtype="float16")
+    cu = torch.tensor([0, 400, 500, 700], dtype=torch.int32, device="cuda")
+
+    def step():
+        out, lse = bl.attention(q, k, v, cu, cu, T, window=150, sinks=2)
+        return out, lse, *bl.attention_backward(dout, q, k, v, out, lse, cu, cu, T, T, window=150, sinks=2)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for bounds in ([0, 400, 500, 700], [10, 10, 300, 333], [5, 260, 261, 262], [0, 0, 0, 0], [0, 1, 699, 700]):
+        cu.copy_(torch.tensor(bounds, dtype=torch.int32))
+        for t in held:
+            t.fill_(7.0)
+        graph.replay()
+        want = step()
+        ok(bl)
+        for a, b in zip(held, want):
+            assert torch.equal(a, b)
+        lo, hi = bounds[0], bounds[-1]
+        for rest in (slice(0, lo), slice(hi, T)):
+            assert not any(held[i][rest].any() for i in (0, 2, 3, 4)) and (held[1][:, rest] == -float("inf")).all()
+        check_forward(q, k, v, cu, cu, 150, 2, held[0], held[1], "float16")

@@ -335,12 +335,13 @@ bl_status launch_attn_bwd(AttnArgs a, float* norms, cudaStream_t st) {
       !allow_smem(attn_dq_kernel<T, DP>, AbCfg<DP>::kDqSmem, done_q))
     return BL_ERR_CUDA;
   const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
-  // The row sums: rows as they come, or CTAs by sequence and key head. Of those no more than fill
-  // the SMs several times, whatever the longest lengths say (they may be loose).
+  // The row sums: rows as they come, or CTAs by sequence and key head. Of those no more than run at
+  // once (6 an SM), whatever the longest lengths say (they may be loose): 4096 tokens, 32/8 heads of
+  // 128, 18.4 us, one CTA a piece 22.6.
   using Ad = AdCfg<T, DP>;
   const int64_t query_parts = ceil_div(a.max_q, Ad::tokens(a.Hq / a.Hkv)), key_parts = ceil_div(a.max_k, Ad::kMost);
   const int64_t pairs = int64_t(a.Hkv) * a.B, parts = query_parts > key_parts ? query_parts : key_parts;
-  const int64_t most = ceil_div(148 * 64, pairs);
+  const int64_t most = 148 * 6 / pairs > 1 ? 148 * 6 / pairs : 1;
   a.parts = int(parts < most ? parts : most);
   const int64_t gd = Ad::kNorms ? pairs * a.parts : int64_t(grid_for(a.Tq * a.Hq, Ad::kRows, 8));
   if (!int32_max(gq) || !int32_max(gk * a.splits) || !int32_max(gd + kClearCtas)) return BL_ERR_UNSUPPORTED;

@@ -292,9 +292,23 @@ bl_status clear_alone(AttnArgs a, cudaStream_t st) {
   return launch_status();
 }
 
-// The backward's workspace: two norms of each sequence and key head (float16), delta [Hq, Tq],
-// the parts of dK and dV.
-size_t norm_bytes(const bl_attn_call* c) { return align_up(c->t == BL_T_F16 ? size_t(c->B) * size_t(c->Hkv) * 8 : 1); }
+// CTAs of the float16 row sums by sequence and key head: no more than run at once (6 an SM),
+// whatever the longest lengths say (they may be loose). 4096 tokens, 32/8 heads of 128, 18.6 us,
+// one CTA a piece 22.6.
+template <int DP> int norm_parts(const bl_attn_call* c) {
+  using Ad = AdCfg<__half, DP>;
+  const int64_t queries = ceil_div(longest(c->max_q, c->Tq), Ad::tokens(c->Hq / c->Hkv));
+  const int64_t keys = ceil_div(longest(c->max_k, c->Tk), Ad::kMost), pairs = int64_t(c->Hkv) * c->B;
+  const int64_t parts = queries > keys ? queries : keys, most = 148 * 6 / pairs > 1 ? 148 * 6 / pairs : 1;
+  return int(parts < most ? parts : most);
+}
+int norm_parts(const bl_attn_call* c) { return c->t != BL_T_F16 ? 0 : c->D <= 64 ? norm_parts<64>(c) : norm_parts<128>(c); }
+// The backward's workspace: the row sums' norms of each sequence and key head (float16), delta
+// [Hq, Tq], the parts of dK and dV.
+size_t norm_bytes(const bl_attn_call* c) {
+  const size_t bytes = size_t(c->B) * size_t(c->Hkv) * size_t(norm_parts(c)) * 8;
+  return align_up(bytes ? bytes : 1);
+}
 size_t delta_bytes(const bl_attn_call* c) { return align_up(size_t(c->Tq) * size_t(c->Hq) * 4); }
 
 // CTAs that share the query heads of one key block: one as soon as the key blocks fill
@@ -335,18 +349,10 @@ bl_status launch_attn_bwd(AttnArgs a, float* norms, cudaStream_t st) {
       !allow_smem(attn_dq_kernel<T, DP>, AbCfg<DP>::kDqSmem, done_q))
     return BL_ERR_CUDA;
   const int64_t gq = int64_t(a.Hq) * a.B * ceil_div(a.max_q, 128), gk = int64_t(a.Hkv) * a.B * ceil_div(a.max_k, 128);
-  // The row sums: rows as they come, or CTAs by sequence and key head. Of those no more than run at
-  // once (6 an SM), whatever the longest lengths say (they may be loose): 4096 tokens, 32/8 heads of
-  // 128, 18.4 us, one CTA a piece 22.6.
   using Ad = AdCfg<T, DP>;
-  const int64_t query_parts = ceil_div(a.max_q, Ad::tokens(a.Hq / a.Hkv)), key_parts = ceil_div(a.max_k, Ad::kMost);
-  const int64_t pairs = int64_t(a.Hkv) * a.B, parts = query_parts > key_parts ? query_parts : key_parts;
-  const int64_t most = 148 * 6 / pairs > 1 ? 148 * 6 / pairs : 1;
-  a.parts = int(parts < most ? parts : most);
-  const int64_t gd = Ad::kNorms ? pairs * a.parts : int64_t(grid_for(a.Tq * a.Hq, Ad::kRows, 8));
+  const int64_t gd = Ad::kNorms ? int64_t(a.Hkv) * a.B * a.parts : int64_t(grid_for(a.Tq * a.Hq, Ad::kRows, 8));
   if (!int32_max(gq) || !int32_max(gk * a.splits) || !int32_max(gd + kClearCtas)) return BL_ERR_UNSUPPORTED;
   a.work = int(gd);
-  if (f16 && cudaMemsetAsync(norms, 0, size_t(a.B) * size_t(a.Hkv) * 8, st) != cudaSuccess) return BL_ERR_CUDA;
   if (queries) attn_delta_kernel<T, DP><<<unsigned(a.work + (a.clear ? kClearCtas : 0)), 256, 0, st>>>(a, norms);
   else if (a.clear && clear_alone(a, st) != BL_OK) return BL_ERR_CUDA;
   if (queries && gq > 0) attn_dq_kernel<T, DP><<<unsigned(gq), kAbThreads, AbCfg<DP>::kDqSmem, st>>>(maps, a, norms);
@@ -567,6 +573,7 @@ bl_status bl_attention_backward_ex(const bl_attn_call* call, const void* out, co
   a.clear = clear;
   float* norms = static_cast<float*>(ws);
   a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + norm_bytes(call));
+  a.parts = norm_parts(call);
   a.splits = dkv_splits(call);
   a.split_heads = int(ceil_div(call->Hq / call->Hkv, a.splits));
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + norm_bytes(call) + delta_bytes(call));

@@ -58,11 +58,18 @@ struct AbCfg {
 
 template <typename T> __device__ __forceinline__ constexpr float p_scale_log2() { return std::is_same<T, __half>::value ? 14.f : 0.f; }
 
-// 2^k for dS (float16), from the largest squared row norms of dO and V of sequence b and key head hk.
-template <typename T> __device__ __forceinline__ float ds_scale(const AttnArgs& a, const float* norms, int b, int hk) {
+// 2^k for dS (float16), from the largest squared row norms of dO and V that the CTAs of the row
+// sums found of sequence b and key head hk; for whole warps.
+template <typename T> __device__ __forceinline__ float ds_scale(const AttnArgs& a, const float* norms, int b, int hk, int lane) {
   if (!std::is_same<T, __half>::value) return 1.f;
-  norms += 2 * (int64_t(b) * a.Hkv + hk);
-  const float most = 2.02f * sqrtf(norms[0]) * sqrtf(norms[1]);
+  const float2* part = reinterpret_cast<const float2*>(norms) + (int64_t(b) * a.Hkv + hk) * a.parts;
+  float o = 0.f, v = 0.f;
+#pragma unroll 4
+  for (int i = lane; i < a.parts; i += 32) {
+    o = fmaxf(o, part[i].x);
+    v = fmaxf(v, part[i].y);
+  }
+  const float most = 2.02f * sqrtf(warp_max(o)) * sqrtf(warp_max(v));
   if (!(most > 0.f && most < INFINITY)) return 1.f;
   return exp2f(fminf(fmaxf(floorf(log2f(32768.f / most)), -100.f), 100.f));
 }
@@ -70,10 +77,10 @@ template <typename T> __device__ __forceinline__ float ds_scale(const AttnArgs& 
 // delta[h, row] = sum dO O, one group of DP / 8 lanes a row; for float16 also the largest
 // squared norms of the rows of dO and V (order does not matter to a maximum).  bfloat16 takes
 // all rows alike.  For float16 a CTA takes the heads of one key head over some tokens of one
-// sequence, about two rows a group, and as many of the sequence's keys: one atomic a CTA and
-// norm, on words that only its (sequence, key head) has.  (Four rows: 9.9 against 8.0 us for 5
-// sequences of up to 777 tokens, 6/2 heads; 23.6 against 27.6 for 2 x 4096, 20/5 heads.)  Rows dealt out over all sequences there,
-// too, took 10 us more for 64 sequences of 128 tokens, 8 heads of 64 (55 us in all): atomics
+// sequence, about two rows a group, and as many of the sequence's keys, and leaves its two norms
+// in a place of its own: no atomics, and nothing to clear before (a clearing takes 3 us).  (Four
+// rows: 9.9 against 8.0 us for 5 sequences of up to 777 tokens, 6/2 heads; 23.6 against 27.6 for
+// 2 x 4096, 20/5 heads.)  Rows dealt out over all sequences there, too, with atomics, took 10 us more for 64 sequences of 128 tokens, 8 heads of 64 (55 us in all): atomics
 // wherever a group's row passes into another sequence; in bfloat16 looking up the sequence costs
 // 13.5 -> 18.6 us (4096 tokens, 32 heads of 128).
 template <typename T, int DP> struct AdCfg {
@@ -148,11 +155,10 @@ attn_delta_kernel(const AttnArgs a, float* norms) {
       tops[1][threadIdx.x >> 5] = top_v;
     }
     __syncthreads();
-    if (threadIdx.x < 2) {                              // squares: not negative, so their bits are ordered
+    if (threadIdx.x < 2) {
       float t = 0.f;
       for (int w = 0; w < 8; ++w) t = fmaxf(t, tops[threadIdx.x][w]);
-      unsigned int* to = reinterpret_cast<unsigned int*>(norms) + 2 * (int64_t(b) * a.Hkv + hk) + threadIdx.x;
-      if (__float_as_uint(t) > *reinterpret_cast<volatile unsigned int*>(to)) atomicMax(to, __float_as_uint(t));
+      norms[2 * ((int64_t(b) * a.Hkv + hk) * a.parts + rest / a.B) + threadIdx.x] = t;
     }
   }
 }
@@ -318,6 +324,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                 // S, dP, dV, dK: 128 columns each
+  float mult = 1.f;                                                     // dS's scale, in the softmax warps
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
@@ -448,7 +455,8 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t S = tmem + lanes + half * 64, dP = S + 128;
     const float c = a.scale * kLog2e;
-    const float mult = ds_scale<T>(a, norms, b, hk), f = mult * exp2f(-p_scale_log2<T>());
+    mult = ds_scale<T>(a, norms, b, hk, lane);
+    const float f = mult * exp2f(-p_scale_log2<T>());
     bool fine = true;
     for (int it = 0; it < n; ++it) {
       const int i0 = first + it % per * 128;
@@ -542,7 +550,7 @@ attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, cons
     const int row = (warp & 3) * 32 + lane, j = j0 + row;
     const bool keys = warp >= 4;
     const uint32_t acc = tmem + (uint32_t((warp & 3) * 32) << 16) + (keys ? 384 : 256);
-    const float f = keys ? a.scale / ds_scale<T>(a, norms, b, hk) : exp2f(-p_scale_log2<T>());
+    const float f = keys ? a.scale / mult : exp2f(-p_scale_log2<T>());
     const int64_t at = (int64_t(s.k0 + j) * a.Hkv + hk) * a.D;
     T* out = static_cast<T*>(keys ? a.dk : a.dv) + at;
     if (a.splits > 1)
@@ -611,6 +619,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uint32_t(uniform(int(s_tmem)));                 // S0, S1, dP, dQ: 128 columns each
+  float mult = 1.f;                                                     // dS's scale, in the softmax warps
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
@@ -697,7 +706,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
       lse = l == -INFINITY ? kNoRow : l * kLog2e;
       delta = a.delta[int64_t(h) * a.Tq + s.q0 + i];
     }
-    const float mult = ds_scale<T>(a, norms, b, hk);
+    mult = ds_scale<T>(a, norms, b, hk, lane);
     bool fine = true;
     for (int it = 0; it < n; ++it) {
       const int j0 = blocks.at(it);
@@ -768,7 +777,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps, const AttnArgs a, const
     const int row = warp * 32 + lane, i = i0 + row;
     T* out = static_cast<T*>(a.dq) + (int64_t(s.q0 + i) * a.Hq + h) * a.D;
     const uint32_t acc = tmem + (uint32_t(warp * 32) << 16) + 384;
-    if (!store_row<T, DP>(acc, out, a.D, a.scale / ds_scale<T>(a, norms, b, hk), i < s.nq, n == 0) && i < s.nq) raise_status(kDevNonFinite);
+    if (!store_row<T, DP>(acc, out, a.D, a.scale / mult, i < s.nq, n == 0) && i < s.nq) raise_status(kDevNonFinite);
   }
   tc_fence_before();
   __syncthreads();
